@@ -465,6 +465,146 @@ size_t pre_attn_drafter_workspace_bytes(int R, int max_blocks, int part_blocks);
  * PA_ERR_WORKSPACE; PA_ERR_CUDA if a launch fails. */
 int pre_attn_drafter_attention(const pa_drafter_args *args, void *stream);
 
+/* ------------------------------------------- reading the caches back
+ *
+ * What a sparse layer does with the step's outputs and caches: the indexer
+ * scores over an NVFP4 index cache (pre_attn_index_scores reads the FP8
+ * one), the selection of each row's key blocks from such scores, and the
+ * attention over the FP8 or NVFP4 KV caches, on the selected blocks or on
+ * every block.  The pages print none of the three; these are the plain
+ * definitions, in the conventions of pre_attn_index_scores: request r
+ * (r < R) owns rows m = r * q_len + i (i < q_len) at positions
+ * p = seq_lens[r] - q_len + i, a row's blocks are b < nb = p / 128 + 1 (128
+ * keys each), and key j sits at cache slot
+ * block_table[r * bt_width + j / 128] * 128 + j % 128, where the step wrote
+ * it.  A request with seq_lens[r] < 1 has no keys (a padded batch); one with
+ * 1 <= seq_lens[r] < q_len or more than bt_width blocks is taken as one
+ * without keys and raises PA_DEV_SLOT_RANGE.  NVFP4 pages hold block_size
+ * tokens: a multiple of 4 that divides 128, or a multiple of 128. */
+
+/* Indexer scores over an NVFP4 index cache (PA_CACHE_NVFP4: index_k as E2M1
+ * codes with E4M3 group scales, no global scale).  Row m of `scores`,
+ * columns j < nb * 128:
+ *   index_scale * sum_d iq[m][head*128 + d] * e2m1(code_j[d]) * e4m3(sf_j[d / 16])
+ * for j <= p in a block that is not pinned, -inf otherwise (as
+ * pre_attn_index_scores); products exact, f32 sums.  Columns from nb * 128
+ * on, and the scored columns of a block whose id lies outside the cache
+ * (flagged), are not written. */
+typedef struct pa_index_nvfp4_args {
+  const void *iq;             /* [R * q_len, iq_stride] bf16, 8-byte aligned */
+  int64_t iq_stride;          /* elements a row: a multiple of 4, >= (head + 1) * 128 */
+  int head;                   /* the index_q head scored */
+  const void *idx_cache;      /* pa_caches.idx_cache: idx_pages pages, 32-byte aligned */
+  int64_t idx_pages;
+  int64_t idx_page_bytes;     /* a multiple of 32, >= block_size * 72 */
+  int block_size;             /* tokens a page (see above) */
+  const int32_t *block_table; /* [R, bt_width] page-128 block ids */
+  const int32_t *seq_lens;    /* [R] */
+  int R;                      /* requests, 0 .. 65535 */
+  int q_len;                  /* rows a request, 1 .. 16 */
+  int bt_width;               /* 1 .. 16384 */
+  int init_blocks;            /* pinned first blocks */
+  int local_blocks;           /* pinned last blocks */
+  float index_scale;          /* pre_attn_index_scale_log2e(sm_scale) */
+  float *scores;              /* [R * q_len, score_stride] f32, 16-byte aligned */
+  int64_t score_stride;       /* floats a row: a multiple of 4, >= bt_width * 128 */
+  uint32_t *status;           /* device status word: PA_DEV_SLOT_RANGE */
+} pa_index_nvfp4_args;
+
+/* Compute those scores on `stream`, after the previous kernel on it
+ * (programmatic dependent launch).  Allocates nothing, never synchronises.
+ * Errors (nothing launched): PA_ERR_NULL, PA_ERR_SHAPE, PA_ERR_CONFIG
+ * (negative block counts, NaN scale), PA_ERR_ALIGN, PA_ERR_UNSUPPORTED
+ * (block_size neither divides 128 nor is a multiple of it); PA_ERR_CUDA if
+ * the launch fails. */
+int pre_attn_index_scores_nvfp4(const pa_index_nvfp4_args *args, void *stream);
+
+/* The blocks each row attends, per index head h: the pinned ones (b < init
+ * or b >= nb - local) and, of the others, the topk - (pinned blocks) with
+ * the largest score, a block's score being the maximum of its 128 columns
+ * of the row (NaN columns ignored).  A block without a score above -inf is
+ * not selected; equal scores go to the lower block.  blocks[m][h] gets the
+ * ids (positions in the request, not physical blocks) in ascending order,
+ * then -1 up to topk; counts[m][h] how many there are.  Only columns below
+ * nb * 128 of unpinned blocks are read. */
+typedef struct pa_select_args {
+  const float *scores;        /* [n_heads][R * q_len][score_stride] f32, 16-byte aligned */
+  int64_t score_stride;       /* floats a row: a multiple of 4, >= bt_width * 128 */
+  int64_t score_head_stride;  /* floats a head: a multiple of 4, >= R * q_len * score_stride for n_heads > 1 */
+  int n_heads;                /* index heads, 1 .. 64 */
+  const int32_t *seq_lens;    /* [R] */
+  int R;                      /* 0 .. 65535 */
+  int q_len;                  /* 1 .. 16 */
+  int bt_width;               /* blocks a score row holds, 1 .. 16384 */
+  int init_blocks, local_blocks; /* as the scores were made; init + local <= topk */
+  int topk;                   /* blocks a row attends at most, pinned ones included: 1 .. 256 */
+  int32_t *blocks;            /* [R * q_len, n_heads, topk] */
+  int32_t *counts;            /* [R * q_len, n_heads] */
+  uint32_t *status;           /* device status word: PA_DEV_SLOT_RANGE */
+} pa_select_args;
+
+/* Select on `stream`, after the previous kernel on it (programmatic
+ * dependent launch).  Allocates nothing, never synchronises.  Errors
+ * (nothing launched): PA_ERR_NULL, PA_ERR_SHAPE, PA_ERR_CONFIG (negative
+ * block counts, init + local > topk), PA_ERR_ALIGN; PA_ERR_CUDA if the
+ * launch fails. */
+int pre_attn_select_blocks(const pa_select_args *args, void *stream);
+
+/* Attention over the step's KV caches.  Query head hq of row m reads KV
+ * head h = hq / (n_q_heads / n_kv_heads):
+ *   out[m][hq] = sum_j softmax_j(sm_scale * q . k_j) v_j
+ * over the keys j <= p of the row's blocks: blocks[m][h][0 .. counts[m][h])
+ * (any order; an id twice counts once), or every block with blocks == NULL.
+ * k = e4m3 * k_scale, v = e4m3 * v_scale (PA_CACHE_FP8), or e2m1 * e4m3 group
+ * scale * global scale (PA_CACHE_NVFP4).  A row without keys, or whose every
+ * score is -inf, gets zeros; keys after p and unselected blocks are not
+ * looked at, whatever they hold.  bf16 q is used exactly up to 2^-29 of its
+ * head row's largest value; scores, softmax statistics and sums are f32, the
+ * weights enter the second product in f16. */
+typedef struct pa_attention_args {
+  const void *q;              /* [R * q_len, q_stride] bf16, or NULL; 16-byte aligned */
+  const void *q_fp8;          /* [R * q_len, q_stride] E4M3, or NULL; 16-byte aligned.  Exactly one of the two */
+  float q_fp8_scale;          /* dequantisation scale of q_fp8 (> 0, finite) */
+  int64_t q_stride;           /* elements a row: a multiple of 16, >= n_q_heads * 128 */
+  int n_q_heads, n_kv_heads;  /* n_q_heads = n_kv_heads * group, group 1 .. 16; n_kv_heads 1, 2 or 4 */
+  int cache_format;           /* enum pa_cache_format */
+  int block_size;             /* NVFP4: tokens a page (see above); FP8: 16 */
+  int kv_page_stride;         /* FP8: page-16 pages a 128-token block, as in pa_config: 0 (8) or >= 8 */
+  const pa_caches *caches;    /* host struct: the K / V fields of the format are read.  FP8: k_cache, v_cache, k_scale
+                                 and v_scale 16-byte aligned; NVFP4: kv_cache and kv_page_bytes multiples of 32 */
+  const int32_t *block_table; /* [R, bt_width] page-128 block ids */
+  const int32_t *seq_lens;    /* [R] keys of each request, its q_len rows' own included */
+  const int32_t *blocks;      /* [R * q_len, n_kv_heads, topk], or NULL: every block */
+  const int32_t *counts;      /* [R * q_len, n_kv_heads], with blocks */
+  int topk;                   /* with blocks: 1 .. 256 */
+  int R;                      /* 0 .. 65535 */
+  int q_len;                  /* 1 .. 16 */
+  int bt_width;               /* 1 .. 16384 */
+  float sm_scale;             /* > 0, finite */
+  void *out;                  /* [R * q_len, out_stride] bf16, 16-byte aligned; no overlap with q */
+  int64_t out_stride;         /* elements a row: a multiple of 8, >= n_q_heads * 128 */
+  void *workspace;            /* pre_attn_attention_workspace_bytes() of scratch, 256-byte aligned; no initial
+                                 contents needed; calls that share it must be ordered on the GPU */
+  size_t workspace_bytes;
+  uint32_t *status;           /* device status word: PA_DEV_SLOT_RANGE (a block id outside the cache or the
+                                 row's blocks: skipped; a request as above), PA_DEV_WAIT_TIMEOUT */
+  uint32_t flags;             /* PA_FLAG_NO_PDL, PA_FLAG_TEST_WAIT_TIMEOUT */
+} pa_attention_args;
+
+/* Workspace bytes of a call with these sizes on a device of num_sms SMs
+ * (partial results of requests that several SMs share).  Host arithmetic;
+ * 0 for arguments out of range. */
+size_t pre_attn_attention_workspace_bytes(int R, int q_len, int n_kv_heads, int num_sms);
+
+/* Run the attention on `stream`, after the previous kernel on it
+ * (programmatic dependent launch): one kernel, and one that joins the parts
+ * of requests that several SMs share.  Allocates nothing, never synchronises.
+ * Errors (nothing launched): PA_ERR_NULL, PA_ERR_SHAPE, PA_ERR_CONFIG
+ * (formats, head counts, scales, both or neither q, unknown flags),
+ * PA_ERR_ALIGN, PA_ERR_ALIAS (out overlaps q), PA_ERR_WORKSPACE,
+ * PA_ERR_UNSUPPORTED (block_size, as above); PA_ERR_CUDA if a launch fails. */
+int pre_attn_attention(const pa_attention_args *args, void *stream);
+
 /* Main kernels a call can run (pre_attn_path). */
 enum {
   PA_PATH_GEMV = 0,         /* skinny path: prologue, then the FP8 GEMV on one cluster per head */

@@ -85,6 +85,31 @@ class pa_drafter_args(ctypes.Structure):
                 ("prof_before", _vp), ("prof_after", _vp)]
 
 
+class pa_index_nvfp4_args(ctypes.Structure):
+    _fields_ = [("iq", _vp), ("iq_stride", ctypes.c_int64), ("head", ctypes.c_int), ("idx_cache", _vp),
+                ("idx_pages", ctypes.c_int64), ("idx_page_bytes", ctypes.c_int64), ("block_size", ctypes.c_int),
+                ("block_table", _vp), ("seq_lens", _vp), ("R", ctypes.c_int), ("q_len", ctypes.c_int),
+                ("bt_width", ctypes.c_int), ("init_blocks", ctypes.c_int), ("local_blocks", ctypes.c_int),
+                ("index_scale", ctypes.c_float), ("scores", _vp), ("score_stride", ctypes.c_int64), ("status", _vp)]
+
+
+class pa_select_args(ctypes.Structure):
+    _fields_ = [("scores", _vp), ("score_stride", ctypes.c_int64), ("score_head_stride", ctypes.c_int64),
+                ("n_heads", ctypes.c_int), ("seq_lens", _vp), ("R", ctypes.c_int), ("q_len", ctypes.c_int),
+                ("bt_width", ctypes.c_int), ("init_blocks", ctypes.c_int), ("local_blocks", ctypes.c_int),
+                ("topk", ctypes.c_int), ("blocks", _vp), ("counts", _vp), ("status", _vp)]
+
+
+class pa_attention_args(ctypes.Structure):
+    _fields_ = [("q", _vp), ("q_fp8", _vp), ("q_fp8_scale", ctypes.c_float), ("q_stride", ctypes.c_int64),
+                ("n_q_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("cache_format", ctypes.c_int),
+                ("block_size", ctypes.c_int), ("kv_page_stride", ctypes.c_int), ("caches", ctypes.POINTER(pa_caches)),
+                ("block_table", _vp), ("seq_lens", _vp), ("blocks", _vp), ("counts", _vp), ("topk", ctypes.c_int),
+                ("R", ctypes.c_int), ("q_len", ctypes.c_int), ("bt_width", ctypes.c_int), ("sm_scale", ctypes.c_float),
+                ("out", _vp), ("out_stride", ctypes.c_int64), ("workspace", _vp),
+                ("workspace_bytes", ctypes.c_size_t), ("status", _vp), ("flags", ctypes.c_uint32)]
+
+
 class PreAttnError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -128,6 +153,10 @@ def load(path: str = LIB_PATH):
         "pre_attn_drafter_part_blocks": (i, [i, i, i]),
         "pre_attn_drafter_workspace_bytes": (sz, [i, i, i]),
         "pre_attn_drafter_attention": (i, [ctypes.POINTER(pa_drafter_args), _vp]),
+        "pre_attn_index_scores_nvfp4": (i, [ctypes.POINTER(pa_index_nvfp4_args), _vp]),
+        "pre_attn_select_blocks": (i, [ctypes.POINTER(pa_select_args), _vp]),
+        "pre_attn_attention_workspace_bytes": (sz, [i, i, i, i]),
+        "pre_attn_attention": (i, [ctypes.POINTER(pa_attention_args), _vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
@@ -285,6 +314,32 @@ def pre_attn_drafter_attention(args: pa_drafter_args, stream=None, check: bool =
     if check and st != PA_OK:
         raise PreAttnError(st, "pre_attn_drafter_attention " +
                            (pre_attn_last_cuda_error() if st == PA_ERR_CUDA else ""))
+    return st
+
+
+def pre_attn_index_scores_nvfp4(args: pa_index_nvfp4_args, stream=None, check: bool = True) -> int:
+    st = load().pre_attn_index_scores_nvfp4(ctypes.byref(args), stream_ptr(stream))
+    if check and st != PA_OK:
+        raise PreAttnError(st, "pre_attn_index_scores_nvfp4 " +
+                           (pre_attn_last_cuda_error() if st == PA_ERR_CUDA else ""))
+    return st
+
+
+def pre_attn_select_blocks(args: pa_select_args, stream=None, check: bool = True) -> int:
+    st = load().pre_attn_select_blocks(ctypes.byref(args), stream_ptr(stream))
+    if check and st != PA_OK:
+        raise PreAttnError(st, "pre_attn_select_blocks " + (pre_attn_last_cuda_error() if st == PA_ERR_CUDA else ""))
+    return st
+
+
+def pre_attn_attention_workspace_bytes(R: int, q_len: int, n_kv_heads: int, num_sms: int) -> int:
+    return int(load().pre_attn_attention_workspace_bytes(int(R), int(q_len), int(n_kv_heads), int(num_sms)))
+
+
+def pre_attn_attention(args: pa_attention_args, stream=None, check: bool = True) -> int:
+    st = load().pre_attn_attention(ctypes.byref(args), stream_ptr(stream))
+    if check and st != PA_OK:
+        raise PreAttnError(st, "pre_attn_attention " + (pre_attn_last_cuda_error() if st == PA_ERR_CUDA else ""))
     return st
 
 

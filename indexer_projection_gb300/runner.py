@@ -79,3 +79,129 @@ class PreAttn:
         if stream is None:
             stream = torch.cuda.current_stream(self.device)
         return B.pre_attn_device_status(self.workspace, stream)
+
+
+class CacheReader:
+    """What a layer reads back of its caches: the indexer scores, the block
+    selection and the attention, for up to ``max_requests`` requests of
+    ``q_len`` rows whose block tables hold ``bt_width`` page-128 blocks.
+
+    ``caches`` is PreAttn.fp8_caches(...) or PreAttn.nvfp4_caches(...): the
+    fields that a call reads have to be set (the index cache for
+    ``index_scores``, the K / V ones for ``attend``) and their tensors kept
+    alive by the caller.  Owns a workspace and a status word; calls of one
+    reader are ordered by their stream, or by the caller.  Every tensor is on
+    ``device``; seq_lens, block tables, block lists and counts are contiguous
+    int32, scores and query rows have contiguous columns.
+    """
+
+    def __init__(self, n_q_heads: int, n_kv_heads: int, *, cache_format: int, caches: B.pa_caches, max_requests: int,
+                 q_len: int, bt_width: int, topk: int = 0, init_blocks: int = 0, local_blocks: int = 0,
+                 block_size: int = 16, kv_page_stride: int = 0, sm_scale: float = 128 ** -0.5, flags: int = 0,
+                 device: torch.device | str | None = None):
+        B.load()
+        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.n_q_heads, self.n_kv_heads, self.cache_format, self.caches = n_q_heads, n_kv_heads, cache_format, caches
+        self.max_requests, self.q_len, self.bt_width, self.topk = max_requests, q_len, bt_width, topk
+        self.init_blocks, self.local_blocks, self.block_size = init_blocks, local_blocks, block_size
+        self.index_scale = B.pre_attn_index_scale_log2e(sm_scale)
+        sms = torch.cuda.get_device_properties(self.device).multi_processor_count
+        self.ws_bytes = B.pre_attn_attention_workspace_bytes(max_requests, q_len, n_kv_heads, sms)
+        if self.ws_bytes == 0:
+            raise ValueError(f"max_requests {max_requests}, q_len {q_len} or n_kv_heads {n_kv_heads} out of range")
+        # the first 256 bytes hold the status word
+        self.workspace = torch.empty(256 + self.ws_bytes, dtype=torch.uint8, device=self.device)
+        B.pre_attn_workspace_init(self.workspace, 256, torch.cuda.current_stream(self.device))
+        self.status = self.workspace.data_ptr()
+        self._attn = B.pa_attention_args(None, None, 1.0, 0, n_q_heads, n_kv_heads, cache_format, block_size,
+                                         kv_page_stride, B.ctypes.pointer(caches), None, None, None, None, 0, 0, q_len,
+                                         bt_width, sm_scale, None, 0, self.status + 256, self.ws_bytes, self.status,
+                                         flags)
+
+    def _stream(self, stream):
+        if torch.cuda.current_device() != self.device.index:
+            raise ValueError(f"the current device is not the reader's ({self.device})")
+        return torch.cuda.current_stream(self.device) if stream is None else stream
+
+    def _requests(self, seq_lens, block_table=None) -> int:
+        R = seq_lens.shape[0]
+        if R > self.max_requests:
+            raise ValueError(f"{R} requests: the reader holds {self.max_requests}")
+        self._ints(seq_lens, (R,), "seq_lens")
+        if block_table is not None:
+            self._ints(block_table, (R, self.bt_width), "block_table")
+        return R
+
+    def _ints(self, x, shape, name):
+        if x.dtype is not torch.int32 or tuple(x.shape) != shape or not x.is_contiguous():
+            raise ValueError(f"{name}: a contiguous int32 tensor of shape {shape} is wanted")
+
+    def _rows(self, x, dtypes, rows, cols, name):
+        if x.dtype not in dtypes or x.dim() != 2 or x.shape[0] != rows or x.shape[1] < cols or x.stride(1) != 1:
+            raise ValueError(f"{name}: [{rows}, >= {cols}] of {dtypes} with contiguous columns is wanted")
+        return x.stride(0) if rows > 1 else cols  # elements a row (a single row's stride says nothing)
+
+    def index_scores(self, iq, head: int, block_table, seq_lens, scores, *, scale: float | None = None, stream=None,
+                     check: bool = True) -> int:
+        """Scores of index_q head ``head`` (iq [M, >= (head + 1) * 128] bf16) into scores [M, >= bt_width * 128] f32."""
+        R = self._requests(seq_lens, block_table)
+        iq_stride = self._rows(iq, (torch.bfloat16,), R * self.q_len, (head + 1) * 128, "iq")
+        score_stride = self._rows(scores, (torch.float32,), R * self.q_len, self.bt_width * 128, "scores")
+        c, scale = self.caches, self.index_scale if scale is None else scale
+        if self.cache_format == B.PA_CACHE_FP8:
+            a = B.pa_index_args(iq.data_ptr(), iq_stride, head, c.index_cache, c.num_index_slots,
+                                block_table.data_ptr(), seq_lens.data_ptr(), R, self.q_len, self.bt_width,
+                                self.init_blocks, self.local_blocks, scale, scores.data_ptr(), score_stride,
+                                self.status, 0)
+            return B.pre_attn_index_scores(a, self._stream(stream), check)
+        a = B.pa_index_nvfp4_args(iq.data_ptr(), iq_stride, head, c.idx_cache, c.idx_pages, c.idx_page_bytes,
+                                  self.block_size, block_table.data_ptr(), seq_lens.data_ptr(), R, self.q_len,
+                                  self.bt_width, self.init_blocks, self.local_blocks, scale, scores.data_ptr(),
+                                  score_stride, self.status)
+        return B.pre_attn_index_scores_nvfp4(a, self._stream(stream), check)
+
+    def select_blocks(self, scores, seq_lens, blocks, counts, *, stream=None, check: bool = True) -> int:
+        """The blocks of each row and head from scores [heads, M, >= bt_width * 128] into blocks [M, heads, topk]."""
+        R = self._requests(seq_lens)
+        M, heads = R * self.q_len, scores.shape[0]
+        if (scores.dtype is not torch.float32 or scores.dim() != 3 or scores.shape[1] != M
+                or heads < 1 or scores.shape[2] < self.bt_width * 128 or scores.stride(2) != 1):
+            raise ValueError(f"scores: f32 [heads, {M}, >= {self.bt_width * 128}] with contiguous columns is wanted")
+        self._ints(blocks, (M, heads, self.topk), "blocks")
+        self._ints(counts, (M, heads), "counts")
+        stride = scores.stride(1) if M > 1 else self.bt_width * 128
+        a = B.pa_select_args(scores.data_ptr(), stride, scores.stride(0) if heads > 1 else M * stride, heads,
+                             seq_lens.data_ptr(), R, self.q_len, self.bt_width, self.init_blocks, self.local_blocks, self.topk,
+                             blocks.data_ptr(), counts.data_ptr(), self.status)
+        return B.pre_attn_select_blocks(a, self._stream(stream), check)
+
+    def attend(self, q, block_table, seq_lens, out, *, blocks=None, counts=None, q_fp8_scale: float = 1.0, stream=None,
+               check: bool = True) -> int:
+        """Attention of q [M, >= n_q_heads * 128] (bf16, or E4M3 with q_fp8_scale) into out (bf16, as wide): over the
+        blocks of each row and KV head (blocks [M, n_kv_heads, topk], counts [M, n_kv_heads]), or all without."""
+        R = self._requests(seq_lens, block_table)
+        M = R * self.q_len
+        q_stride = self._rows(q, (torch.bfloat16, torch.float8_e4m3fn), M, self.n_q_heads * 128, "q")
+        out_stride = self._rows(out, (torch.bfloat16,), M, self.n_q_heads * 128, "out")
+        a = self._attn
+        if q.dtype is torch.bfloat16:
+            a.q, a.q_fp8 = q.data_ptr(), None
+        else:
+            a.q, a.q_fp8, a.q_fp8_scale = None, q.data_ptr(), q_fp8_scale
+        a.q_stride, a.out, a.out_stride, a.R = q_stride, out.data_ptr(), out_stride, R
+        a.block_table, a.seq_lens = block_table.data_ptr(), seq_lens.data_ptr()
+        if blocks is None:
+            a.blocks = a.counts = None
+        else:
+            self._ints(blocks, (M, self.n_kv_heads, self.topk), "blocks")
+            if counts is None:
+                raise ValueError("blocks come with their counts")
+            self._ints(counts, (M, self.n_kv_heads), "counts")
+            a.blocks, a.counts, a.topk = blocks.data_ptr(), counts.data_ptr(), self.topk
+        return B.pre_attn_attention(a, self._stream(stream), check)
+
+    def device_status(self, stream=None) -> int:
+        """PA_DEV_* bits of the calls since the last reading (read and cleared; synchronises)."""
+        return B.pre_attn_device_status(self.workspace, self._stream(stream))
