@@ -16,7 +16,7 @@
 // producer warp keeps a ring of 128-key blocks in flight with bulk copies;
 // a query row's (up to 16) heads are the 16 rows of mma.sync m16n8k16, and
 // the eight compute warps are dealt to the item's rows: WPR = 8, 4, 2 or 1
-// warps a row, each with 1 / WPR of a block's keys.
+// warps a row, each with its part of the keys.
 //
 // Arithmetic.  E4M3 codes and E2M1 code x E4M3 scale are f16 values, so keys
 // and values are converted exactly in registers and multiplied on the f16
@@ -37,11 +37,16 @@
 #include "pa_device.cuh"
 #include "pa_f16.cuh"
 #include "pa_launch.h"
+#include "pa_tma.h"
 
 namespace pa {
 
 constexpr int kAtWarps = 8;                        // compute warps
-constexpr int kAtThreads = 32 * (kAtWarps + 1);    // and the producer
+constexpr int kAtThreads = 32 * (kAtWarps + 4);    // and the producer's warpgroup (one warp of it works)
+// Registers a thread after the split (setmaxnreg): the compute warps hold o,
+// the queries and the codes of 32 keys.  Their sum must not exceed what the
+// CTA was launched with, which launch_attn checks.
+constexpr int kAtComputeRegs = 200, kAtProducerRegs = 96;
 constexpr int kAtMaxRows = 8;                      // query rows an item
 constexpr int kAtMaxItems = 2048;                  // items the sliced grid lists in shared memory
 constexpr int kAtMaxWidth = 16384;                 // block-table width
@@ -64,7 +69,8 @@ struct AttnParams {
   const int32_t *block_table, *seq_lens, *blocks, *counts;
   int topk;                          // 0: every block
   int R, q_len, bt_width, n_kv, group;
-  int row_groups, rows_per;          // items of a (request, KV head), rows an item
+  int lg_kv, lg_groups;              // log2 of n_kv and of the items a (request, KV head) has
+  int rows_per;                      // rows an item (the last of a request may have fewer)
   int items, sliced;
   float score_scale, out_scale;
   __nv_bfloat16 *out;
@@ -76,6 +82,12 @@ struct AttnParams {
   int test_timeout;
 };
 
+// Tensor maps of a block's copies: FP8 K pages, V pages, K scales, V scales;
+// NVFP4 a KV head's K and V slots (pages of up to 128 tokens).
+struct AttnMaps {
+  CUtensorMap m[4];
+};
+
 template <int FMT>
 struct AttnStage;
 template <>
@@ -84,8 +96,9 @@ struct AttnStage<0> {  // K and V pages as they are (8 of 2048 bytes each), then
   static constexpr int stages(bool joined) { return joined ? 4 : 5; }
 };
 template <>
-struct AttnStage<1> {  // 128 x 64 bytes of K, of V, then 128 x 8 scale bytes of K (linear), of V (4-token groups)
-  static constexpr int kV = 8192, kKs = 16384, kVs = 17408, kBytes = 18432;
+struct AttnStage<1> {  // pieces of pt = min(block_size, 128) tokens: K codes (64 bytes a token), K scales (8), V codes,
+                       // V scales, as the page holds them
+  static constexpr int kBytes = 18432;
   static constexpr int stages(bool joined) { return joined ? 7 : 10; }
 };
 
@@ -96,7 +109,7 @@ struct AttnShared {
   int2 info[10];    // block (-1: the end of an item), rows that attend it
   int scan[kAtWarps];
   float2 ml[kAtWarps][16];
-  int offs[kAtMaxItems + 1];
+  int offs[kAtMaxItems + 8];
   uint16_t list[kAtMaxRows * kAtMaxTopk];
   uint32_t bits[kAtMaxRows][kAtMaxWidth / 32];
 };
@@ -118,10 +131,10 @@ struct AttnItem {
 };
 __device__ __forceinline__ AttnItem attn_item(const AttnParams &a, int it, bool *bad) {
   AttnItem x;
-  x.h = it % a.n_kv;
-  const int rg = it / a.n_kv;
-  x.r = rg / a.row_groups;
-  x.row0 = (rg - x.r * a.row_groups) * a.rows_per;
+  x.h = it & (a.n_kv - 1);
+  const int rg = it >> a.lg_kv;
+  x.r = rg >> a.lg_groups;
+  x.row0 = (rg - (x.r << a.lg_groups)) * a.rows_per;
   x.rows = min(a.rows_per, a.q_len - x.row0);
   x.seq = __ldg(a.seq_lens + x.r);
   if (x.seq > 0 && (x.seq < a.q_len || (x.seq - 1) / 128 + 1 > a.bt_width)) {
@@ -140,8 +153,10 @@ __device__ __forceinline__ int attn_units(const AttnParams &a, int it, bool *bad
   if (x.seq == 0) return 1;
   if (a.topk == 0) return x.blocks_upto(x.rows);
   int n = 0;
-  for (int i = 0; i < x.rows; ++i)
-    n += min(max(__ldg(a.counts + ((int64_t)x.r * a.q_len + x.row0 + i) * a.n_kv + x.h), 0), a.topk);
+  const int32_t *c = a.counts + ((int64_t)x.r * a.q_len + x.row0) * a.n_kv + x.h;
+#pragma unroll
+  for (int i = 0; i < kAtMaxRows; ++i)
+    if (i < x.rows) n += min(max(__ldg(c + i * a.n_kv), 0), a.topk);
   return max(n, 1);
 }
 
@@ -150,11 +165,22 @@ struct AttnSlice {
   int lo, hi, total, cta, ctas;
 };
 
+__device__ __forceinline__ void tma_pages(uint32_t dst, const CUtensorMap *map, int row, int page, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(page), "r"(smem_u32(bar))
+      : "memory");
+}
+
 template <int FMT, int WPR>
-__global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_constant__ AttnParams a) {
+__global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_constant__ AttnMaps maps,
+                                                                const __grid_constant__ AttnParams a) {
   using St = AttnStage<FMT>;
   constexpr int kStages = St::stages(WPR > 1);
-  constexpr int kKeys = 128 / WPR;  // keys of a block a warp takes
+  // a warp takes 32 keys at least: with eight warps a row, two groups of four
+  // take alternate blocks
+  constexpr int kParts = WPR > 4 ? 4 : WPR, kGroups = WPR / kParts, kKeys = 128 / kParts;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
   float *joint = reinterpret_cast<float *>(ring + kStages * St::kBytes);  // [warp][16 heads][128], WPR > 1
@@ -177,37 +203,33 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
   sl.cta = blockIdx.x;
   int first_item = blockIdx.x;
   if (a.sliced) {
-    // units of every item, then their running sums: 8 items a thread
-    constexpr int kPer = kAtMaxItems / (32 * kAtWarps);
-    int n[kPer], sum = 0;
+    // the running sums of the items' units, 256 items a round
+    int before = 0;
     bool bad = false;
-    if (warp < kAtWarps) {
+    for (int i0 = 0; i0 < a.items; i0 += 32 * kAtWarps) {
+      const int it = i0 + tid;
+      const int n = warp < kAtWarps && it < a.items ? attn_units(a, it, &bad) : 0;
+      int incl = n;
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int it = tid * kPer + k;
-        n[k] = it < a.items ? attn_units(a, it, &bad) : 0;
-        sum += n[k];
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
       }
-    }
-    int incl = sum;
+      if (warp < kAtWarps && lane == 31) sh.scan[warp] = incl;
+      __syncthreads();
+      int round = 0, mine = before + incl - n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      for (int w = 0; w < kAtWarps; ++w) {
+        const int v = sh.scan[w];
+        if (w < warp) mine += v;
+        round += v;
+      }
+      if (warp < kAtWarps) sh.offs[it] = mine;
+      before += round;
+      __syncthreads();
     }
-    if (warp < kAtWarps && lane == 31) sh.scan[warp] = incl;
+    if (tid == 0) sh.offs[a.items] = before;
     if (blockIdx.x == 0 && bad) set_status(a.status, kDevSlotRange);
-    __syncthreads();
-    if (warp < kAtWarps) {
-      int run = incl - sum;
-      for (int w = 0; w < warp; ++w) run += sh.scan[w];
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        sh.offs[tid * kPer + k] = run;
-        run += n[k];
-      }
-      if (tid == 32 * kAtWarps - 1) sh.offs[kAtMaxItems] = run;
-    }
     __syncthreads();
     sl.total = sh.offs[a.items];
     sl.ctas = min((int)gridDim.x, sl.total);
@@ -237,7 +259,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     return true;
   };
 
-  if (warp == kAtWarps) {
+  if (warp >= kAtWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtProducerRegs));
+    if (warp > kAtWarps) return;
     // -------------------------------------------------------------- producer
     int j = 0;
     bool ok = true;
@@ -261,16 +285,26 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
         // union's blocks u0 .. u1 in ascending order
         const int words = (nb + 31) / 32;
         __syncwarp();
-        for (int k = lane; k < x.rows * words; k += 32) sh.bits[k / words][k % words] = 0;
-        __syncwarp();
+        for (int i = 0; i < x.rows; ++i)
+          for (int w = lane; w < words; w += 32) sh.bits[i][w] = 0;
+        const int64_t at = ((int64_t)x.r * a.q_len + x.row0) * a.n_kv + x.h;
+        int count[kAtMaxRows];
+#pragma unroll
+        for (int i = 0; i < kAtMaxRows; ++i) count[i] = i < x.rows ? __ldg(a.counts + at + i * a.n_kv) : 0;
         bool out_of_range = false;
-        for (int k = lane; k < x.rows * a.topk; k += 32) {
-          const int i = k / a.topk, e = k - i * a.topk;
-          const int64_t at = ((int64_t)x.r * a.q_len + x.row0 + i) * a.n_kv + x.h;
-          if (e >= __ldg(a.counts + at)) continue;
-          const int b = __ldg(a.blocks + at * a.topk + e);
-          if (b < 0 || b > (x.first + i) / 128) out_of_range = true;
-          else atomicOr(&sh.bits[i][b >> 5], 1u << (b & 31));
+        for (int e0 = 0; e0 < a.topk; e0 += 32) {
+          int b[kAtMaxRows];
+          const bool in = e0 + lane < a.topk;
+#pragma unroll
+          for (int i = 0; i < kAtMaxRows; ++i)
+            b[i] = in && i < x.rows ? __ldg(a.blocks + (at + i * a.n_kv) * a.topk + e0 + lane) : 0;
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < kAtMaxRows; ++i)
+            if (in && e0 + lane < count[i]) {
+              if (b[i] < 0 || b[i] > (x.first + i) / 128) out_of_range = true;
+              else atomicOr(&sh.bits[i][b[i] >> 5], 1u << (b[i] & 31));
+            }
         }
         if (__any_sync(0xffffffffu, out_of_range) && lane == 0) set_status(a.status, kDevSlotRange);
         __syncwarp();
@@ -331,26 +365,20 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
             mbar_expect_tx(bar, St::kBytes);
           }
           __syncwarp();
-          if (FMT == 0) {  // 8 pages x (K, V, K scales, V scales), one copy a lane
-            const int pg = lane & 7, kind = lane >> 3;
-            const int64_t page = (id * a.kps + pg) * a.n_kv + x.h;
-            if (kind < 2)
-              bulk_g2s(st + kind * St::kV + pg * 2048, (kind ? a.v_cache : a.k_cache) + page * 2048, 2048, bar);
-            else
-              bulk_g2s(st + (kind == 3 ? St::kVs : St::kKs) + pg * 64, (kind == 3 ? a.v_scale : a.k_scale) + page * 16,
-                       64, bar);
-          } else {  // pieces of min(bs, 128) tokens x (K codes, K scales, V codes, V scales)
-            const int pt = min(a.bs, 128), pieces = 128 / pt;
-            for (int c = lane; c < 4 * pieces; c += 32) {
-              const int piece = c >> 2, v2 = (c >> 1) & 1, sf = c & 1;
-              const int64_t slot = id * 128 + piece * pt, page = slot / a.bs;
-              const int t0 = (int)(slot - page * a.bs);
-              const uint8_t *base8 = a.kv_cache + page * a.kv_page_bytes + (int64_t)(2 * x.h + v2) * a.bs * 72;
-              if (sf)
-                bulk_g2s(st + (v2 ? St::kVs : St::kKs) + piece * pt * 8, base8 + a.bs * 64 + t0 * 8, pt * 8, bar);
-              else
-                bulk_g2s(st + (v2 ? St::kV : 0) + piece * pt * 64, base8 + t0 * 64, pt * 64, bar);
+          if constexpr (FMT == 0) {  // the block's 8 pages of the head: K, V, their scales
+            if (lane < 4) {
+              const int off = lane == 0 ? 0 : lane == 1 ? St::kV : lane == 2 ? St::kKs : St::kVs;
+              tma_pages(smem_u32(st + off), &maps.m[lane], x.h, (int)(id * a.kps), bar);
             }
+          } else if (a.bs <= 128) {  // the head's K and V slots of 128 / bs pages
+            if (lane == 0)
+              tma_pages(smem_u32(st), &maps.m[0], 2 * x.h * max(a.bs >> 4, 1), (int)(id * (128 / a.bs)), bar);
+          } else if (lane < 4) {  // 128 tokens within a page: K codes, K scales, V codes, V scales
+            const int v2 = lane >> 1, sf = lane & 1;
+            const int64_t page = id * 128 / a.bs;
+            const int t0 = (int)(id * 128 - page * a.bs);
+            const uint8_t *base8 = a.kv_cache + page * a.kv_page_bytes + (int64_t)(2 * x.h + v2) * a.bs * 72;
+            bulk_g2s(st + v2 * 9216 + sf * 8192, base8 + (sf ? a.bs * 64 + t0 * 8 : t0 * 64), sf ? 1024 : 8192, bar);
           }
           ++j;
         }
@@ -372,7 +400,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
   }
 
   // ----------------------------------------------------------------- compute
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAtComputeRegs));
   const int row = warp / WPR, part = warp % WPR;
+  const int key0 = part % kParts * kKeys;
+  const int pt = min(a.bs, 128);  // NVFP4: tokens a piece of a stage
   int j = 0;
   uint32_t fin_phase = 0;
   auto fin_sync = [&]() {  // all compute warps; bounded
@@ -439,7 +470,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
     float mref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    int ev = -126;  // FP8: o is in units of 2^ev
+    int ev = -126;  // FP8: o is in units of 2^ev, V scales up to 2^(ev + 1) = vlimit
+    float vlimit = pow2i(-125);
     while (true) {
       const int s = j % kStages;
       bool got = mbar_wait(&sh.full[s], (uint32_t)(j / kStages) & 1, a.status, a.lim);
@@ -447,18 +479,20 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
       if (!__all_sync(0xffffffffu, got)) return;  // the warp gives up; the others' waits are bounded too
       const int2 info = sh.info[s];
       ++j;
-      if (info.x >= 0 && ((info.y >> row) & 1)) {
+      if (info.x >= 0 && ((info.y >> row) & 1) && (kGroups == 1 || (j & (kGroups - 1)) == part / kParts)) {
         const uint8_t *st = ring + s * St::kBytes;
         const bool cut = info.x * 128 + 127 > p;  // keys after the row's position
 #pragma unroll 1
-        for (int k0 = part * kKeys; k0 < (part + 1) * kKeys; k0 += 16) {
-          // scores of 16 keys: this thread's are keys k0 + 4 t .. + 3
-          float c[2][4];
+        for (int k0 = key0; k0 < key0 + kKeys; k0 += 32) {
+          // scores of 32 keys: this thread's are keys k0 + 16 y + 4 t + (e + rot) % 4, y = 0, 1, e = 0 .. 3
+          float c[4][4];
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
+          for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) c[nt][e] = 0.f;
-          float sv[2][4];  // [head g, g + 8][key]
+          float sv[2][8];     // [head g, g + 8][4 y + e]
+          uint32_t vraw[32];  // the value codes of those keys, read before the softmax needs its results
+          uint32_t vsf[2];
           if constexpr (FMT == 0) {
             // a page is [8 chunks of 16 dims][16 tokens][16 bytes].  Column n
             // of tile nt is key 4 (n / 2) + 2 (nt ^ n / 4) + n % 2: the eight
@@ -468,83 +502,133 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
             const uint32_t at = smem_u32(st) + (k0 >> 4) * 2048 + (lane >> 4) * 256 + tok * 16;
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc) {
-              uint32_t w[4];
-              ldsm_x4(at + cc * 512, w);
+              uint32_t w[2][4];
+              ldsm_x4(at + cc * 512, w[0]);
+              ldsm_x4(at + 2048 + cc * 512, w[1]);
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const uint2 k2 = e4m3x4_f16(w[y]);
-                mma_f16(c[y & 1], qf[2 * cc + (y >> 1)], k2.x, k2.y);
-              }
+              for (int z = 0; z < 2; ++z)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                  for (int u = 0; u < 2; ++u) {
+                    const uint2 k2 = e4m3x4_f16(w[y][2 * z + u]);
+                    mma_f16(c[2 * y + u], qf[2 * cc + z], k2.x, k2.y);
+                  }
+            }
+            // a page of values is [128 dims][16 tokens]
+            const uint32_t vat = smem_u32(st) + St::kV + (k0 >> 4) * 2048 + lane * 16;
+#pragma unroll
+            for (int q4 = 0; q4 < 8; ++q4) {
+              uint32_t w[4];
+              ldsm_x4(vat + q4 * 512, w);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) vraw[4 * q4 + y] = w[y];
             }
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                sv[hh][e] = t < 2 ? c[0][2 * hh + e] : c[1][2 * hh + e];
-                sv[hh][2 + e] = t < 2 ? c[1][2 * hh + e] : c[0][2 * hh + e];
-              }
+              for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float lo = c[2 * y][2 * hh + e], hi = c[2 * y + 1][2 * hh + e];
+                  sv[hh][4 * y + e] = t < 2 ? lo : hi;
+                  sv[hh][4 * y + 2 + e] = t < 2 ? hi : lo;
+                }
           } else {
             // a token is 64 bytes of codes; thread t takes the 16 of dims
             // 32 t .. + 31 (two scale groups).  Column n of tile nt is key
-            // 4 (n / 2) + 2 nt + n % 2
+            // 4 (n / 2) + (2 nt + n % 2 + n / 2) % 4: with that rotation the
+            // value reads below meet in a bank two at a time, not four
+            uint32_t f0[4], f1[4];
+            uint4 kw[4];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              const int tok = k0 + 4 * (g >> 1) + 2 * nt + (g & 1);
-              const uint4 w4 = *reinterpret_cast<const uint4 *>(st + tok * 64 + 16 * t);
-              const uint32_t sf2 = *reinterpret_cast<const uint16_t *>(st + St::kKs + tok * 8 + 2 * t);
-              const uint32_t fh = e4m3x4_f16(sf2).x;
-              const uint32_t f0 = __byte_perm(fh, fh, 0x1010), f1 = __byte_perm(fh, fh, 0x3232);
-              const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+            for (int nt = 0; nt < 4; ++nt) {
+              const int quad = k0 + 16 * (nt >> 1) + 4 * (g >> 1), in = quad & (pt - 1);
+              const int tok = in + ((2 * (nt & 1) + (g & 1) + (g >> 1)) & 3);
+              const uint8_t *kp = st + (quad - in) * 144;
+              kw[nt] = *reinterpret_cast<const uint4 *>(kp + tok * 64 + 16 * t);
+              const uint32_t fh = e4m3x4_f16(*reinterpret_cast<const uint16_t *>(kp + pt * 64 + tok * 8 + 2 * t)).x;
+              f0[nt] = __byte_perm(fh, fh, 0x1010), f1[nt] = __byte_perm(fh, fh, 0x3232);
+            }
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+              for (int nt = 0; nt < 4; ++nt) {
                 uint32_t h[4];
-                e2m1x8_f16(w[y], h);
-                const uint32_t f = y < 2 ? f0 : f1;
+                e2m1x8_f16(y == 0 ? kw[nt].x : y == 1 ? kw[nt].y : y == 2 ? kw[nt].z : kw[nt].w, h);
+                const uint32_t f = y < 2 ? f0[nt] : f1[nt];
                 mma_f16(c[nt], qf[2 * y], mul_f16x2(h[0], f), mul_f16x2(h[1], f));
                 mma_f16(c[nt], qf[2 * y + 1], mul_f16x2(h[2], f), mul_f16x2(h[3], f));
               }
+            // values: thread g takes dims 16 g .. + 15 (one scale group) of its tokens
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int quad = k0 + 16 * y + 4 * t, in = quad & (pt - 1);
+              const uint8_t *vp = st + (quad - in) * 144 + pt * 72;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint2 w2 = *reinterpret_cast<const uint2 *>(vp + (in + ((e + t) & 3)) * 64 + 8 * g);
+                vraw[16 * y + 2 * e] = w2.x, vraw[16 * y + 2 * e + 1] = w2.y;
+              }
+              const uint32_t f4 = *reinterpret_cast<const uint32_t *>(vp + pt * 64 + in * 8 + 4 * g);
+              vsf[y] = __funnelshift_r(f4, f4, 8 * t);
             }
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) sv[hh][e] = c[0][2 * hh + e], sv[hh][2 + e] = c[1][2 * hh + e];
+              for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  sv[hh][4 * y + e] = c[2 * y][2 * hh + e], sv[hh][4 * y + 2 + e] = c[2 * y + 1][2 * hh + e];
           }
           // scale, mask
-          float vs[4];
-          if constexpr (FMT == 0) {
-            const float4 k4 = *reinterpret_cast<const float4 *>(st + St::kKs + (k0 + 4 * t) * 4);
-            const float4 v4 = *reinterpret_cast<const float4 *>(st + St::kVs + (k0 + 4 * t) * 4);
-            const float ks[4] = {k4.x, k4.y, k4.z, k4.w};
-            vs[0] = v4.x, vs[1] = v4.y, vs[2] = v4.z, vs[3] = v4.w;
+          float vs[8];
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
+          for (int y = 0; y < 2; ++y) {
+            float ks[4] = {1.f, 1.f, 1.f, 1.f};
+            if constexpr (FMT == 0) {
+              const float4 k4 = *reinterpret_cast<const float4 *>(st + St::kKs + (k0 + 16 * y + 4 * t) * 4);
+              const float4 v4 = *reinterpret_cast<const float4 *>(st + St::kVs + (k0 + 16 * y + 4 * t) * 4);
+              ks[0] = k4.x, ks[1] = k4.y, ks[2] = k4.z, ks[3] = k4.w;
+              vs[4 * y] = v4.x, vs[4 * y + 1] = v4.y, vs[4 * y + 2] = v4.z, vs[4 * y + 3] = v4.w;
+            }
 #pragma unroll
-              for (int e = 0; e < 4; ++e) sv[hh][e] *= ks[e] * sc[hh];
-          } else {
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) sv[hh][e] *= sc[hh];
+            for (int e = 0; e < 4; ++e) {
+              sv[0][4 * y + e] *= FMT == 0 ? ks[e] * sc[0] : sc[0];
+              sv[1][4 * y + e] *= FMT == 0 ? ks[e] * sc[1] : sc[1];
+            }
           }
-          int left = 4;  // of this thread's four keys, those up to the row's position
-          if (cut) {
-            left = min(max(p - info.x * 128 - k0 - 4 * t + 1, 0), 4);
+          if (cut) {  // keys after the row's position: no score, no value (whatever the cache holds there)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (e >= left) {
-                sv[0][e] = sv[1][e] = -INFINITY;
-                if constexpr (FMT == 0) vs[e] = 0.f;
-              }
+            for (int y = 0; y < 2; ++y) {
+              const int left = p - info.x * 128 - k0 - 16 * y - 4 * t;  // the last of the four keys that counts
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if ((FMT == 0 ? e : (e + t) & 3) > left) {
+                  sv[0][4 * y + e] = sv[1][4 * y + e] = -INFINITY;
+                  if constexpr (FMT == 0) {
+                    vs[4 * y + e] = 0.f;
+#pragma unroll
+                    for (int n = 0; n < 16; ++n) vraw[16 * y + n] &= ~(0xffu << (8 * e));
+                  } else {
+                    vraw[16 * y + 2 * e] = vraw[16 * y + 2 * e + 1] = 0u;
+                    vsf[y] &= ~(0xffu << (8 * e));
+                  }
+                }
+            }
           }
           // the reference m (and the V unit) move only when a score (a V
           // scale) has outgrown them
-          const float top0 = fmaxf(fmaxf(sv[0][0], sv[0][1]), fmaxf(sv[0][2], sv[0][3]));
-          const float top1 = fmaxf(fmaxf(sv[1][0], sv[1][1]), fmaxf(sv[1][2], sv[1][3]));
-          bool grow = top0 > mref[0] + kAtSlack || top1 > mref[1] + kAtSlack;
-          float vtop = 0.f;
+          float top[2], vtop = 0.f;
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh)
+            top[hh] = fmaxf(fmaxf(fmaxf(sv[hh][0], sv[hh][1]), fmaxf(sv[hh][2], sv[hh][3])),
+                            fmaxf(fmaxf(sv[hh][4], sv[hh][5]), fmaxf(sv[hh][6], sv[hh][7])));
+          bool grow = top[0] > mref[0] + kAtSlack || top[1] > mref[1] + kAtSlack;
           if constexpr (FMT == 0) {
-            vtop = fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])), fmaxf(fabsf(vs[2]), fabsf(vs[3])));
-            grow |= vtop > pow2i(min(ev + 1, 127));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) vtop = fmaxf(vtop, fabsf(vs[e]));
+            grow |= vtop > vlimit;
           }
           if (__any_sync(0xffffffffu, grow)) {
             float f = 1.f;
@@ -552,81 +636,67 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
               const int e2 = max(ev, min(exponent_of(quad_max(vtop)), 126));
               f = e2 - ev > 125 ? 0.f : pow2i(ev - e2);  // nothing summed yet where it is 0
               ev = e2;
+              vlimit = pow2i(ev + 1);
             }
-            const float nm[2] = {fmaxf(mref[0], quad_max(top0)), fmaxf(mref[1], quad_max(top1))};
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              const float al = nm[hh] == mref[hh] ? 1.f : ex2_approx(mref[hh] - nm[hh]);
-              mref[hh] = nm[hh];
+              const float nm = fmaxf(mref[hh], quad_max(top[hh]));
+              const float al = nm == mref[hh] ? 1.f : ex2_approx(mref[hh] - nm);
+              mref[hh] = nm;
               l[hh] *= al;
 #pragma unroll
               for (int n = 0; n < 16; ++n) o[n][2 * hh] *= al * f, o[n][2 * hh + 1] *= al * f;
             }
           }
-          uint32_t pa[4];
+          uint32_t pa[2][4];
           {
             float unit = 1.f;
             if constexpr (FMT == 0) unit = pow2i(-ev);
-            float w[2][4];
+            float w[2][8];
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
               const float base = mref[hh] == -INFINITY ? 0.f : mref[hh] - kAtLift;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float y = ex2_approx(sv[hh][e] - base);
-                l[hh] += y;
-                w[hh][e] = FMT == 0 ? y * (vs[e] * unit) : y;
+              for (int e = 0; e < 8; ++e) {
+                const float x2 = ex2_approx(sv[hh][e] - base);
+                l[hh] += x2;
+                w[hh][e] = FMT == 0 ? x2 * (vs[e] * unit) : x2;
               }
             }
-            pa[0] = f16x2_bits(w[0][0], w[0][1]);
-            pa[1] = f16x2_bits(w[1][0], w[1][1]);
-            pa[2] = f16x2_bits(w[0][2], w[0][3]);
-            pa[3] = f16x2_bits(w[1][2], w[1][3]);
-          }
-          // o += weights . values (keys 4 t, 4 t + 1 | 4 t + 2, 4 t + 3 are this thread's k rows)
-          if constexpr (FMT == 0) {
-            // a page is [128 dims][16 tokens]: tile n's rows are dims 8 n ..
-            const uint32_t keep = left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
-            const uint32_t at = smem_u32(st) + St::kV + (k0 >> 4) * 2048 + lane * 16;
-#pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-              uint32_t w[4];
-              ldsm_x4(at + q4 * 512, w);
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const uint2 v2 = e4m3x4_f16(cut ? w[y] & keep : w[y]);
-                mma_f16(o[4 * q4 + y], pa, v2.x, v2.y);
-              }
-            }
-          } else {
-            // thread g takes dims 16 g .. + 15 (one scale group) of its four
-            // tokens; nibbles of two tokens are paired before the conversion
-            uint32_t w[4][2];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint2 w2 = *reinterpret_cast<const uint2 *>(st + St::kV + (k0 + 4 * t + e) * 64 + 8 * g);
-              w[e][0] = w2.x, w[e][1] = w2.y;
-            }
-            uint32_t sf4 = *reinterpret_cast<const uint32_t *>(st + St::kVs + (k0 + 4 * t) * 8 + 4 * g);
-            if (cut) {
-              sf4 &= left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (e >= left) w[e][0] = w[e][1] = 0u;
-            }
-            const uint2 f = e4m3x4_f16(sf4);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              constexpr uint32_t kLow = 0x0f0f0f0fu;
-              uint32_t e01[4], d01[4], e23[4], d23[4];  // even, odd dims of tokens 0, 1 and 2, 3
-              e2m1x8_f16((w[0][y] & kLow) | ((w[1][y] & kLow) << 4), e01);
-              e2m1x8_f16(((w[0][y] >> 4) & kLow) | (w[1][y] & ~kLow), d01);
-              e2m1x8_f16((w[2][y] & kLow) | ((w[3][y] & kLow) << 4), e23);
-              e2m1x8_f16(((w[2][y] >> 4) & kLow) | (w[3][y] & ~kLow), d23);
+              pa[y][0] = f16x2_bits(w[0][4 * y], w[0][4 * y + 1]);
+              pa[y][1] = f16x2_bits(w[1][4 * y], w[1][4 * y + 1]);
+              pa[y][2] = f16x2_bits(w[0][4 * y + 2], w[0][4 * y + 3]);
+              pa[y][3] = f16x2_bits(w[1][4 * y + 2], w[1][4 * y + 3]);
+            }
+          }
+          // o += weights . values
 #pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                mma_f16(o[8 * y + 2 * b], pa, mul_f16x2(e01[b], f.x), mul_f16x2(e23[b], f.y));
-                mma_f16(o[8 * y + 2 * b + 1], pa, mul_f16x2(d01[b], f.x), mul_f16x2(d23[b], f.y));
+          for (int y = 0; y < 2; ++y) {
+            if constexpr (FMT == 0) {
+#pragma unroll
+              for (int n = 0; n < 16; ++n) {
+                const uint2 v2 = e4m3x4_f16(vraw[16 * y + n]);
+                mma_f16(o[n], pa[y], v2.x, v2.y);
+              }
+            } else {
+              // nibbles of two tokens are paired before the conversion
+              const uint2 f = e4m3x4_f16(vsf[y]);
+              const uint32_t *w = vraw + 16 * y;
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                constexpr uint32_t kLow = 0x0f0f0f0fu;
+                uint32_t e01[4], d01[4], e23[4], d23[4];  // even, odd dims of tokens 0, 1 and 2, 3
+                e2m1x8_f16((w[z] & kLow) | ((w[2 + z] & kLow) << 4), e01);
+                e2m1x8_f16(((w[z] >> 4) & kLow) | (w[2 + z] & ~kLow), d01);
+                e2m1x8_f16((w[4 + z] & kLow) | ((w[6 + z] & kLow) << 4), e23);
+                e2m1x8_f16(((w[4 + z] >> 4) & kLow) | (w[6 + z] & ~kLow), d23);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                  mma_f16(o[8 * z + 2 * b], pa[y], mul_f16x2(e01[b], f.x), mul_f16x2(e23[b], f.y));
+                  mma_f16(o[8 * z + 2 * b + 1], pa[y], mul_f16x2(d01[b], f.x), mul_f16x2(d23[b], f.y));
+                }
               }
             }
           }
@@ -677,17 +747,25 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
 #pragma unroll
               for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int n = 0; n < 16; n += 2)
-                  *reinterpret_cast<uint32_t *>(dst + 16 * (2 * t + e) + n) =
-                      bf16x2_bits(o[n][2 * hh + e] * inv, o[n + 1][2 * hh + e] * inv);
+                for (int n = 0; n < 16; n += 8) {
+                  auto two = [&](int k) { return bf16x2_bits(o[k][2 * hh + e] * inv, o[k + 1][2 * hh + e] * inv); };
+                  *reinterpret_cast<uint4 *>(dst + 16 * (2 * t + e) + n) = make_uint4(two(n), two(n + 2), two(n + 4), two(n + 6));
+                }
             }
           } else {
             float *dst = pp + (row * 16 + head) * kHeadDim;
+            if constexpr (FMT == 0) {
 #pragma unroll
-            for (int n = 0; n < 16; ++n)
+              for (int n = 0; n < 16; ++n)
+                *reinterpret_cast<float2 *>(dst + 8 * n + 2 * t) = make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
+            } else {
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                dst[FMT == 0 ? 8 * n + 2 * t + e : 16 * (2 * t + e) + n] = o[n][2 * hh + e];
+#pragma unroll
+                for (int n = 0; n < 16; n += 4)
+                  *reinterpret_cast<float4 *>(dst + 16 * (2 * t + e) + n) =
+                      make_float4(o[n][2 * hh + e], o[n + 1][2 * hh + e], o[n + 2][2 * hh + e], o[n + 3][2 * hh + e]);
+            }
             if (t == 0)
               *reinterpret_cast<float2 *>(pp + kAtMaxRows * 16 * kHeadDim + (row * 16 + head) * 2) =
                   make_float2(mref[hh], l[hh]);
@@ -695,45 +773,59 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
         }
       }
     } else {
-      // the row's warps meet in shared memory
+      // the row's warps meet in shared memory: [warp][head][128], pairs of
+      // dims moved within the row so that a store's lanes hit distinct banks
+      auto place = [](int head, int d) {
+        return head * kHeadDim + (d ^ ((head & 3) << 3) ^ (FMT == 0 ? 0 : 2 * (d >> 5)));
+      };
       float *mine = joint + warp * 16 * kHeadDim;
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const int head = g + 8 * hh;
+        if constexpr (FMT == 0) {
 #pragma unroll
-        for (int n = 0; n < 16; ++n)
+          for (int n = 0; n < 16; ++n)
+            *reinterpret_cast<float2 *>(mine + place(head, 8 * n + 2 * t)) = make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
+        } else {
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            mine[head * kHeadDim + (FMT == 0 ? 8 * n + 2 * t + e : 16 * (2 * t + e) + n)] = o[n][2 * hh + e];
+#pragma unroll
+            for (int n = 0; n < 16; n += 2)
+              *reinterpret_cast<float2 *>(mine + place(head, 16 * (2 * t + e) + n)) =
+                  make_float2(o[n][2 * hh + e], o[n + 1][2 * hh + e]);
+        }
         if (t == 0) sh.ml[warp][head] = make_float2(mref[hh], l[hh]);
       }
       if (!fin_sync()) return;
       if (row < x.rows) {
         for (int head = part; head < a.group; head += WPR) {
-          float top = -INFINITY;
+          float top = -INFINITY, sum = 0.f;
 #pragma unroll
           for (int w = 0; w < WPR; ++w) top = fmaxf(top, sh.ml[row * WPR + w][head].x);
-          float sum = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // dims 2 lane, 64 + 2 lane
 #pragma unroll
           for (int w = 0; w < WPR; ++w) {
             const float2 ml = sh.ml[row * WPR + w][head];
-            const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ml.x == top ? 1.f : ex2_approx(ml.x - top);
-            const float4 y =
-                *reinterpret_cast<const float4 *>(joint + ((row * WPR + w) * 16 + head) * kHeadDim + 4 * lane);
+            const float f = ml.x == top ? 1.f : ex2_approx(ml.x - top);
             sum += f * ml.y;
-            if (f != 0.f) acc.x += f * y.x, acc.y += f * y.y, acc.z += f * y.z, acc.w += f * y.w;
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const float2 y = *reinterpret_cast<const float2 *>(joint + (row * WPR + w) * 16 * kHeadDim +
+                                                                 place(head, 64 * z + 2 * lane));
+              if (f != 0.f) acc[z].x += f * y.x, acc[z].y += f * y.y;
+            }
           }
-          if (whole) {
-            const float inv = sum == 0.f ? 0.f : a.out_scale / sum;
-            *reinterpret_cast<uint2 *>(a.out + m * a.out_stride + (int64_t)(x.h * a.group + head) * kHeadDim + 4 * lane) =
-                make_uint2(bf16x2_bits(acc.x * inv, acc.y * inv), bf16x2_bits(acc.z * inv, acc.w * inv));
-          } else {
-            *reinterpret_cast<float4 *>(pp + (row * 16 + head) * kHeadDim + 4 * lane) = acc;
-            if (lane == 0)
-              *reinterpret_cast<float2 *>(pp + kAtMaxRows * 16 * kHeadDim + (row * 16 + head) * 2) =
-                  make_float2(top, sum);
+          const float inv = sum == 0.f ? 0.f : a.out_scale / sum;
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            if (whole)
+              *reinterpret_cast<uint32_t *>(a.out + m * a.out_stride + (int64_t)(x.h * a.group + head) * kHeadDim + 64 * z +
+                                            2 * lane) = bf16x2_bits(acc[z].x * inv, acc[z].y * inv);
+            else
+              *reinterpret_cast<float2 *>(pp + (row * 16 + head) * kHeadDim + 64 * z + 2 * lane) = acc[z];
           }
+          if (!whole && lane == 0)
+            *reinterpret_cast<float2 *>(pp + kAtMaxRows * 16 * kHeadDim + (row * 16 + head) * 2) = make_float2(top, sum);
         }
       }
       if (!fin_sync()) return;  // `joint` is free for the next item
@@ -742,49 +834,98 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
 }
 
 // Join the partial results of items that several CTAs share, in CTA order:
-// a warp an (item, row, head), a lane four dims.  The first CTA's partial is
-// its slot 1 (the item starts there), the others' their slot 0.
-__global__ void __launch_bounds__(128) pa_attn_join_kernel(const __grid_constant__ AttnParams a, int grid) {
+// W warps a (item, row, head), each every W-th partial, 16 of them in flight
+// a lane (four dims); the W sums meet in shared memory.  The first CTA's
+// partial is its slot 1 (the item starts there), the others' their slot 0.
+constexpr int kJoinWarps = 8;
+template <int W>
+__global__ void __launch_bounds__(32 * kJoinWarps) pa_attn_join_kernel(const __grid_constant__ AttnParams a, int grid) {
+  __shared__ float4 acc_s[kJoinWarps][32];
+  __shared__ float2 ml_s[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int it = blockIdx.x / a.rows_per, row = blockIdx.x % a.rows_per, head = 4 * blockIdx.y + warp;
+  const int it = blockIdx.x / a.rows_per, row = blockIdx.x % a.rows_per;
+  const int head = blockIdx.y * (kJoinWarps / W) + warp / W;
+  const int h = it & (a.n_kv - 1), rg = it >> a.lg_kv, r = rg >> a.lg_groups;
+  const int row0 = (rg - (r << a.lg_groups)) * a.rows_per;
   pdl_wait();
-  if (head >= a.group) return;
   const int2 s = a.shares[it];
   const int c0 = max(s.x, 0), c1 = min(s.y, grid - 1);
-  if (c1 <= c0) return;
-  const int rg = it / a.n_kv, h = it % a.n_kv, r = rg / a.row_groups, row0 = (rg - r * a.row_groups) * a.rows_per;
-  if (row0 + row >= a.q_len) return;
-  auto part = [&](int c) { return a.part + (int64_t)(2 * c + (c == c0 ? 1 : 0)) * kAtPartFloats; };
-  const int at = row * 16 + head;
-  float top = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part(c)[kAtMaxRows * 16 * kHeadDim + 2 * at]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float sum = 0.f;
+  if (c1 <= c0 || row0 + row >= a.q_len) return;  // the same for the whole CTA
+  const bool have = head < a.group;
+  const float *base = a.part + (int64_t)2 * c0 * kAtPartFloats + (row * 16 + (have ? head : 0)) * kHeadDim + 4 * lane;
+  const float *mls = a.part + (int64_t)2 * c0 * kAtPartFloats + kAtMaxRows * 16 * kHeadDim + (row * 16 + (have ? head : 0)) * 2;
+  float top = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float2 ml = *reinterpret_cast<const float2 *>(part(c) + kAtMaxRows * 16 * kHeadDim + 2 * at);
-    const float4 y = *reinterpret_cast<const float4 *>(part(c) + at * kHeadDim + 4 * lane);
-    const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ml.x == top ? 1.f : ex2_approx(ml.x - top);
-    sum += f * ml.y;
-    if (f != 0.f) acc.x += f * y.x, acc.y += f * y.y, acc.z += f * y.z, acc.w += f * y.w;
+  constexpr int kIn = 16;
+  const int n = c1 - c0 + 1;
+  for (int k0 = warp % W; k0 < n; k0 += W * kIn) {
+    float4 y[kIn];
+    float2 ml[kIn];
+    float t2 = top;
+#pragma unroll
+    for (int k = 0; k < kIn; ++k) {
+      const int c = k0 + k * W;
+      const int64_t off = (int64_t)(2 * c + (c == 0 ? 1 : 0)) * kAtPartFloats;
+      ml[k] = c < n ? *reinterpret_cast<const float2 *>(mls + off) : make_float2(-INFINITY, 0.f);
+      y[k] = c < n ? *reinterpret_cast<const float4 *>(base + off) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < kIn; ++k) t2 = fmaxf(t2, ml[k].x);
+    const float f0 = top == t2 ? 1.f : ex2_approx(top - t2);
+    top = t2;
+    sum *= f0, acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
+#pragma unroll
+    for (int k = 0; k < kIn; ++k) {
+      const float f = ml[k].x == top ? 1.f : ex2_approx(ml[k].x - top);
+      sum += f * ml[k].y;
+      if (f != 0.f) acc.x += f * y[k].x, acc.y += f * y[k].y, acc.z += f * y[k].z, acc.w += f * y[k].w;
+    }
   }
+  if constexpr (W > 1) {
+    acc_s[warp][lane] = acc;
+    if (lane == 0) ml_s[warp] = make_float2(top, sum);
+    __syncthreads();
+    if (warp % W) return;
+    float t2 = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < W; ++w) t2 = fmaxf(t2, ml_s[warp + w].x);
+    sum = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float2 ml = ml_s[warp + w];
+      const float4 y = acc_s[warp + w][lane];
+      const float f = ml.x == t2 ? 1.f : ex2_approx(ml.x - t2);
+      sum += f * ml.y;
+      if (f != 0.f) acc.x += f * y.x, acc.y += f * y.y, acc.z += f * y.z, acc.w += f * y.w;
+    }
+  }
+  if (!have) return;
   const float inv = sum == 0.f ? 0.f : a.out_scale / sum;
   const int64_t m = (int64_t)r * a.q_len + row0 + row;
   *reinterpret_cast<uint2 *>(a.out + m * a.out_stride + (int64_t)(h * a.group + head) * kHeadDim + 4 * lane) =
       make_uint2(bf16x2_bits(acc.x * inv, acc.y * inv), bf16x2_bits(acc.z * inv, acc.w * inv));
 }
 
-// Rows an item of q_len rows takes, and items a (request, KV head).
-static inline void attn_rows(int q_len, int *groups, int *rows) {
-  *groups = (q_len + kAtMaxRows - 1) / kAtMaxRows;
-  *rows = (q_len + *groups - 1) / *groups;
+static bool attn_maps(AttnMaps *maps, const AttnParams &a, int fmt) {
+  if (fmt == 0) {
+    const uint64_t kv = (uint64_t)a.n_kv, pages = (uint64_t)a.num_pages16;
+    return map_page_rows(&maps->m[0], a.k_cache, 2048, kv, kv * 2048, pages, 1, 8) &&
+           map_page_rows(&maps->m[1], a.v_cache, 2048, kv, kv * 2048, pages, 1, 8) &&
+           map_page_rows(&maps->m[2], a.k_scale, 64, kv, kv * 64, pages, 1, 8) &&
+           map_page_rows(&maps->m[3], a.v_scale, 64, kv, kv * 64, pages, 1, 8);
+  }
+  if (a.bs > 128) return true;
+  const uint32_t row = 72u * (a.bs < 16 ? a.bs : 16), per = a.bs < 16 ? 1 : a.bs / 16;  // rows of a slot
+  return map_page_rows(&maps->m[0], a.kv_cache, row, (uint64_t)2 * a.n_kv * per, (uint64_t)a.kv_page_bytes,
+                       (uint64_t)a.kv_pages, 2 * per, 128u / a.bs);
 }
 
 template <int FMT>
 static cudaError_t launch_attn(const AttnParams &a, int sms, bool pdl, cudaStream_t stream) {
-  using Kern = void (*)(const AttnParams);
+  AttnMaps maps;
+  if (!attn_maps(&maps, a, FMT)) return cudaErrorInvalidValue;
+  using Kern = void (*)(const AttnMaps, const AttnParams);
   Kern kern = pa_attn_kernel<FMT, 1>;
   int smem = attn_smem<FMT, 1>();
   if (a.rows_per == 1) kern = pa_attn_kernel<FMT, 8>, smem = attn_smem<FMT, 8>();
@@ -792,6 +933,16 @@ static cudaError_t launch_attn(const AttnParams &a, int sms, bool pdl, cudaStrea
   else if (a.rows_per <= 4) kern = pa_attn_kernel<FMT, 2>, smem = attn_smem<FMT, 2>();
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), smem);
   if (e != cudaSuccess) return e;
+  static int regs[4] = {0, 0, 0, 0};  // of the four kernels at launch
+  int &held = regs[a.rows_per == 1 ? 0 : a.rows_per == 2 ? 1 : a.rows_per <= 4 ? 2 : 3];
+  if (held == 0) {
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, reinterpret_cast<const void *>(kern));
+    if (e != cudaSuccess) return e;
+    held = at.numRegs;
+  }
+  if (held * kAtThreads < 32 * kAtWarps * kAtComputeRegs + (kAtThreads - 32 * kAtWarps) * kAtProducerRegs)
+    return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -802,12 +953,14 @@ static cudaError_t launch_attn(const AttnParams &a, int sms, bool pdl, cudaStrea
   cfg.gridDim = dim3(a.sliced ? sms : a.items);
   cfg.blockDim = dim3(kAtThreads);
   cfg.dynamicSmemBytes = smem;
-  e = cudaLaunchKernelEx(&cfg, kern, a);
+  e = cudaLaunchKernelEx(&cfg, kern, maps, a);
   if (e != cudaSuccess || !a.sliced || a.test_timeout) return e;
-  cfg.gridDim = dim3(a.items * a.rows_per, (a.group + 3) / 4);
-  cfg.blockDim = dim3(128);
+  // few items: many partials each, a CTA a head; else a warp a head
+  const bool many = a.items * 8 <= sms;
+  cfg.gridDim = dim3(a.items * a.rows_per, many ? a.group : (a.group + kJoinWarps - 1) / kJoinWarps);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, pa_attn_join_kernel, a, sms);
+  return cudaLaunchKernelEx(&cfg, many ? pa_attn_join_kernel<kJoinWarps> : pa_attn_join_kernel<1>, a, sms);
 }
 
 }  // namespace pa
@@ -842,14 +995,15 @@ extern "C" int pre_attn_attention(const pa_attention_args *in, void *stream) {
   int kps = x.kv_page_stride;
   if (fp8) {
     if (!c.k_cache || !c.v_cache || !c.k_scale || !c.v_scale) return PA_ERR_NULL;
-    if (x.block_size != 16 || (kps != 0 && kps < 8) || c.num_pages16 < 1) return PA_ERR_CONFIG;
+    if (x.block_size != 16 || (kps != 0 && kps < 8) || c.num_pages16 < 1 || c.num_pages16 > INT32_MAX)
+      return PA_ERR_CONFIG;
     if (!aligned(c.k_cache, 16) || !aligned(c.v_cache, 16) || !aligned(c.k_scale, 16) || !aligned(c.v_scale, 16))
       return PA_ERR_ALIGN;
     if (kps == 0) kps = 8;
   } else {
     if (!c.kv_cache) return PA_ERR_NULL;
     const int bs = x.block_size;
-    if (bs < 4 || bs % 4 || bs > 1024 || c.kv_pages < 1) return PA_ERR_CONFIG;
+    if (bs < 4 || bs % 4 || bs > 1024 || c.kv_pages < 1 || c.kv_pages > INT32_MAX) return PA_ERR_CONFIG;
     if (128 % bs && bs % 128) return PA_ERR_UNSUPPORTED;
     if (c.kv_page_bytes < (int64_t)2 * x.n_kv_heads * bs * 72) return PA_ERR_CONFIG;
     if (!(c.k_global_scale > 0.0f) || !(c.v_global_scale > 0.0f)) return PA_ERR_CONFIG;
@@ -895,8 +1049,10 @@ extern "C" int pre_attn_attention(const pa_attention_args *in, void *stream) {
   a.bt_width = x.bt_width;
   a.n_kv = x.n_kv_heads;
   a.group = x.n_q_heads / x.n_kv_heads;
-  pa::attn_rows(x.q_len, &a.row_groups, &a.rows_per);
-  a.items = x.R * a.row_groups * x.n_kv_heads;
+  a.lg_kv = x.n_kv_heads == 4 ? 2 : x.n_kv_heads - 1;
+  a.lg_groups = x.q_len > pa::kAtMaxRows ? 1 : 0;
+  a.rows_per = (x.q_len + a.lg_groups) >> a.lg_groups;
+  a.items = x.R * x.n_kv_heads << a.lg_groups;
   a.sliced = a.items <= pa::kAtMaxItems;
   a.score_scale = (float)((double)x.sm_scale * 1.4426950408889634 * (x.q ? 1.0 : (double)x.q_fp8_scale) *
                           (fp8 ? 1.0 : (double)c.k_global_scale));

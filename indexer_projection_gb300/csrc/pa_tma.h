@@ -55,4 +55,20 @@ inline bool map_scale_atoms(CUtensorMap *map, const void *base, int row_blocks, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of row_bytes (a multiple of 16) in pages: dim 0 a row, dim 1 the
+// page's rows (row_bytes apart), dim 2 the pages (page_bytes apart); one box
+// is box_rows rows of each of box_pages pages, in that order.
+inline bool map_page_rows(CUtensorMap *map, const void *base, uint32_t row_bytes, uint64_t rows, uint64_t page_bytes,
+                          uint64_t pages, uint32_t box_rows, uint32_t box_pages) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)row_bytes / 8, (cuuint64_t)rows, (cuuint64_t)pages};
+  cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)page_bytes};
+  cuuint32_t box[3] = {row_bytes / 8, box_rows, box_pages};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 3, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace pa
