@@ -93,35 +93,49 @@ struct AttnStage;
 template <>
 struct AttnStage<0> {  // K and V pages as they are (8 of 2048 bytes each), then the scales of 128 tokens
   static constexpr int kV = 16384, kKs = 32768, kVs = 33280, kBytes = 33792;
-  static constexpr int stages(bool joined) { return joined ? 4 : 5; }
 };
 template <>
 struct AttnStage<1> {  // pieces of pt = min(block_size, 128) tokens: K codes (64 bytes a token), K scales (8), V codes,
                        // V scales, as the page holds them
   static constexpr int kBytes = 18432;
-  static constexpr int stages(bool joined) { return joined ? 7 : 10; }
+};
+constexpr int kAtMaxStages = 10;
+
+// 32 blocks of a segment, resolved ahead of their copies.
+struct AttnBatch {
+  int blk[32];   // ids in the cache (-1: none)
+  int2 info[32]; // block of the request, rows that attend it
+  int n, seq, first_pos;
+  int first, last;  // of the segment
 };
 
+template <int ROWS>  // rows of an item at most
 struct AttnShared {
-  uint64_t full[10], empty[10];
-  uint64_t fin;     // the compute warps, twice an item
-  uint64_t never;   // testing: nothing arrives on it
-  int2 info[10];    // block (-1: the end of an item), rows that attend it
+  uint64_t full[kAtMaxStages], empty[kAtMaxStages];
+  uint64_t batch_full[2], batch_empty[2];
+  uint64_t q_full, q_empty;  // an item's queries; read into registers at once
+  uint64_t fin;              // the compute warps among themselves
+  uint64_t never;            // testing: nothing arrives on it
+  int2 info[kAtMaxStages];   // a stage's block (-1: the end of a segment), rows that attend it
+  int2 q_item;               // first row's position, keys
   int scan[kAtWarps];
-  float2 ml[kAtWarps][16];
+  AttnBatch batch[2];
+  float2 ml[kAtWarps / 2][16];
   int offs[kAtMaxItems + 8];
-  uint16_t list[kAtMaxRows * kAtMaxTopk];
-  uint32_t bits[kAtMaxRows][kAtMaxWidth / 32];
+  uint16_t list[ROWS * kAtMaxTopk];
+  uint32_t bits[ROWS][kAtMaxWidth / 32];
 };
 
+constexpr int kAtSmem = 232448;  // 227 KB a CTA
 template <int FMT, int WPR>
-constexpr int attn_smem() {
-  return AttnStage<FMT>::stages(WPR > 1) * AttnStage<FMT>::kBytes + (WPR > 1 ? kAtWarps * 16 * kHeadDim * 4 : 0) +
-         (int)sizeof(AttnShared) + 128;
-}
-static_assert(attn_smem<0, 8>() <= 232448 && attn_smem<0, 1>() <= 232448 && attn_smem<1, 8>() <= 232448 &&
-                  attn_smem<1, 1>() <= 232448,
-              "a CTA has 227 KB of shared memory");
+struct AttnSmem {  // stages, then the queries, the buffer where a row's warps meet, the rest
+  static constexpr int kRows = kAtWarps / WPR, kQ = kRows * 16 * kHeadDim * 2, kJoint = WPR > 1 ? 4 * 8192 : 0;
+  using Shared = AttnShared<kRows>;
+  static constexpr int kRest = kQ + kJoint + (int)sizeof(Shared) + 128;
+  static constexpr int kFit = (kAtSmem - kRest) / AttnStage<FMT>::kBytes;
+  static constexpr int kStages = kFit < kAtMaxStages ? kFit : kAtMaxStages;
+  static constexpr int kBytes = kStages * AttnStage<FMT>::kBytes + kRest;
+};
 
 // An item's request, KV head and rows; its request is without keys when
 // seq < 1, seq < q_len or its blocks exceed the table.
@@ -129,13 +143,19 @@ struct AttnItem {
   int r, h, row0, rows, seq, first;  // first: position of row row0
   __device__ int blocks_upto(int rows_) const { return seq > 0 ? (first + rows_ - 1) / 128 + 1 : 0; }
 };
-__device__ __forceinline__ AttnItem attn_item(const AttnParams &a, int it, bool *bad) {
+// its place, without the request's keys
+__device__ __forceinline__ AttnItem attn_place(const AttnParams &a, int it) {
   AttnItem x;
   x.h = it & (a.n_kv - 1);
   const int rg = it >> a.lg_kv;
   x.r = rg >> a.lg_groups;
   x.row0 = (rg - (x.r << a.lg_groups)) * a.rows_per;
   x.rows = min(a.rows_per, a.q_len - x.row0);
+  x.seq = x.first = 0;
+  return x;
+}
+__device__ __forceinline__ AttnItem attn_item(const AttnParams &a, int it, bool *bad) {
+  AttnItem x = attn_place(a, it);
   x.seq = __ldg(a.seq_lens + x.r);
   if (x.seq > 0 && (x.seq < a.q_len || (x.seq - 1) / 128 + 1 > a.bt_width)) {
     *bad = true;
@@ -177,15 +197,17 @@ template <int FMT, int WPR>
 __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_constant__ AttnMaps maps,
                                                                 const __grid_constant__ AttnParams a) {
   using St = AttnStage<FMT>;
-  constexpr int kStages = St::stages(WPR > 1);
+  using Sm = AttnSmem<FMT, WPR>;
+  static_assert(Sm::kBytes <= kAtSmem && Sm::kStages >= 3, "shared memory of a CTA");
+  constexpr int kStages = Sm::kStages;
   // a warp takes 32 keys at least: with eight warps a row, two groups of four
   // take alternate blocks
   constexpr int kParts = WPR > 4 ? 4 : WPR, kGroups = WPR / kParts, kKeys = 128 / kParts;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
-  float *joint = reinterpret_cast<float *>(ring + kStages * St::kBytes);  // [warp][16 heads][128], WPR > 1
-  AttnShared &sh = *reinterpret_cast<AttnShared *>(ring + kStages * St::kBytes +
-                                                   (WPR > 1 ? kAtWarps * 16 * kHeadDim * 4 : 0));
+  uint8_t *q_smem = ring + kStages * St::kBytes;  // [row][group][128], as q holds them
+  float2 *joint = reinterpret_cast<float2 *>(q_smem + Sm::kQ);  // [4 warps][32][lane]
+  typename Sm::Shared &sh = *reinterpret_cast<typename Sm::Shared *>(q_smem + Sm::kQ + Sm::kJoint);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   pdl_wait();  // queries, caches and lists come from the previous kernels
@@ -195,6 +217,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
       mbar_init(&sh.full[s], 1);
       mbar_init(&sh.empty[s], kAtWarps);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sh.batch_full[s], 1);
+      mbar_init(&sh.batch_empty[s], 1);
+    }
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_empty, kAtWarps);
     mbar_init(&sh.fin, kAtWarps);
     mbar_init(&sh.never, 1);
     fence_mbar_init();
@@ -261,15 +289,80 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
 
   if (warp >= kAtWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtProducerRegs));
-    if (warp > kAtWarps) return;
-    // -------------------------------------------------------------- producer
-    int j = 0;
+    if (warp > kAtWarps + 1) return;
+    if (warp == kAtWarps) {
+      // ------------------------------------------------------------ the copies
+      // one thread: an item's queries when its first batch comes, then a
+      // stage a block
+      if (lane != 0) return;
+      int j = 0, nq = 0;  // stages filled, items begun
+      bool ok = true;
+      auto acquire = [&]() {
+        return mbar_wait(&sh.empty[j % kStages], ((uint32_t)(j / kStages) & 1) ^ 1, a.status, a.lim);
+      };
+      int v0, v1, v, it = first_item;
+      for (int nbt = 0; ok && segment(it, v0, v1, v); ++nbt) {
+        const AttnBatch &bt = sh.batch[nbt & 1];
+        if (!(ok = mbar_wait(&sh.batch_full[nbt & 1], (uint32_t)(nbt >> 1) & 1, a.status, a.lim))) break;
+        const AttnItem x = attn_place(a, it);
+        if (bt.first) {
+          if (!(ok = mbar_wait(&sh.q_empty, (uint32_t)(nq & 1) ^ 1, a.status, a.lim))) break;
+          sh.q_item = make_int2(bt.first_pos, bt.seq);
+          const int es = a.q_is_fp8 ? 1 : 2, bytes = a.group * kHeadDim * es;
+          const uint8_t *src = a.q + (((int64_t)x.r * a.q_len + x.row0) * a.q_stride + x.h * a.group * kHeadDim) * es;
+          mbar_expect_tx(&sh.q_full, x.rows * bytes);
+          for (int i = 0; i < x.rows; ++i, src += a.q_stride * es) bulk_g2s(q_smem + i * bytes, src, bytes, &sh.q_full);
+          ++nq;
+        }
+        for (int k = 0; k < bt.n; ++k) {
+          const int64_t id = bt.blk[k];
+          if (id < 0) continue;
+          if (!(ok = acquire())) break;
+          const int s = j % kStages;
+          uint64_t *bar = &sh.full[s];
+          uint8_t *st = ring + s * St::kBytes;
+          sh.info[s] = bt.info[k];
+          mbar_expect_tx(bar, St::kBytes);
+          if constexpr (FMT == 0) {  // the block's 8 pages of the head: K, V, their scales
+            const int page = (int)(id * a.kps);
+            tma_pages(smem_u32(st), &maps.m[0], x.h, page, bar);
+            tma_pages(smem_u32(st + St::kKs), &maps.m[2], x.h, page, bar);
+            tma_pages(smem_u32(st + St::kV), &maps.m[1], x.h, page, bar);
+            tma_pages(smem_u32(st + St::kVs), &maps.m[3], x.h, page, bar);
+          } else if (a.bs <= 128) {  // the head's K and V slots of 128 / bs pages
+            tma_pages(smem_u32(st), &maps.m[0], 2 * x.h * max(a.bs >> 4, 1), (int)(id * (128 / a.bs)), bar);
+          } else {  // 128 tokens within a page: K codes, K scales, V codes, V scales
+            const int64_t page = id * 128 / a.bs;
+            const int t0 = (int)(id * 128 - page * a.bs);
+            const uint8_t *slot = a.kv_cache + page * a.kv_page_bytes + (int64_t)(2 * x.h) * a.bs * 72;
+            for (int v2 = 0; v2 < 2; ++v2, slot += a.bs * 72) {
+              bulk_g2s(st + v2 * 9216, slot + t0 * 64, 8192, bar);
+              bulk_g2s(st + v2 * 9216 + 8192, slot + a.bs * 64 + t0 * 8, 1024, bar);
+            }
+          }
+          ++j;
+        }
+        if (!ok) break;
+        if (bt.last) {
+          if (!(ok = acquire())) break;
+          sh.info[j % kStages] = make_int2(-1, 0);
+          mbar_arrive(&sh.full[j % kStages]);
+          ++j;
+          ++it;
+        }
+        mbar_arrive(&sh.batch_empty[nbt & 1]);
+      }
+      // the copies issued land before the CTA exits
+      for (int k = j - 1; k >= 0 && k >= j - kStages; --k)
+        mbar_wait(&sh.full[k % kStages], (uint32_t)(k / kStages) & 1, a.status, a.lim);
+      if (nq > 0) mbar_wait(&sh.q_full, (uint32_t)(nq - 1) & 1, a.status, a.lim);
+      return;
+    }
+    // -------------------------------------------------- what is to be copied
+    // a batch of up to 32 blocks ahead of the copies, so that the lists' and
+    // block table's latency (behind the copies already asked for) is hidden
     bool ok = true;
-    auto acquire = [&]() {  // stage j % kStages is free (lane 0's answer for the warp)
-      bool got = true;
-      if (lane == 0) got = mbar_wait(&sh.empty[j % kStages], ((uint32_t)(j / kStages) & 1) ^ 1, a.status, a.lim);
-      return __shfl_sync(0xffffffffu, got, 0) != 0;
-    };
+    int nbt = 0;
     int v0, v1, v;
     for (int it = first_item; ok && segment(it, v0, v1, v); ++it) {
       bool bad = false;
@@ -335,7 +428,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
         }
         __syncwarp();
       }
-      for (int base = u0; ok && base < u1; base += 32) {
+      for (int base = u0; ok && (base < u1 || base == u0); base += 32) {
         // 32 blocks at a time, one a lane: their ids and the rows they serve
         int b = -1, rows = 0;
         int64_t blk = -1;
@@ -351,51 +444,22 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
             set_status(a.status, kDevSlotRange);
           }
         }
-        const int m = min(32, u1 - base);
-        for (int k = 0; k < m; ++k) {
-          const int64_t id = __shfl_sync(0xffffffffu, blk, k);
-          const int bk = __shfl_sync(0xffffffffu, b, k), rk = __shfl_sync(0xffffffffu, rows, k);
-          if (id < 0) continue;
-          if (!(ok = acquire())) break;
-          const int s = j % kStages;
-          uint64_t *bar = &sh.full[s];
-          uint8_t *st = ring + s * St::kBytes;
-          if (lane == 0) {
-            sh.info[s] = make_int2(bk, rk);
-            mbar_expect_tx(bar, St::kBytes);
-          }
-          __syncwarp();
-          if constexpr (FMT == 0) {  // the block's 8 pages of the head: K, V, their scales
-            if (lane < 4) {
-              const int off = lane == 0 ? 0 : lane == 1 ? St::kV : lane == 2 ? St::kKs : St::kVs;
-              tma_pages(smem_u32(st + off), &maps.m[lane], x.h, (int)(id * a.kps), bar);
-            }
-          } else if (a.bs <= 128) {  // the head's K and V slots of 128 / bs pages
-            if (lane == 0)
-              tma_pages(smem_u32(st), &maps.m[0], 2 * x.h * max(a.bs >> 4, 1), (int)(id * (128 / a.bs)), bar);
-          } else if (lane < 4) {  // 128 tokens within a page: K codes, K scales, V codes, V scales
-            const int v2 = lane >> 1, sf = lane & 1;
-            const int64_t page = id * 128 / a.bs;
-            const int t0 = (int)(id * 128 - page * a.bs);
-            const uint8_t *base8 = a.kv_cache + page * a.kv_page_bytes + (int64_t)(2 * x.h + v2) * a.bs * 72;
-            bulk_g2s(st + v2 * 9216 + sf * 8192, base8 + (sf ? a.bs * 64 + t0 * 8 : t0 * 64), sf ? 1024 : 8192, bar);
-          }
-          ++j;
-        }
-      }
-      if (ok && (ok = acquire())) {  // the end of the segment
+        if (lane == 0) ok = mbar_wait(&sh.batch_empty[nbt & 1], ((uint32_t)(nbt >> 1) & 1) ^ 1, a.status, a.lim);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        AttnBatch &bt = sh.batch[nbt & 1];
+        bt.blk[lane] = blk < 0 ? -1 : (int)blk;
+        bt.info[lane] = make_int2(b, rows);
         if (lane == 0) {
-          sh.info[j % kStages] = make_int2(-1, 0);
-          mbar_arrive(&sh.full[j % kStages]);
+          bt.n = min(32, u1 - base);
+          bt.first_pos = x.first, bt.seq = x.seq;
+          bt.first = base == u0, bt.last = base + 32 >= u1;
         }
-        ++j;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.batch_full[nbt & 1]);
+        ++nbt;
       }
-      __syncwarp();
     }
-    // the copies issued land before the CTA exits
-    if (lane == 0)
-      for (int k = j - 1; k >= 0 && k >= j - kStages; --k)
-        mbar_wait(&sh.full[k % kStages], (uint32_t)(k / kStages) & 1, a.status, a.lim);
     return;
   }
 
@@ -405,7 +469,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
   const int key0 = part % kParts * kKeys;
   const int pt = min(a.bs, 128);  // NVFP4: tokens a piece of a stage
   int j = 0;
-  uint32_t fin_phase = 0;
+  uint32_t nq = 0, fin_phase = 0;
   auto fin_sync = [&]() {  // all compute warps; bounded
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.fin);
@@ -415,8 +479,13 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
   };
   int v0, v1, v;
   for (int it = first_item; segment(it, v0, v1, v); ++it) {
-    bool bad = false;
-    const AttnItem x = attn_item(a, it, &bad);
+    AttnItem x = attn_place(a, it);
+    {
+      const bool got = mbar_wait(&sh.q_full, nq & 1, a.status, a.lim);
+      if (!__all_sync(0xffffffffu, got)) return;
+      ++nq;
+    }
+    x.first = sh.q_item.x, x.seq = sh.q_item.y;
     const bool live = row < x.rows && x.seq > 0;
     const int p = x.first + row;
     // the row's queries as A fragments: heads g and g + 8, k-step ks holding
@@ -426,24 +495,23 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     float sc[2];  // score = product * sc (* the key's scale)
     {
       float qv[2][32];
-      const int64_t m = (int64_t)x.r * a.q_len + x.row0 + row;
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const int head = g + 8 * hh;
         const bool have = live && head < a.group;
-        const int64_t at = m * a.q_stride + (int64_t)(x.h * a.group + head) * kHeadDim;
+        const int at = (row * a.group + head) * kHeadDim;
         float top = 0.f;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
           const int d = FMT == 0 ? 16 * ks + 4 * t : 32 * t + 4 * ks;
           if (a.q_is_fp8) {
-            const uint32_t w = have ? __ldg(reinterpret_cast<const uint32_t *>(a.q + at + d)) : 0u;
+            const uint32_t w = have ? *reinterpret_cast<const uint32_t *>(q_smem + at + d) : 0u;
             const uint2 h2 = e4m3x4_f16(w);
             const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&h2.x));
             const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&h2.y));
             qv[hh][4 * ks] = f0.x, qv[hh][4 * ks + 1] = f0.y, qv[hh][4 * ks + 2] = f1.x, qv[hh][4 * ks + 3] = f1.y;
           } else {
-            const uint2 w = have ? __ldg(reinterpret_cast<const uint2 *>(a.q + 2 * (at + d))) : make_uint2(0u, 0u);
+            const uint2 w = have ? *reinterpret_cast<const uint2 *>(q_smem + 2 * (at + d)) : make_uint2(0u, 0u);
             qv[hh][4 * ks] = bf16_to_f32(w.x & 0xffffu), qv[hh][4 * ks + 1] = bf16_to_f32(w.x >> 16);
             qv[hh][4 * ks + 2] = bf16_to_f32(w.y & 0xffffu), qv[hh][4 * ks + 3] = bf16_to_f32(w.y >> 16);
           }
@@ -463,6 +531,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
           qf[ks][hh] = f16x2_bits(qv[hh][4 * ks], qv[hh][4 * ks + 1]);
           qf[ks][2 + hh] = f16x2_bits(qv[hh][4 * ks + 2], qv[hh][4 * ks + 3]);
         }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_empty);
     }
     float o[16][4];  // n8 tile n: FP8 dims 8 n + 2 t + e, NVFP4 dims 16 (2 t + e) + n; heads g (0, 1) and g + 8 (2, 3)
 #pragma unroll
@@ -470,6 +540,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
     float mref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float glimit[2] = {-INFINITY, -INFINITY};  // the reference moves when a lifted score is above
     int ev = -126;  // FP8: o is in units of 2^ev, V scales up to 2^(ev + 1) = vlimit
     float vlimit = pow2i(-125);
     while (true) {
@@ -495,10 +566,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
           uint32_t vsf[2];
           if constexpr (FMT == 0) {
             // a page is [8 chunks of 16 dims][16 tokens][16 bytes].  Column n
-            // of tile nt is key 4 (n / 2) + 2 (nt ^ n / 4) + n % 2: the eight
-            // rows of each 8x8 tile then sit in distinct banks
+            // of tile nt is key 4 (n / 2) + 2 nt + n % 2 (the rows of an 8x8
+            // tile meet in a bank two at a time; an order without that cost
+            // 16 selects a step and was slower)
             const int n = lane & 7, nt = (lane >> 3) & 1;
-            const int tok = 4 * (n >> 1) + 2 * (nt ^ (n >> 2)) + (n & 1);
+            const int tok = 4 * (n >> 1) + 2 * nt + (n & 1);
             const uint32_t at = smem_u32(st) + (k0 >> 4) * 2048 + (lane >> 4) * 256 + tok * 16;
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc) {
@@ -524,16 +596,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
 #pragma unroll
               for (int y = 0; y < 4; ++y) vraw[4 * q4 + y] = w[y];
             }
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const float lo = c[2 * y][2 * hh + e], hi = c[2 * y + 1][2 * hh + e];
-                  sv[hh][4 * y + e] = t < 2 ? lo : hi;
-                  sv[hh][4 * y + 2 + e] = t < 2 ? hi : lo;
-                }
           } else {
             // a token is 64 bytes of codes; thread t takes the 16 of dims
             // 32 t .. + 31 (two scale groups).  Column n of tile nt is key
@@ -573,30 +635,34 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
               const uint32_t f4 = *reinterpret_cast<const uint32_t *>(vp + pt * 64 + in * 8 + 4 * g);
               vsf[y] = __funnelshift_r(f4, f4, 8 * t);
             }
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  sv[hh][4 * y + e] = c[2 * y][2 * hh + e], sv[hh][4 * y + 2 + e] = c[2 * y + 1][2 * hh + e];
           }
-          // scale, mask
-          float vs[8];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float ks[4] = {1.f, 1.f, 1.f, 1.f};
-            if constexpr (FMT == 0) {
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                sv[hh][4 * y + e] = c[2 * y][2 * hh + e], sv[hh][4 * y + 2 + e] = c[2 * y + 1][2 * hh + e];
+          // x = score - reference (in log2 units, lifted by kAtLift): at most
+          // kAtLift + kAtSlack while the reference holds
+          f32x2 ksc[2][4], vs2[4];  // the score's factor of [head][pair of keys]; the pair's V scales
+          if constexpr (FMT == 0) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
               const float4 k4 = *reinterpret_cast<const float4 *>(st + St::kKs + (k0 + 16 * y + 4 * t) * 4);
               const float4 v4 = *reinterpret_cast<const float4 *>(st + St::kVs + (k0 + 16 * y + 4 * t) * 4);
-              ks[0] = k4.x, ks[1] = k4.y, ks[2] = k4.z, ks[3] = k4.w;
-              vs[4 * y] = v4.x, vs[4 * y + 1] = v4.y, vs[4 * y + 2] = v4.z, vs[4 * y + 3] = v4.w;
-            }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              sv[0][4 * y + e] *= FMT == 0 ? ks[e] * sc[0] : sc[0];
-              sv[1][4 * y + e] *= FMT == 0 ? ks[e] * sc[1] : sc[1];
+              for (int hh = 0; hh < 2; ++hh) {
+                ksc[hh][2 * y] = mul2(pack2(k4.x, k4.y), pack2(sc[hh], sc[hh]));
+                ksc[hh][2 * y + 1] = mul2(pack2(k4.z, k4.w), pack2(sc[hh], sc[hh]));
+              }
+              vs2[2 * y] = pack2(v4.x, v4.y), vs2[2 * y + 1] = pack2(v4.z, v4.w);
             }
+          } else {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) ksc[hh][k] = pack2(sc[hh], sc[hh]);
           }
           if (cut) {  // keys after the row's position: no score, no value (whatever the cache holds there)
 #pragma unroll
@@ -607,7 +673,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
                 if ((FMT == 0 ? e : (e + t) & 3) > left) {
                   sv[0][4 * y + e] = sv[1][4 * y + e] = -INFINITY;
                   if constexpr (FMT == 0) {
-                    vs[4 * y + e] = 0.f;
+                    auto put = [&](f32x2 &d, float x) {
+                      const float2 u = unpack2(d);
+                      d = e & 1 ? pack2(u.x, x) : pack2(x, u.y);
+                    };
+                    put(ksc[0][2 * y + (e >> 1)], 1.f), put(ksc[1][2 * y + (e >> 1)], 1.f);
+                    put(vs2[2 * y + (e >> 1)], 0.f);
 #pragma unroll
                     for (int n = 0; n < 16; ++n) vraw[16 * y + n] &= ~(0xffu << (8 * e));
                   } else {
@@ -617,17 +688,31 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
                 }
             }
           }
-          // the reference m (and the V unit) move only when a score (a V
-          // scale) has outgrown them
+          f32x2 x[2][4];
           float top[2], vtop = 0.f;
+          auto scores = [&]() {
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh)
-            top[hh] = fmaxf(fmaxf(fmaxf(sv[hh][0], sv[hh][1]), fmaxf(sv[hh][2], sv[hh][3])),
-                            fmaxf(fmaxf(sv[hh][4], sv[hh][5]), fmaxf(sv[hh][6], sv[hh][7])));
-          bool grow = top[0] > mref[0] + kAtSlack || top[1] > mref[1] + kAtSlack;
+            for (int hh = 0; hh < 2; ++hh) {
+              const float off = mref[hh] == -INFINITY ? 0.f : kAtLift - mref[hh];
+              top[hh] = -INFINITY;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                x[hh][k] = fma2(pack2(sv[hh][2 * k], sv[hh][2 * k + 1]), ksc[hh][k], pack2(off, off));
+                const float2 u = unpack2(x[hh][k]);
+                top[hh] = fmaxf(top[hh], fmaxf(u.x, u.y));
+              }
+            }
+          };
+          scores();
+          // the reference (and the V unit) move only when a score (a V scale)
+          // has outgrown them, or there is none yet
+          bool grow = top[0] > glimit[0] || top[1] > glimit[1];
           if constexpr (FMT == 0) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) vtop = fmaxf(vtop, fabsf(vs[e]));
+            for (int k = 0; k < 4; ++k) {
+              const float2 u = unpack2(vs2[k]);
+              vtop = fmaxf(vtop, fmaxf(fabsf(u.x), fabsf(u.y)));
+            }
             grow |= vtop > vlimit;
           }
           if (__any_sync(0xffffffffu, grow)) {
@@ -640,36 +725,33 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
             }
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              const float nm = fmaxf(mref[hh], quad_max(top[hh]));
-              const float al = nm == mref[hh] ? 1.f : ex2_approx(mref[hh] - nm);
+              const float was = mref[hh], tm = quad_max(top[hh]);  // the quad's largest score is tm, less the lift
+              const float now = was == -INFINITY ? tm : was + (tm - kAtLift);
+              const float nm = fmaxf(was, now);
+              const float al = nm == was ? 1.f : ex2_approx(was - nm);
               mref[hh] = nm;
+              glimit[hh] = nm == -INFINITY ? -INFINITY : kAtLift + kAtSlack;
               l[hh] *= al;
 #pragma unroll
               for (int n = 0; n < 16; ++n) o[n][2 * hh] *= al * f, o[n][2 * hh + 1] *= al * f;
             }
+            scores();
           }
           uint32_t pa[2][4];
-          {
-            float unit = 1.f;
-            if constexpr (FMT == 0) unit = pow2i(-ev);
-            float w[2][8];
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const float base = mref[hh] == -INFINITY ? 0.f : mref[hh] - kAtLift;
+          for (int hh = 0; hh < 2; ++hh) {
+            f32x2 sum = pack2(0.f, 0.f);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float x2 = ex2_approx(sv[hh][e] - base);
-                l[hh] += x2;
-                w[hh][e] = FMT == 0 ? x2 * (vs[e] * unit) : x2;
-              }
+            for (int k = 0; k < 4; ++k) {
+              const float2 u = unpack2(x[hh][k]);
+              f32x2 w = pack2(ex2_approx(u.x), ex2_approx(u.y));
+              sum = add2(sum, w);
+              if constexpr (FMT == 0) w = mul2(w, mul2(vs2[k], pack2(pow2i(-ev), pow2i(-ev))));
+              const float2 r = unpack2(w);
+              pa[k >> 1][(k & 1) * 2 + hh] = f16x2_bits(r.x, r.y);
             }
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              pa[y][0] = f16x2_bits(w[0][4 * y], w[0][4 * y + 1]);
-              pa[y][1] = f16x2_bits(w[1][4 * y], w[1][4 * y + 1]);
-              pa[y][2] = f16x2_bits(w[0][4 * y + 2], w[0][4 * y + 3]);
-              pa[y][3] = f16x2_bits(w[1][4 * y + 2], w[1][4 * y + 3]);
-            }
+            const float2 u = unpack2(sum);
+            l[hh] += u.x + u.y;
           }
           // o += weights . values
 #pragma unroll
@@ -729,113 +811,89 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     } else if (a.sliced && tid == 0) {
       a.shares[it] = make_int2(0, 0);
     }
-    const int64_t m = (int64_t)x.r * a.q_len + x.row0 + row;
-    if constexpr (WPR == 1) {
-      if (row < x.rows) {
+    if constexpr (WPR > 1) {
+      // a row's warps meet pairwise: the upper half of them hand o, m and l to
+      // the lower half through shared memory, until one is left
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int head = g + 8 * hh;
-          if (head >= a.group) continue;
-          if (whole) {
-            const float inv = l[hh] == 0.f ? 0.f : a.out_scale / l[hh];
-            __nv_bfloat16 *dst = a.out + m * a.out_stride + (int64_t)(x.h * a.group + head) * kHeadDim;
-            if constexpr (FMT == 0) {
+      for (int half = WPR / 2; half > 0; half /= 2) {
+        const int slot = row * half + (part & (half - 1));
+        float2 *box = joint + slot * 1024 + lane;
+        if (part >= half && part < 2 * half) {
 #pragma unroll
-              for (int n = 0; n < 16; ++n)
-                *reinterpret_cast<uint32_t *>(dst + 8 * n + 2 * t) = bf16x2_bits(o[n][2 * hh] * inv, o[n][2 * hh + 1] * inv);
-            } else {
+          for (int n = 0; n < 16; ++n)
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
+            for (int hh = 0; hh < 2; ++hh) box[(2 * n + hh) * 32] = make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
+          if (t == 0) sh.ml[slot][g] = make_float2(mref[0], l[0]), sh.ml[slot][g + 8] = make_float2(mref[1], l[1]);
+        }
+        if (!fin_sync()) return;
+        if (part < half) {
 #pragma unroll
-                for (int n = 0; n < 16; n += 8) {
-                  auto two = [&](int k) { return bf16x2_bits(o[k][2 * hh + e] * inv, o[k + 1][2 * hh + e] * inv); };
-                  *reinterpret_cast<uint4 *>(dst + 16 * (2 * t + e) + n) = make_uint4(two(n), two(n + 2), two(n + 4), two(n + 6));
-                }
+          for (int hh = 0; hh < 2; ++hh) {
+            const float2 ml = sh.ml[slot][g + 8 * hh];
+            const float top = fmaxf(mref[hh], ml.x);
+            const float f0 = mref[hh] == top ? 1.f : ex2_approx(mref[hh] - top);
+            const float f1 = ml.x == top ? 1.f : ex2_approx(ml.x - top);
+            mref[hh] = top;
+            l[hh] = f0 * l[hh] + f1 * ml.y;
+#pragma unroll
+            for (int n = 0; n < 16; ++n) {
+              const float2 y = box[(2 * n + hh) * 32];
+              o[n][2 * hh] = f0 * o[n][2 * hh] + f1 * y.x;
+              o[n][2 * hh + 1] = f0 * o[n][2 * hh + 1] + f1 * y.y;
             }
-          } else {
-            float *dst = pp + (row * 16 + head) * kHeadDim;
-            if constexpr (FMT == 0) {
-#pragma unroll
-              for (int n = 0; n < 16; ++n)
-                *reinterpret_cast<float2 *>(dst + 8 * n + 2 * t) = make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int n = 0; n < 16; n += 4)
-                  *reinterpret_cast<float4 *>(dst + 16 * (2 * t + e) + n) =
-                      make_float4(o[n][2 * hh + e], o[n + 1][2 * hh + e], o[n + 2][2 * hh + e], o[n + 3][2 * hh + e]);
-            }
-            if (t == 0)
-              *reinterpret_cast<float2 *>(pp + kAtMaxRows * 16 * kHeadDim + (row * 16 + head) * 2) =
-                  make_float2(mref[hh], l[hh]);
           }
         }
+        if (!fin_sync()) return;
       }
-    } else {
-      // the row's warps meet in shared memory: [warp][head][128], pairs of
-      // dims moved within the row so that a store's lanes hit distinct banks
-      auto place = [](int head, int d) {
-        return head * kHeadDim + (d ^ ((head & 3) << 3) ^ (FMT == 0 ? 0 : 2 * (d >> 5)));
-      };
-      float *mine = joint + warp * 16 * kHeadDim;
+    }
+    const int64_t m = (int64_t)x.r * a.q_len + x.row0 + row;
+    if (part == 0 && row < x.rows) {
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const int head = g + 8 * hh;
-        if constexpr (FMT == 0) {
+        if (head >= a.group) continue;
+        if (whole) {
+          const float inv = l[hh] == 0.f ? 0.f : a.out_scale / l[hh];
+          __nv_bfloat16 *dst = a.out + m * a.out_stride + (int64_t)(x.h * a.group + head) * kHeadDim;
+          if constexpr (FMT == 0) {
 #pragma unroll
-          for (int n = 0; n < 16; ++n)
-            *reinterpret_cast<float2 *>(mine + place(head, 8 * n + 2 * t)) = make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
+            for (int n = 0; n < 16; ++n)
+              *reinterpret_cast<uint32_t *>(dst + 8 * n + 2 * t) = bf16x2_bits(o[n][2 * hh] * inv, o[n][2 * hh + 1] * inv);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int n = 0; n < 16; n += 8) {
+                auto two = [&](int k) { return bf16x2_bits(o[k][2 * hh + e] * inv, o[k + 1][2 * hh + e] * inv); };
+                *reinterpret_cast<uint4 *>(dst + 16 * (2 * t + e) + n) = make_uint4(two(n), two(n + 2), two(n + 4), two(n + 6));
+              }
+          }
         } else {
+          float *dst = pp + (row * 16 + head) * kHeadDim;
+          if constexpr (FMT == 0) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
+            for (int n = 0; n < 16; ++n)
+              *reinterpret_cast<float2 *>(dst + 8 * n + 2 * t) = make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
+          } else {
 #pragma unroll
-            for (int n = 0; n < 16; n += 2)
-              *reinterpret_cast<float2 *>(mine + place(head, 16 * (2 * t + e) + n)) =
-                  make_float2(o[n][2 * hh + e], o[n + 1][2 * hh + e]);
-        }
-        if (t == 0) sh.ml[warp][head] = make_float2(mref[hh], l[hh]);
-      }
-      if (!fin_sync()) return;
-      if (row < x.rows) {
-        for (int head = part; head < a.group; head += WPR) {
-          float top = -INFINITY, sum = 0.f;
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int w = 0; w < WPR; ++w) top = fmaxf(top, sh.ml[row * WPR + w][head].x);
-          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // dims 2 lane, 64 + 2 lane
-#pragma unroll
-          for (int w = 0; w < WPR; ++w) {
-            const float2 ml = sh.ml[row * WPR + w][head];
-            const float f = ml.x == top ? 1.f : ex2_approx(ml.x - top);
-            sum += f * ml.y;
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const float2 y = *reinterpret_cast<const float2 *>(joint + (row * WPR + w) * 16 * kHeadDim +
-                                                                 place(head, 64 * z + 2 * lane));
-              if (f != 0.f) acc[z].x += f * y.x, acc[z].y += f * y.y;
-            }
+              for (int n = 0; n < 16; n += 4)
+                *reinterpret_cast<float4 *>(dst + 16 * (2 * t + e) + n) =
+                    make_float4(o[n][2 * hh + e], o[n + 1][2 * hh + e], o[n + 2][2 * hh + e], o[n + 3][2 * hh + e]);
           }
-          const float inv = sum == 0.f ? 0.f : a.out_scale / sum;
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            if (whole)
-              *reinterpret_cast<uint32_t *>(a.out + m * a.out_stride + (int64_t)(x.h * a.group + head) * kHeadDim + 64 * z +
-                                            2 * lane) = bf16x2_bits(acc[z].x * inv, acc[z].y * inv);
-            else
-              *reinterpret_cast<float2 *>(pp + (row * 16 + head) * kHeadDim + 64 * z + 2 * lane) = acc[z];
-          }
-          if (!whole && lane == 0)
-            *reinterpret_cast<float2 *>(pp + kAtMaxRows * 16 * kHeadDim + (row * 16 + head) * 2) = make_float2(top, sum);
+          if (t == 0)
+            *reinterpret_cast<float2 *>(pp + kAtMaxRows * 16 * kHeadDim + (row * 16 + head) * 2) =
+                make_float2(mref[hh], l[hh]);
         }
       }
-      if (!fin_sync()) return;  // `joint` is free for the next item
     }
   }
 }
 
 // Join the partial results of items that several CTAs share, in CTA order:
-// W warps a (item, row, head), each every W-th partial, 16 of them in flight
-// a lane (four dims); the W sums meet in shared memory.  The first CTA's
+// W warps a (item, row, head), each every W-th partial, several of them in
+// flight a lane (four dims); the W sums meet in shared memory.  The first CTA's
 // partial is its slot 1 (the item starts there), the others' their slot 0.
 constexpr int kJoinWarps = 8;
 template <int W>
@@ -856,7 +914,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) pa_attn_join_kernel(const __g
   const float *mls = a.part + (int64_t)2 * c0 * kAtPartFloats + kAtMaxRows * 16 * kHeadDim + (row * 16 + (have ? head : 0)) * 2;
   float top = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kIn = 16;
+  constexpr int kIn = W > 1 ? 16 : 4;
   const int n = c1 - c0 + 1;
   for (int k0 = warp % W; k0 < n; k0 += W * kIn) {
     float4 y[kIn];
@@ -927,10 +985,10 @@ static cudaError_t launch_attn(const AttnParams &a, int sms, bool pdl, cudaStrea
   if (!attn_maps(&maps, a, FMT)) return cudaErrorInvalidValue;
   using Kern = void (*)(const AttnMaps, const AttnParams);
   Kern kern = pa_attn_kernel<FMT, 1>;
-  int smem = attn_smem<FMT, 1>();
-  if (a.rows_per == 1) kern = pa_attn_kernel<FMT, 8>, smem = attn_smem<FMT, 8>();
-  else if (a.rows_per == 2) kern = pa_attn_kernel<FMT, 4>, smem = attn_smem<FMT, 4>();
-  else if (a.rows_per <= 4) kern = pa_attn_kernel<FMT, 2>, smem = attn_smem<FMT, 2>();
+  int smem = AttnSmem<FMT, 1>::kBytes;
+  if (a.rows_per == 1) kern = pa_attn_kernel<FMT, 8>, smem = AttnSmem<FMT, 8>::kBytes;
+  else if (a.rows_per == 2) kern = pa_attn_kernel<FMT, 4>, smem = AttnSmem<FMT, 4>::kBytes;
+  else if (a.rows_per <= 4) kern = pa_attn_kernel<FMT, 2>, smem = AttnSmem<FMT, 2>::kBytes;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), smem);
   if (e != cudaSuccess) return e;
   static int regs[4] = {0, 0, 0, 0};  // of the four kernels at launch
