@@ -6,8 +6,7 @@
 // 8 scale bytes a token, linear).
 //
 // A skinny contraction over a key stream that HBM bounds (72 bytes a key in,
-// 4 bytes a (row, key) out).  A warp takes a 128-key block, 32 keys at a
-// time, straight from global memory into fragments: lane (g, t) reads the 16
+// 4 bytes a (row, key) out).  A warp takes half a 128-key block, straight from global memory into fragments: lane (g, t) reads the 16
 // code bytes of dims 32 t .. + 31 of keys 4 g .. 4 g + 3, so a load
 // instruction covers whole 64-byte tokens and no byte passes through shared
 // memory.  Row g of tile 0 / row g + 8 of tile 0 / row g of tile 1 / row
@@ -27,7 +26,7 @@
 
 namespace pa {
 
-constexpr int kI4Warps = 8;
+constexpr int kI4Warps = 4;     // a CTA: half a 128-key block a warp
 constexpr int kI4MaxWidth = 16384;
 
 struct Index4Params {
@@ -46,13 +45,15 @@ struct Index4Params {
 };
 
 template <int NT>  // n8 tiles of query rows: q_len <= 8 * NT
-__global__ void __launch_bounds__(32 * kI4Warps) pa_index_scores_nvfp4_kernel(const __grid_constant__ Index4Params a) {
+__global__ void __launch_bounds__(32 * kI4Warps, NT == 1 ? 6 : 4) pa_index_scores_nvfp4_kernel(const __grid_constant__ Index4Params a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int r = blockIdx.y, b = blockIdx.x * kI4Warps + warp;
+  const int r = blockIdx.y, unit = blockIdx.x * kI4Warps + warp;
+  const int b = unit >> 1, half = unit & 1;  // the block's keys 64 half .. + 63
   pdl_wait();
   pdl_trigger();
   const int seq = __ldg(a.seq_lens + r);
+  const int64_t blk = b < a.bt_width ? __ldg(a.block_table + (int64_t)r * a.bt_width + b) : -1;
   if (seq < 1) return;
   const int nb_max = (seq - 1) / 128 + 1;
   if (seq < a.q_len || nb_max > a.bt_width) {
@@ -64,10 +65,25 @@ __global__ void __launch_bounds__(32 * kI4Warps) pa_index_scores_nvfp4_kernel(co
   // the rows that score the block: b < nb - local, nb = p / 128 + 1, and b >= init
   const bool scored_any = b >= a.init_blocks && b < (seq - 1) / 128 + 1 - a.local_blocks;
   if (scored_any) {
-    const int64_t blk = __ldg(a.block_table + (int64_t)r * a.bt_width + b);
     if (blk < 0 || (blk + 1) * 128 > a.idx_pages * a.bs) {
       if (lane == 0) set_status(a.status, kDevSlotRange);
     } else {
+      // the block's codes and scales, all on their way at once.  Its tokens
+      // are pieces of pt = min(block_size, 128), a page each, from token t0
+      const int pt = min(a.bs, 128), lg = 31 - __clz(pt);
+      const int64_t page0 = a.bs <= 128 ? blk << (7 - lg) : blk * 128 / a.bs;
+      const int t0 = a.bs <= 128 ? 0 : (int)(blk * 128 - page0 * a.bs);
+      uint4 kw[2][4];
+      uint32_t ksf[2][4];
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int off = 64 * half + 32 * z + 4 * g + u, tok = t0 + (off & (pt - 1));
+          const uint8_t *base = a.idx_cache + (page0 + (off >> lg)) * a.idx_page_bytes;
+          kw[z][u] = __ldg(reinterpret_cast<const uint4 *>(base + tok * 64 + 16 * t));
+          ksf[z][u] = __ldg(reinterpret_cast<const uint16_t *>(base + a.bs * 64 + tok * 8 + 2 * t));
+        }
       // query rows as B fragments: column g of tile nt is row 8 nt + g
       uint32_t qf[NT][8][2];
       float sc[NT][2];
@@ -95,17 +111,11 @@ __global__ void __launch_bounds__(32 * kI4Warps) pa_index_scores_nvfp4_kernel(co
 #pragma unroll
         for (int e = 0; e < 2; ++e) sc[nt][e] = a.index_scale * __shfl_sync(0xffffffffu, up, 4 * (2 * t + e));
       }
-      for (int k0 = 0; k0 < 128; k0 += 32) {
-        uint4 w[4];
-        uint32_t sf[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int64_t slot = blk * 128 + k0 + 4 * g + u, page = slot / a.bs;
-          const int tok = (int)(slot - page * a.bs);
-          const uint8_t *base = a.idx_cache + page * a.idx_page_bytes;
-          w[u] = __ldg(reinterpret_cast<const uint4 *>(base + tok * 64 + 16 * t));
-          sf[u] = __ldg(reinterpret_cast<const uint16_t *>(base + a.bs * 64 + tok * 8 + 2 * t));
-        }
+      for (int z = 0; z < 2; ++z) {
+        const int k0 = 64 * half + 32 * z;
+        const uint4 *w = kw[z];
+        const uint32_t *sf = ksf[z];
         float c[2][NT][4];
 #pragma unroll
         for (int x = 0; x < 2; ++x)
@@ -162,8 +172,8 @@ __global__ void __launch_bounds__(32 * kI4Warps) pa_index_scores_nvfp4_kernel(co
   for (int i = 0; i < a.q_len; ++i) {
     const int p = p0 + i;
     if (b > p / 128 || (b >= a.init_blocks && b < p / 128 + 1 - a.local_blocks)) continue;
-    *reinterpret_cast<float4 *>(a.scores + ((int64_t)r * a.q_len + i) * a.score_stride + b * 128 + 4 * lane) =
-        make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    *reinterpret_cast<float2 *>(a.scores + ((int64_t)r * a.q_len + i) * a.score_stride + b * 128 + 64 * half + 2 * lane) =
+        make_float2(-INFINITY, -INFINITY);
   }
 }
 
@@ -175,7 +185,7 @@ static cudaError_t launch_index4(const Index4Params &a, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  cfg.gridDim = dim3((a.bt_width + kI4Warps - 1) / kI4Warps, a.R);
+  cfg.gridDim = dim3((2 * a.bt_width + kI4Warps - 1) / kI4Warps, a.R);
   cfg.blockDim = dim3(32 * kI4Warps);
   return a.q_len <= 8 ? cudaLaunchKernelEx(&cfg, pa_index_scores_nvfp4_kernel<1>, a)
                       : cudaLaunchKernelEx(&cfg, pa_index_scores_nvfp4_kernel<2>, a);

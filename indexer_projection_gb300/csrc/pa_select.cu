@@ -6,9 +6,10 @@
 // small calls).  A cluster of CTAs takes one (row, head), each CTA a run of
 // its blocks; a block's maximum becomes a 32-bit key whose unsigned order is
 // the scores' (0: not selectable, all ones: pinned) in the first CTA's shared
-// memory.  That CTA finds the topk-th key by radix selection (8 bits a pass)
-// and writes the blocks above it, and the first of those equal to it, in
-// block order.
+// memory.  That CTA finds the last key to be taken by radix selection (8 bits
+// a pass from the highest bit in which the keys differ, until a digit is
+// taken whole) and writes the blocks above it, and the first of those equal
+// to it, in block order.
 #include <cstdint>
 
 #include "../../include/pre_attn.h"
@@ -41,8 +42,9 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 
 __global__ void __launch_bounds__(kSelThreads) pa_select_kernel(const __grid_constant__ SelectParams a) {
   extern __shared__ uint32_t keys[];  // [bt_width], of the cluster's first CTA
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t pick[2];        // the digit found, what remains to take in it
+  __shared__ uint32_t hist[2][256];
+  __shared__ int3 pick;               // the digit found, what remains to take in it, what it holds
+  __shared__ uint4 warp_range[kSelThreads / 32];
   __shared__ int warp_sum[2][kSelThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t ctas, rank;
@@ -60,74 +62,139 @@ __global__ void __launch_bounds__(kSelThreads) pa_select_kernel(const __grid_con
   const float *row = a.scores + (int64_t)h * a.head_stride + (int64_t)m * a.score_stride;
   const uint32_t keys0 = mapa(smem_u32(keys), 0);
   cluster_wait();
-  const int b1 = (int)((int64_t)nb * (rank + 1) / ctas);
-  for (int b = (int)((int64_t)nb * rank / ctas) + warp; b < b1; b += kSelThreads / 32) {
-    const bool pinned = b < a.init_blocks || b >= nb - a.local_blocks;
-    uint32_t key = 0xffffffffu;
-    if (!pinned) {
-      const float4 v = __ldg(reinterpret_cast<const float4 *>(row + b * 128) + lane);
-      float x = fmaxf(fmaxf(fmaxf(-INFINITY, v.x), fmaxf(-INFINITY, v.y)), fmaxf(fmaxf(-INFINITY, v.z), fmaxf(-INFINITY, v.w)));
+  // eight lanes a block, four blocks a warp: each lane has four 16-byte loads
+  // of its block in flight, twice (blocks b and b + 32)
+  const int b0 = (int)((int64_t)nb * rank / ctas), b1 = (int)((int64_t)nb * (rank + 1) / ctas);
+  const int sub = lane & 7;
+  constexpr int kStep = kSelThreads / 8;
+  for (int b = b0 + (tid >> 3); b < b1 + (tid >> 3); b += 2 * kStep) {  // the same number of turns for a warp's lanes
+    float4 v[2][4];
+    bool read[2];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-      key = score_key(x);
+    for (int u = 0; u < 2; ++u) {
+      const int bu = b + u * kStep;
+      read[u] = bu < b1 && bu >= a.init_blocks && bu < nb - a.local_blocks;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[u][k] = read[u] ? __ldg(reinterpret_cast<const float4 *>(row + bu * 128) + 8 * k + sub)
+                          : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     }
-    if (lane == 0) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(keys0 + 4 * b), "r"(key) : "memory");
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int bu = b + u * kStep;
+      float x = -INFINITY;  // fmaxf leaves NaN out
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x = fmaxf(fmaxf(fmaxf(x, v[u][k].x), fmaxf(v[u][k].y, v[u][k].z)), v[u][k].w);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+      if (sub == 0 && bu < b1)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(keys0 + 4 * bu), "r"(read[u] ? score_key(x) : 0xffffffffu)
+                     : "memory");
+    }
   }
   cluster_sync();
   if (rank != 0) return;
-  // the topk-th largest key: T, of whose holders `need` are taken
-  uint32_t T = 0, need = (uint32_t)a.topk;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    hist[tid] = 0;
-    __syncthreads();
-    for (int b = tid; b < nb; b += kSelThreads)
-      if (shift == 24 || (keys[b] >> (shift + 8)) == (T >> (shift + 8))) atomicAdd(&hist[(keys[b] >> shift) & 255u], 1u);
-    __syncthreads();
-    if (warp == 0) {
-      // digits from the top: lane l holds 255 - 8 l .. 248 - 8 l
-      uint32_t c[8], sum = 0;
+  // what is to be found: of the keys that are neither pinned nor 0, the
+  // `need` largest; how many there are, and their range
+  int pins = 0;
+  uint32_t most = 0, least = 0xffffffffu;
+  int some = 0;
+  for (int b = tid; b < nb; b += kSelThreads) {
+    const uint32_t k = keys[b];
+    if (k == 0xffffffffu) ++pins;
+    else if (k != 0) ++some, most = max(most, k), least = min(least, k);
+  }
+  pins = __reduce_add_sync(0xffffffffu, pins), some = __reduce_add_sync(0xffffffffu, some);
+  most = __reduce_max_sync(0xffffffffu, most), least = __reduce_min_sync(0xffffffffu, least);
+  if (lane == 0) warp_range[warp] = make_uint4(pins, some, most, least);
+  hist[0][tid] = 0;
+  __syncthreads();
+  pins = some = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum += c[k] = hist[255 - 8 * lane - k];
-      uint32_t incl = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+  for (int w = 0; w < kSelThreads / 32; ++w) {
+    const uint4 r4 = warp_range[w];
+    pins += r4.x, some += r4.y, most = max(most, r4.z), least = min(least, r4.w);
+  }
+  // the need-th largest key: radix selection from the highest bit in which
+  // they differ, 8 bits a pass, until a digit's keys are all taken.  In the
+  // end a block is taken if its key is above T, or is T and among the first
+  // `need` such
+  int need = a.topk - pins;
+  uint32_t T = 0;
+  if (need <= 0) T = 0xfffffffeu, need = 0;
+  else if (some <= need) need = 0;
+  else {
+    int left = 32 - __clz(most ^ least);  // bits not settled yet
+    T = left < 32 ? most >> left << left : 0u;
+    for (int pass = 0; left > 0; ++pass) {
+      const int bits = min(left, 8), shift = left - bits;
+      uint32_t *h0 = hist[pass & 1];
+      for (int b = tid; b < nb; b += kSelThreads) {
+        const uint32_t k = keys[b];
+        if (k != 0 && k != 0xffffffffu && (left == 32 || ((k ^ T) >> left) == 0))
+          atomicAdd(&h0[(k >> shift) & ((1u << bits) - 1u)], 1u);
       }
-      uint32_t before = incl - sum;
-      if (lane == 31 && incl < need) pick[0] = 0, pick[1] = hist[0];  // fewer blocks than topk: all of them
+      __syncthreads();
+      if (warp == 0) {  // digits from the top: lane l holds 255 - 8 l .. 248 - 8 l
+        int c[8], sum = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (before < need && before + c[k] >= need) pick[0] = 255 - 8 * lane - k, pick[1] = need - before;
-        before += c[k];
+        for (int k = 0; k < 8; ++k) sum += c[k] = (int)h0[255 - 8 * lane - k];
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        int before = incl - sum;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (before < need && before + c[k] >= need) pick = make_int3(255 - 8 * lane - k, need - before, c[k]);
+          before += c[k];
+        }
+      } else if (tid >= 32) {
+        for (int k = tid - 32; k < 256; k += kSelThreads - 32) hist[(pass + 1) & 1][k] = 0;
+      }
+      __syncthreads();
+      T |= (uint32_t)pick.x << shift;
+      need = pick.y;
+      left = shift;
+      if (pick.y == pick.z) {  // the whole digit
+        T -= 1, need = 0;
+        break;
       }
     }
-    __syncthreads();
-    T |= pick[0] << shift;
-    need = pick[1];
-    __syncthreads();
   }
-  // blocks above T, and the first `need` equal to it (none where T is 0: not selectable)
-  if (T == 0) need = 0;
   int32_t *out = a.blocks + (int64_t)item * a.topk;
   int taken = 0, equal = 0;  // before this chunk
-  for (int b0 = 0; b0 < nb; b0 += kSelThreads) {
-    const int b = b0 + tid;
+  for (int c0 = 0; c0 < nb; c0 += kSelThreads) {
+    const int b = c0 + tid;
     const uint32_t key = b < nb ? keys[b] : 0u;
-    const uint32_t eq = __ballot_sync(0xffffffffu, key == T && key != 0u);
-    if (lane == 0) warp_sum[0][warp] = __popc(eq);
-    __syncthreads();
-    int e = equal + __popc(eq & ((1u << lane) - 1u));
-    for (int w = 0; w < warp; ++w) e += warp_sum[0][w];
-    for (int w = 0; w < kSelThreads / 32; ++w) equal += warp_sum[0][w];
-    const bool take = key > T || (key == T && key != 0u && e < (int)need);
+    bool take = key > T;
+    if (need > 0) {  // the same for the CTA
+      const uint32_t eq = __ballot_sync(0xffffffffu, key == T);
+      if (lane == 0) warp_sum[0][warp] = __popc(eq);
+      __syncthreads();
+      int e = equal + __popc(eq & ((1u << lane) - 1u));
+#pragma unroll
+      for (int w = 0; w < kSelThreads / 32; ++w) {
+        const int v = warp_sum[0][w];
+        if (w < warp) e += v;
+        equal += v;
+      }
+      take |= key == T && e < need;
+    }
     const uint32_t tk = __ballot_sync(0xffffffffu, take);
     if (lane == 0) warp_sum[1][warp] = __popc(tk);
     __syncthreads();
     int at = taken + __popc(tk & ((1u << lane) - 1u));
-    for (int w = 0; w < warp; ++w) at += warp_sum[1][w];
-    for (int w = 0; w < kSelThreads / 32; ++w) taken += warp_sum[1][w];
+#pragma unroll
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+      const int v = warp_sum[1][w];
+      if (w < warp) at += v;
+      taken += v;
+    }
     if (take) out[at] = b;
+    if (c0 + kSelThreads < nb) __syncthreads();
   }
   for (int k = taken + tid; k < a.topk; k += kSelThreads) out[k] = -1;
   if (tid == 0) a.counts[item] = taken;

@@ -89,8 +89,9 @@ class CacheReader:
     ``caches`` is PreAttn.fp8_caches(...) or PreAttn.nvfp4_caches(...): the
     fields that a call reads have to be set (the index cache for
     ``index_scores``, the K / V ones for ``attend``) and their tensors kept
-    alive by the caller.  Owns a workspace and a status word; calls of one
-    reader are ordered by their stream, or by the caller.  Every tensor is on
+    alive by the caller.  Owns a workspace, a status word and the calls'
+    argument structs: one host thread uses a reader at a time, and its calls
+    are ordered on the GPU by their stream, or by the caller.  Every tensor is on
     ``device``; seq_lens, block tables, block lists and counts are contiguous
     int32, scores and query rows have contiguous columns.
     """
@@ -115,15 +116,29 @@ class CacheReader:
         self.workspace = torch.empty(256 + self.ws_bytes, dtype=torch.uint8, device=self.device)
         B.pre_attn_workspace_init(self.workspace, 256, torch.cuda.current_stream(self.device))
         self.status = self.workspace.data_ptr()
+        # the calls' argument structs, of which a call sets what changes
         self._attn = B.pa_attention_args(None, None, 1.0, 0, n_q_heads, n_kv_heads, cache_format, block_size,
-                                         kv_page_stride, B.ctypes.pointer(caches), None, None, None, None, 0, 0, q_len,
+                                         kv_page_stride, B.ctypes.pointer(caches), None, None, None, None, topk, 0, q_len,
                                          bt_width, sm_scale, None, 0, self.status + 256, self.ws_bytes, self.status,
                                          flags)
+        self._select = B.pa_select_args(None, 0, 0, 0, None, 0, q_len, bt_width, init_blocks, local_blocks, topk, None,
+                                        None, self.status)
+        if cache_format == B.PA_CACHE_FP8:
+            self._scores = B.pa_index_args(None, 0, 0, caches.index_cache, caches.num_index_slots, None, None, 0, q_len,
+                                           bt_width, init_blocks, local_blocks, 0.0, None, 0, self.status, 0)
+            self._run_scores = B.pre_attn_index_scores
+        else:
+            self._scores = B.pa_index_nvfp4_args(None, 0, 0, caches.idx_cache, caches.idx_pages, caches.idx_page_bytes,
+                                                 block_size, None, None, 0, q_len, bt_width, init_blocks, local_blocks, 0.0,
+                                                 None, 0, self.status)
+            self._run_scores = B.pre_attn_index_scores_nvfp4
 
-    def _stream(self, stream):
-        if torch.cuda.current_device() != self.device.index:
+    def _on(self, stream):
+        """The stream of a call: the reader's device has to be the current one."""
+        index = self.device.index
+        if torch.cuda.current_device() != index:
             raise ValueError(f"the current device is not the reader's ({self.device})")
-        return torch.cuda.current_stream(self.device) if stream is None else stream
+        return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream
 
     def _requests(self, seq_lens, block_table=None) -> int:
         R = seq_lens.shape[0]
@@ -135,73 +150,68 @@ class CacheReader:
         return R
 
     def _ints(self, x, shape, name):
-        if x.dtype is not torch.int32 or tuple(x.shape) != shape or not x.is_contiguous():
+        if x.dtype is not torch.int32 or x.shape != shape or not x.is_contiguous():
             raise ValueError(f"{name}: a contiguous int32 tensor of shape {shape} is wanted")
 
-    def _rows(self, x, dtypes, rows, cols, name):
-        if x.dtype not in dtypes or x.dim() != 2 or x.shape[0] != rows or x.shape[1] < cols or x.stride(1) != 1:
-            raise ValueError(f"{name}: [{rows}, >= {cols}] of {dtypes} with contiguous columns is wanted")
-        return x.stride(0) if rows > 1 else cols  # elements a row (a single row's stride says nothing)
+    def _rows(self, x, dtype_ok, rows, cols, name):
+        shape, stride = x.shape, x.stride()
+        if not dtype_ok or len(shape) != 2 or shape[0] != rows or shape[1] < cols or stride[1] != 1:
+            raise ValueError(f"{name}: [{rows}, >= {cols}] with contiguous columns is wanted, not {x.dtype} {tuple(shape)}")
+        return stride[0] if rows > 1 else cols  # elements a row (a single row's stride says nothing)
 
     def index_scores(self, iq, head: int, block_table, seq_lens, scores, *, scale: float | None = None, stream=None,
                      check: bool = True) -> int:
         """Scores of index_q head ``head`` (iq [M, >= (head + 1) * 128] bf16) into scores [M, >= bt_width * 128] f32."""
         R = self._requests(seq_lens, block_table)
-        iq_stride = self._rows(iq, (torch.bfloat16,), R * self.q_len, (head + 1) * 128, "iq")
-        score_stride = self._rows(scores, (torch.float32,), R * self.q_len, self.bt_width * 128, "scores")
-        c, scale = self.caches, self.index_scale if scale is None else scale
-        if self.cache_format == B.PA_CACHE_FP8:
-            a = B.pa_index_args(iq.data_ptr(), iq_stride, head, c.index_cache, c.num_index_slots,
-                                block_table.data_ptr(), seq_lens.data_ptr(), R, self.q_len, self.bt_width,
-                                self.init_blocks, self.local_blocks, scale, scores.data_ptr(), score_stride,
-                                self.status, 0)
-            return B.pre_attn_index_scores(a, self._stream(stream), check)
-        a = B.pa_index_nvfp4_args(iq.data_ptr(), iq_stride, head, c.idx_cache, c.idx_pages, c.idx_page_bytes,
-                                  self.block_size, block_table.data_ptr(), seq_lens.data_ptr(), R, self.q_len,
-                                  self.bt_width, self.init_blocks, self.local_blocks, scale, scores.data_ptr(),
-                                  score_stride, self.status)
-        return B.pre_attn_index_scores_nvfp4(a, self._stream(stream), check)
+        M, a = R * self.q_len, self._scores
+        a.iq_stride = self._rows(iq, iq.dtype is torch.bfloat16, M, (head + 1) * 128, "iq")
+        a.score_stride = self._rows(scores, scores.dtype is torch.float32, M, self.bt_width * 128, "scores")
+        a.iq, a.head, a.block_table, a.seq_lens = iq.data_ptr(), head, block_table.data_ptr(), seq_lens.data_ptr()
+        a.R, a.scores = R, scores.data_ptr()
+        a.index_scale = self.index_scale if scale is None else scale
+        return self._run_scores(a, self._on(stream), check)
 
     def select_blocks(self, scores, seq_lens, blocks, counts, *, stream=None, check: bool = True) -> int:
         """The blocks of each row and head from scores [heads, M, >= bt_width * 128] into blocks [M, heads, topk]."""
         R = self._requests(seq_lens)
-        M, heads = R * self.q_len, scores.shape[0]
-        if (scores.dtype is not torch.float32 or scores.dim() != 3 or scores.shape[1] != M
-                or heads < 1 or scores.shape[2] < self.bt_width * 128 or scores.stride(2) != 1):
-            raise ValueError(f"scores: f32 [heads, {M}, >= {self.bt_width * 128}] with contiguous columns is wanted")
+        M, shape, stride, a = R * self.q_len, scores.shape, scores.stride(), self._select
+        width = self.bt_width * 128
+        if (scores.dtype is not torch.float32 or len(shape) != 3 or shape[0] < 1 or shape[1] != M or shape[2] < width
+                or stride[2] != 1):
+            raise ValueError(f"scores: f32 [heads, {M}, >= {width}] with contiguous columns is wanted")
+        heads = shape[0]
         self._ints(blocks, (M, heads, self.topk), "blocks")
         self._ints(counts, (M, heads), "counts")
-        stride = scores.stride(1) if M > 1 else self.bt_width * 128
-        a = B.pa_select_args(scores.data_ptr(), stride, scores.stride(0) if heads > 1 else M * stride, heads,
-                             seq_lens.data_ptr(), R, self.q_len, self.bt_width, self.init_blocks, self.local_blocks, self.topk,
-                             blocks.data_ptr(), counts.data_ptr(), self.status)
-        return B.pre_attn_select_blocks(a, self._stream(stream), check)
+        a.score_stride = stride[1] if M > 1 else width
+        a.score_head_stride = stride[0] if heads > 1 else M * a.score_stride
+        a.scores, a.n_heads, a.seq_lens, a.R = scores.data_ptr(), heads, seq_lens.data_ptr(), R
+        a.blocks, a.counts = blocks.data_ptr(), counts.data_ptr()
+        return B.pre_attn_select_blocks(a, self._on(stream), check)
 
     def attend(self, q, block_table, seq_lens, out, *, blocks=None, counts=None, q_fp8_scale: float = 1.0, stream=None,
                check: bool = True) -> int:
         """Attention of q [M, >= n_q_heads * 128] (bf16, or E4M3 with q_fp8_scale) into out (bf16, as wide): over the
         blocks of each row and KV head (blocks [M, n_kv_heads, topk], counts [M, n_kv_heads]), or all without."""
         R = self._requests(seq_lens, block_table)
-        M = R * self.q_len
-        q_stride = self._rows(q, (torch.bfloat16, torch.float8_e4m3fn), M, self.n_q_heads * 128, "q")
-        out_stride = self._rows(out, (torch.bfloat16,), M, self.n_q_heads * 128, "out")
-        a = self._attn
-        if q.dtype is torch.bfloat16:
+        M, a, cols = R * self.q_len, self._attn, self.n_q_heads * 128
+        half = q.dtype is torch.bfloat16
+        a.q_stride = self._rows(q, half or q.dtype is torch.float8_e4m3fn, M, cols, "q")
+        a.out_stride = self._rows(out, out.dtype is torch.bfloat16, M, cols, "out")
+        if half:
             a.q, a.q_fp8 = q.data_ptr(), None
         else:
             a.q, a.q_fp8, a.q_fp8_scale = None, q.data_ptr(), q_fp8_scale
-        a.q_stride, a.out, a.out_stride, a.R = q_stride, out.data_ptr(), out_stride, R
-        a.block_table, a.seq_lens = block_table.data_ptr(), seq_lens.data_ptr()
+        a.out, a.R, a.block_table, a.seq_lens = out.data_ptr(), R, block_table.data_ptr(), seq_lens.data_ptr()
         if blocks is None:
             a.blocks = a.counts = None
         else:
-            self._ints(blocks, (M, self.n_kv_heads, self.topk), "blocks")
             if counts is None:
                 raise ValueError("blocks come with their counts")
+            self._ints(blocks, (M, self.n_kv_heads, self.topk), "blocks")
             self._ints(counts, (M, self.n_kv_heads), "counts")
-            a.blocks, a.counts, a.topk = blocks.data_ptr(), counts.data_ptr(), self.topk
-        return B.pre_attn_attention(a, self._stream(stream), check)
+            a.blocks, a.counts = blocks.data_ptr(), counts.data_ptr()
+        return B.pre_attn_attention(a, self._on(stream), check)
 
     def device_status(self, stream=None) -> int:
         """PA_DEV_* bits of the calls since the last reading (read and cleared; synchronises)."""
-        return B.pre_attn_device_status(self.workspace, self._stream(stream))
+        return B.pre_attn_device_status(self.workspace, self._on(stream))
