@@ -28,6 +28,7 @@
 // the V scale over a power of two near the largest V scale so far, so it
 // stays in f16's normal range for keys whose weight is up to 2^-23 of the
 // largest.  The sum of the weights is taken in f32 before that rounding.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -53,7 +54,15 @@ constexpr int kAtMaxWidth = 16384;                 // block-table width
 constexpr int kAtMaxTopk = 256;
 constexpr float kAtLift = 9.0f;   // weights are 2^9 exp2(s - m)
 constexpr float kAtSlack = 4.0f;  // m follows the maximum once that is 2^4 above it
+constexpr int kAtMaxSplit = 8;    // CTAs a cluster
+constexpr int kAtClusterBlocks = 8;  // blocks a CTA of a cluster takes at most
 constexpr int kAtPartFloats = kAtMaxRows * 16 * (kHeadDim + 2);  // o, then (m, l), of one partial
+
+// How the items meet the CTAs: a CTA an item; even slices of all items'
+// blocks over a persistent grid, with partial results joined by a second
+// kernel; or a cluster of CTAs an item, joined through distributed shared
+// memory (small calls: no scan of the items, no second kernel).
+enum { kAtWhole = 0, kAtSliced = 1, kAtCluster = 2 };
 
 struct AttnParams {
   const uint8_t *q;
@@ -71,7 +80,8 @@ struct AttnParams {
   int R, q_len, bt_width, n_kv, group;
   int lg_kv, lg_groups;              // log2 of n_kv and of the items a (request, KV head) has
   int rows_per;                      // rows an item (the last of a request may have fewer)
-  int items, sliced;
+  int items, mode;                   // kAtWhole, kAtSliced, kAtCluster
+  int split;                         // kAtCluster: CTAs an item
   float score_scale, out_scale;
   __nv_bfloat16 *out;
   int64_t out_stride;
@@ -137,6 +147,17 @@ struct AttnSmem {  // stages, then the queries, the buffer where a row's warps m
   static constexpr int kBytes = kStages * AttnStage<FMT>::kBytes + kRest;
 };
 
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+
 // An item's request, KV head and rows; its request is without keys when
 // seq < 1, seq < q_len or its blocks exceed the table.
 struct AttnItem {
@@ -185,6 +206,40 @@ struct AttnSlice {
   int lo, hi, total, cta, ctas;
 };
 
+// Every CTA of a cluster joins a share of its item's (row, head)s from all
+// CTAs' partial results, in CTA order: a warp each, four dims a lane.
+__device__ __forceinline__ void cluster_join(const AttnParams &a, const AttnItem &x, const float *own, int rank, int warp,
+                                             int lane) {
+  const int pairs = x.rows * a.group;
+  for (int k = rank + a.split * warp; k < pairs; k += a.split * kAtWarps) {
+    const int i = k / a.group, head = k - i * a.group, at = i * 16 + head;
+    const uint32_t ml_at = smem_u32(own + kAtMaxRows * 16 * kHeadDim + 2 * at);
+    const uint32_t o_at = smem_u32(own + at * kHeadDim + 4 * lane);
+    float2 ml[kAtMaxSplit];
+    float4 y[kAtMaxSplit];
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < kAtMaxSplit; ++c)
+      if (c < a.split) {
+        ml[c] = ld_cluster_f2(mapa(ml_at, c));
+        y[c] = ld_cluster_f4(mapa(o_at, c));
+        top = fmaxf(top, ml[c].x);
+      }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < kAtMaxSplit; ++c)
+      if (c < a.split) {
+        const float f = ml[c].x == top ? 1.f : ex2_approx(ml[c].x - top);
+        sum += f * ml[c].y;
+        acc.x += f * y[c].x, acc.y += f * y[c].y, acc.z += f * y[c].z, acc.w += f * y[c].w;
+      }
+    const float inv = sum == 0.f ? 0.f : a.out_scale / sum;
+    const int64_t mi = (int64_t)x.r * a.q_len + x.row0 + i;
+    *reinterpret_cast<uint2 *>(a.out + mi * a.out_stride + (int64_t)(x.h * a.group + head) * kHeadDim + 4 * lane) =
+        make_uint2(bf16x2_bits(acc.x * inv, acc.y * inv), bf16x2_bits(acc.z * inv, acc.w * inv));
+  }
+}
+
 __device__ __forceinline__ void tma_pages(uint32_t dst, const CUtensorMap *map, int row, int page, uint64_t *bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
@@ -193,7 +248,7 @@ __device__ __forceinline__ void tma_pages(uint32_t dst, const CUtensorMap *map, 
       : "memory");
 }
 
-template <int FMT, int WPR>
+template <int FMT, int WPR, bool CLUSTER>  // CLUSTER: mode kAtCluster
 __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_constant__ AttnMaps maps,
                                                                 const __grid_constant__ AttnParams a) {
   using St = AttnStage<FMT>;
@@ -230,7 +285,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
   AttnSlice sl;
   sl.cta = blockIdx.x;
   int first_item = blockIdx.x;
-  if (a.sliced) {
+  const int mode = CLUSTER ? (int)kAtCluster : a.mode;
+  if (mode == kAtSliced) {
     // the running sums of the items' units, 256 items a round
     int before = 0;
     bool bad = false;
@@ -267,17 +323,18 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     first_item = 0;
     for (int step = kAtMaxItems / 2; step > 0; step >>= 1)
       if (first_item + step < a.items && sh.offs[first_item + step] <= sl.lo) first_item += step;
-  } else {
-    sl.total = sl.ctas = 0;
-    sl.lo = 0;
-    sl.hi = 1;
+  } else {  // part lo of `total` of one item
+    sl.total = CLUSTER ? a.split : 1;
+    sl.ctas = 0;
+    sl.lo = CLUSTER ? (int)cta_rank() : 0;
+    sl.hi = sl.lo + 1;
+    if (CLUSTER) first_item = blockIdx.x / a.split;
     __syncthreads();
   }
   // segment k of the slice: its item's units v0 .. v1 of v
   auto segment = [&](int it, int &v0, int &v1, int &v) {
-    if (!a.sliced) {
-      v0 = 0;
-      v1 = v = 1;
+    if (mode != kAtSliced) {
+      v0 = sl.lo, v1 = sl.hi, v = sl.total;
       return it == first_item;
     }
     if (it >= a.items || sh.offs[it] >= sl.hi) return false;
@@ -367,12 +424,34 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     for (int it = first_item; ok && segment(it, v0, v1, v); ++it) {
       bool bad = false;
       const AttnItem x = attn_item(a, it, &bad);
-      if (!a.sliced && bad && lane == 0) set_status(a.status, kDevSlotRange);
+      if (mode != kAtSliced && bad && lane == 0) set_status(a.status, kDevSlotRange);
       const int nb = x.blocks_upto(x.rows);
       int u0 = 0, u1 = 0;  // the segment's blocks (of the union list, or of the request)
       if (a.topk == 0) {
         u0 = (int)((int64_t)nb * v0 / v);
         u1 = (int)((int64_t)nb * v1 / v);
+      } else if (x.rows == 1 && a.topk <= 32) {
+        // one short list, an entry a lane: its distinct blocks in list order
+        if (nb > 0) {
+          const int64_t at = ((int64_t)x.r * a.q_len + x.row0) * a.n_kv + x.h;
+          const int count = __ldg(a.counts + at);
+          int b = lane < a.topk ? __ldg(a.blocks + at * a.topk + lane) : -1;
+          const bool given = lane < min(count, a.topk);
+          const bool fits = given && b >= 0 && b < nb;
+          if (__any_sync(0xffffffffu, given && !fits) && lane == 0) set_status(a.status, kDevSlotRange);
+          if (!fits) b = -1 - lane;
+          const uint32_t same = __match_any_sync(0xffffffffu, b);
+          const uint32_t kept = __ballot_sync(0xffffffffu, fits && (same & ((1u << lane) - 1u)) == 0);
+          const int total = __popc(kept), pos = __popc(kept & ((1u << lane) - 1u));
+          u0 = total * v0 / v;
+          u1 = total * v1 / v;
+          __syncwarp();
+          if (((kept >> lane) & 1u) && pos >= u0 && pos < u1) {
+            sh.list[pos - u0] = (uint16_t)b;
+            sh.bits[0][b >> 5] = 0xffffffffu;  // (the batches ask it for the rows)
+          }
+          __syncwarp();
+        }
       } else if (nb > 0) {
         // the rows' lists as bit sets over the request's blocks, then the
         // union's blocks u0 .. u1 in ascending order
@@ -801,14 +880,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     }
     const bool whole = v0 == 0 && v1 == v;
     float *pp = nullptr;  // the segment's partial result: [row][head][128], then (m, l)
-    if (!whole) {
+    if (!whole && mode == kAtSliced) {
       const bool head_seg = v0 > 0;  // the item began in an earlier CTA
       pp = a.part + (int64_t)(2 * sl.cta + (head_seg ? 0 : 1)) * kAtPartFloats;
       if (!head_seg && tid == 0) {
         const int last = sh.offs[it + 1] - 1;
         a.shares[it] = make_int2(sl.cta, (int)((((int64_t)last + 1) * sl.ctas - 1) / sl.total));
       }
-    } else if (a.sliced && tid == 0) {
+    } else if (mode == kAtSliced && tid == 0) {
       a.shares[it] = make_int2(0, 0);
     }
     if constexpr (WPR > 1) {
@@ -847,12 +926,18 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
       }
     }
     const int64_t m = (int64_t)x.r * a.q_len + x.row0 + row;
+    float *own = reinterpret_cast<float *>(ring);  // kAtCluster: [row][head][128], then (m, l); the stages are free
+    if constexpr (CLUSTER) {
+      if constexpr (WPR == 1)
+        if (!fin_sync()) return;  // (with more warps a row they have met above)
+      pp = own;
+    }
     if (part == 0 && row < x.rows) {
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const int head = g + 8 * hh;
         if (head >= a.group) continue;
-        if (whole) {
+        if (!CLUSTER && whole) {
           const float inv = l[hh] == 0.f ? 0.f : a.out_scale / l[hh];
           __nv_bfloat16 *dst = a.out + m * a.out_stride + (int64_t)(x.h * a.group + head) * kHeadDim;
           if constexpr (FMT == 0) {
@@ -887,6 +972,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
                 make_float2(mref[hh], l[hh]);
         }
       }
+    }
+    if constexpr (CLUSTER) {
+      cluster_sync();
+      cluster_join(a, x, own, sl.lo, warp, lane);
+      cluster_sync();  // nobody leaves while its shared memory is read
     }
   }
 }
@@ -980,39 +1070,73 @@ static bool attn_maps(AttnMaps *maps, const AttnParams &a, int fmt) {
 }
 
 template <int FMT>
-static cudaError_t launch_attn(const AttnParams &a, int sms, bool pdl, cudaStream_t stream) {
+static cudaError_t launch_attn(const AttnParams &a0, int sms, bool pdl, cudaStream_t stream) {
   AttnMaps maps;
-  if (!attn_maps(&maps, a, FMT)) return cudaErrorInvalidValue;
+  if (!attn_maps(&maps, a0, FMT)) return cudaErrorInvalidValue;
+  AttnParams a = a0;
   using Kern = void (*)(const AttnMaps, const AttnParams);
-  Kern kern = pa_attn_kernel<FMT, 1>;
+  Kern kern = pa_attn_kernel<FMT, 1, false>, clustered = pa_attn_kernel<FMT, 1, true>;
   int smem = AttnSmem<FMT, 1>::kBytes;
-  if (a.rows_per == 1) kern = pa_attn_kernel<FMT, 8>, smem = AttnSmem<FMT, 8>::kBytes;
-  else if (a.rows_per == 2) kern = pa_attn_kernel<FMT, 4>, smem = AttnSmem<FMT, 4>::kBytes;
-  else if (a.rows_per <= 4) kern = pa_attn_kernel<FMT, 2>, smem = AttnSmem<FMT, 2>::kBytes;
+  if (a.rows_per == 1) kern = pa_attn_kernel<FMT, 8, false>, clustered = pa_attn_kernel<FMT, 8, true>, smem = AttnSmem<FMT, 8>::kBytes;
+  else if (a.rows_per == 2) kern = pa_attn_kernel<FMT, 4, false>, clustered = pa_attn_kernel<FMT, 4, true>, smem = AttnSmem<FMT, 4>::kBytes;
+  else if (a.rows_per <= 4) kern = pa_attn_kernel<FMT, 2, false>, clustered = pa_attn_kernel<FMT, 2, true>, smem = AttnSmem<FMT, 2>::kBytes;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), smem);
+  if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void *>(clustered), smem);
   if (e != cudaSuccess) return e;
+  const int variant = a.rows_per == 1 ? 0 : a.rows_per == 2 ? 1 : a.rows_per <= 4 ? 2 : 3;
   static int regs[4] = {0, 0, 0, 0};  // of the four kernels at launch
-  int &held = regs[a.rows_per == 1 ? 0 : a.rows_per == 2 ? 1 : a.rows_per <= 4 ? 2 : 3];
-  if (held == 0) {
-    cudaFuncAttributes at;
+  if (regs[variant] == 0) {
+    cudaFuncAttributes at, ac;
     e = cudaFuncGetAttributes(&at, reinterpret_cast<const void *>(kern));
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&ac, reinterpret_cast<const void *>(clustered));
     if (e != cudaSuccess) return e;
-    held = at.numRegs;
+    regs[variant] = std::min(at.numRegs, ac.numRegs);
   }
-  if (held * kAtThreads < 32 * kAtWarps * kAtComputeRegs + (kAtThreads - 32 * kAtWarps) * kAtProducerRegs)
+  if (regs[variant] * kAtThreads < 32 * kAtWarps * kAtComputeRegs + (kAtThreads - 32 * kAtWarps) * kAtProducerRegs)
     return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  cfg.gridDim = dim3(a.sliced ? sms : a.items);
+  cfg.gridDim = dim3(a.mode == kAtSliced ? sms : a.items);
   cfg.blockDim = dim3(kAtThreads);
   cfg.dynamicSmemBytes = smem;
+  if (a.mode == kAtSliced) {
+    // a cluster an item where all of them are resident at once and a CTA's
+    // share of an item is short: then the scan and the second kernel cost
+    // more than even slices save
+    const int longest = a.topk ? std::min(a.bt_width, a.topk * a.rows_per) : a.bt_width;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    static int resident[4][64][kAtMaxSplit + 1];  // clusters of a size, by device; -1: none
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    for (int n = std::min(kAtMaxSplit, longest); n >= 2 && dev < 64; --n) {
+      if (a.items * n > sms || (longest + n - 1) / n > kAtClusterBlocks) continue;
+      int &held = resident[variant][dev][n];
+      attr[1].val.clusterDim.x = n;
+      if (held == 0) {
+        cfg.gridDim = dim3(n);
+        cfg.numAttrs = 2;
+        int k = 0;
+        held = cudaOccupancyMaxActiveClusters(&k, clustered, &cfg) == cudaSuccess && k > 0 ? k : -1;
+      }
+      if (held >= a.items) {
+        a.mode = kAtCluster;
+        a.split = n;
+        cfg.gridDim = dim3(a.items * n);
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, clustered, maps, a);
+      }
+    }
+    cfg.gridDim = dim3(sms);
+    cfg.numAttrs = 1;
+  }
   e = cudaLaunchKernelEx(&cfg, kern, maps, a);
-  if (e != cudaSuccess || !a.sliced || a.test_timeout) return e;
+  if (e != cudaSuccess || a.mode != kAtSliced || a.test_timeout) return e;
   // few items: many partials each, a CTA a head; else a warp a head
   const bool many = a.items * 8 <= sms;
   cfg.gridDim = dim3(a.items * a.rows_per, many ? a.group : (a.group + kJoinWarps - 1) / kJoinWarps);
@@ -1111,7 +1235,7 @@ extern "C" int pre_attn_attention(const pa_attention_args *in, void *stream) {
   a.lg_groups = x.q_len > pa::kAtMaxRows ? 1 : 0;
   a.rows_per = (x.q_len + a.lg_groups) >> a.lg_groups;
   a.items = x.R * x.n_kv_heads << a.lg_groups;
-  a.sliced = a.items <= pa::kAtMaxItems;
+  a.mode = a.items <= pa::kAtMaxItems ? pa::kAtSliced : pa::kAtWhole;
   a.score_scale = (float)((double)x.sm_scale * 1.4426950408889634 * (x.q ? 1.0 : (double)x.q_fp8_scale) *
                           (fp8 ? 1.0 : (double)c.k_global_scale));
   a.out_scale = fp8 ? 1.0f : c.v_global_scale;
