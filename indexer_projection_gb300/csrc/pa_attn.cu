@@ -32,111 +32,25 @@
 #include <cmath>
 #include <cstdint>
 
-#include <cuda_fp16.h>
-
 #include "../../include/pre_attn.h"
-#include "pa_device.cuh"
-#include "pa_f16.cuh"
-#include "pa_launch.h"
-#include "pa_tma.h"
+#include "pa_attn.cuh"
+#include "pa_attn_tc.h"
 
 namespace pa {
 
-constexpr int kAtWarps = 8;                        // compute warps
 constexpr int kAtThreads = 32 * (kAtWarps + 4);    // and the producer's warpgroup (one warp of it works)
 // Registers a thread after the split (setmaxnreg): the compute warps hold o,
 // the queries and the codes of 32 keys.  Their sum must not exceed what the
 // CTA was launched with, which launch_attn checks.
 constexpr int kAtComputeRegs = 200, kAtProducerRegs = 96;
-constexpr int kAtMaxRows = 8;                      // query rows an item
-constexpr int kAtMaxItems = 2048;                  // items the sliced grid lists in shared memory
-constexpr int kAtMaxWidth = 16384;                 // block-table width
-constexpr int kAtMaxTopk = 256;
-constexpr float kAtLift = 9.0f;   // weights are 2^9 exp2(s - m)
-constexpr float kAtSlack = 4.0f;  // m follows the maximum once that is 2^4 above it
-constexpr int kAtMaxSplit = 8;    // CTAs a cluster
-constexpr int kAtClusterBlocks = 8;  // blocks a CTA of a cluster takes at most
-constexpr int kAtPartFloats = kAtMaxRows * 16 * (kHeadDim + 2);  // o, then (m, l), of one partial
 
-// How the items meet the CTAs: a CTA an item; even slices of all items'
-// blocks over a persistent grid, with partial results joined by a second
-// kernel; or a cluster of CTAs an item, joined through distributed shared
-// memory (small calls: no scan of the items, no second kernel).
-enum { kAtWhole = 0, kAtSliced = 1, kAtCluster = 2 };
-
-struct AttnParams {
-  const uint8_t *q;
-  int q_is_fp8;
-  int64_t q_stride;
-  const uint8_t *k_cache, *v_cache;  // FP8
-  const float *k_scale, *v_scale;
-  int64_t num_pages16;
-  int kps;
-  const uint8_t *kv_cache;           // NVFP4
-  int64_t kv_pages, kv_page_bytes;
-  int bs;
-  const int32_t *block_table, *seq_lens, *blocks, *counts;
-  int topk;                          // 0: every block
-  int R, q_len, bt_width, n_kv, group;
-  int lg_kv, lg_groups;              // log2 of n_kv and of the items a (request, KV head) has
-  int rows_per;                      // rows an item (the last of a request may have fewer)
-  int items, mode;                   // kAtWhole, kAtSliced, kAtCluster
-  int split;                         // kAtCluster: CTAs an item
-  float score_scale, out_scale;
-  __nv_bfloat16 *out;
-  int64_t out_stride;
-  float *part;                       // [2 * grid][kAtPartFloats]
-  int2 *shares;                      // [items] first and last CTA of an item
-  uint32_t *status;
-  uint64_t lim;
-  int test_timeout;
-};
-
-// Tensor maps of a block's copies: FP8 K pages, V pages, K scales, V scales;
-// NVFP4 a KV head's K and V slots (pages of up to 128 tokens).
-struct AttnMaps {
-  CUtensorMap m[4];
-};
-
-template <int FMT>
-struct AttnStage;
-template <>
-struct AttnStage<0> {  // K and V pages as they are (8 of 2048 bytes each), then the scales of 128 tokens
-  static constexpr int kV = 16384, kKs = 32768, kVs = 33280, kBytes = 33792;
-};
-template <>
-struct AttnStage<1> {  // pieces of pt = min(block_size, 128) tokens: K codes (64 bytes a token), K scales (8), V codes,
-                       // V scales, as the page holds them
-  static constexpr int kBytes = 18432;
-};
-constexpr int kAtMaxStages = 10;
-
-// 32 blocks of a segment, resolved ahead of their copies.
-struct AttnBatch {
-  int blk[32];   // ids in the cache (-1: none)
-  int2 info[32]; // block of the request, rows that attend it
-  int n, seq, first_pos;
-  int first, last;  // of the segment
-};
-
-template <int ROWS>  // rows of an item at most
-struct AttnShared {
-  uint64_t full[kAtMaxStages], empty[kAtMaxStages];
-  uint64_t batch_full[2], batch_empty[2];
-  uint64_t q_full, q_empty;  // an item's queries; read into registers at once
-  uint64_t fin;              // the compute warps among themselves
-  uint64_t never;            // testing: nothing arrives on it
-  int2 info[kAtMaxStages];   // a stage's block (-1: the end of a segment), rows that attend it
-  int2 q_item;               // first row's position, keys
-  int scan[kAtWarps];
-  AttnBatch batch[2];
+template <int ROWS>
+struct AttnShared : AttnRing<ROWS> {
+  uint64_t fin;    // the compute warps among themselves
+  uint64_t never;  // testing: nothing arrives on it
   float2 ml[kAtWarps / 2][16];
-  int offs[kAtMaxItems + 8];
-  uint16_t list[ROWS * kAtMaxTopk];
-  uint32_t bits[ROWS][kAtMaxWidth / 32];
 };
 
-constexpr int kAtSmem = 232448;  // 227 KB a CTA
 template <int FMT, int WPR>
 struct AttnSmem {  // stages, then the queries, the buffer where a row's warps meet, the rest
   static constexpr int kRows = kAtWarps / WPR, kQ = kRows * 16 * kHeadDim * 2, kJoint = WPR > 1 ? 4 * 8192 : 0;
@@ -158,57 +72,9 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
   return v;
 }
 
-// An item's request, KV head and rows; its request is without keys when
-// seq < 1, seq < q_len or its blocks exceed the table.
-struct AttnItem {
-  int r, h, row0, rows, seq, first;  // first: position of row row0
-  __device__ int blocks_upto(int rows_) const { return seq > 0 ? (first + rows_ - 1) / 128 + 1 : 0; }
-};
-// its place, without the request's keys
-__device__ __forceinline__ AttnItem attn_place(const AttnParams &a, int it) {
-  AttnItem x;
-  x.h = it & (a.n_kv - 1);
-  const int rg = it >> a.lg_kv;
-  x.r = rg >> a.lg_groups;
-  x.row0 = (rg - (x.r << a.lg_groups)) * a.rows_per;
-  x.rows = min(a.rows_per, a.q_len - x.row0);
-  x.seq = x.first = 0;
-  return x;
-}
-__device__ __forceinline__ AttnItem attn_item(const AttnParams &a, int it, bool *bad) {
-  AttnItem x = attn_place(a, it);
-  x.seq = __ldg(a.seq_lens + x.r);
-  if (x.seq > 0 && (x.seq < a.q_len || (x.seq - 1) / 128 + 1 > a.bt_width)) {
-    *bad = true;
-    x.seq = 0;
-  }
-  if (x.seq < 0) x.seq = 0;
-  x.first = x.seq - a.q_len + x.row0;
-  return x;
-}
-// The share of the grid's work that an item stands for (at least one unit):
-// its blocks, or the length of its rows' lists (whose union the producer
-// scales to it).
-__device__ __forceinline__ int attn_units(const AttnParams &a, int it, bool *bad) {
-  const AttnItem x = attn_item(a, it, bad);
-  if (x.seq == 0) return 1;
-  if (a.topk == 0) return x.blocks_upto(x.rows);
-  int n = 0;
-  const int32_t *c = a.counts + ((int64_t)x.r * a.q_len + x.row0) * a.n_kv + x.h;
-#pragma unroll
-  for (int i = 0; i < kAtMaxRows; ++i)
-    if (i < x.rows) n += min(max(__ldg(c + i * a.n_kv), 0), a.topk);
-  return max(n, 1);
-}
-
-// The CTA's slice as segments: item it, units v0 .. v1 of its v.
-struct AttnSlice {
-  int lo, hi, total, cta, ctas;
-};
-
 // Every CTA of a cluster joins a share of its item's (row, head)s from all
 // CTAs' partial results, in CTA order: a warp each, four dims a lane.
-__device__ __forceinline__ void cluster_join(const AttnParams &a, const AttnItem &x, const float *own, int rank, int warp,
+__device__ __forceinline__ void cluster_join(const CacheAttnParams &a, const AttnItem &x, const float *own, int rank, int warp,
                                              int lane) {
   const int pairs = x.rows * a.group;
   for (int k = rank + a.split * warp; k < pairs; k += a.split * kAtWarps) {
@@ -240,17 +106,9 @@ __device__ __forceinline__ void cluster_join(const AttnParams &a, const AttnItem
   }
 }
 
-__device__ __forceinline__ void tma_pages(uint32_t dst, const CUtensorMap *map, int row, int page, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-      "[%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(page), "r"(smem_u32(bar))
-      : "memory");
-}
-
 template <int FMT, int WPR, bool CLUSTER>  // CLUSTER: mode kAtCluster
 __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_constant__ AttnMaps maps,
-                                                                const __grid_constant__ AttnParams a) {
+                                                                const __grid_constant__ CacheAttnParams a) {
   using St = AttnStage<FMT>;
   using Sm = AttnSmem<FMT, WPR>;
   static_assert(Sm::kBytes <= kAtSmem && Sm::kStages >= 3, "shared memory of a CTA");
@@ -282,263 +140,13 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     mbar_init(&sh.never, 1);
     fence_mbar_init();
   }
-  AttnSlice sl;
-  sl.cta = blockIdx.x;
-  int first_item = blockIdx.x;
   const int mode = CLUSTER ? (int)kAtCluster : a.mode;
-  if (mode == kAtSliced) {
-    // the running sums of the items' units, 256 items a round
-    int before = 0;
-    bool bad = false;
-    for (int i0 = 0; i0 < a.items; i0 += 32 * kAtWarps) {
-      const int it = i0 + tid;
-      const int n = warp < kAtWarps && it < a.items ? attn_units(a, it, &bad) : 0;
-      int incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (warp < kAtWarps && lane == 31) sh.scan[warp] = incl;
-      __syncthreads();
-      int round = 0, mine = before + incl - n;
-#pragma unroll
-      for (int w = 0; w < kAtWarps; ++w) {
-        const int v = sh.scan[w];
-        if (w < warp) mine += v;
-        round += v;
-      }
-      if (warp < kAtWarps) sh.offs[it] = mine;
-      before += round;
-      __syncthreads();
-    }
-    if (tid == 0) sh.offs[a.items] = before;
-    if (blockIdx.x == 0 && bad) set_status(a.status, kDevSlotRange);
-    __syncthreads();
-    sl.total = sh.offs[a.items];
-    sl.ctas = min((int)gridDim.x, sl.total);
-    if (sl.cta >= sl.ctas) return;
-    sl.lo = (int)((int64_t)sl.total * sl.cta / sl.ctas);
-    sl.hi = (int)((int64_t)sl.total * (sl.cta + 1) / sl.ctas);
-    first_item = 0;
-    for (int step = kAtMaxItems / 2; step > 0; step >>= 1)
-      if (first_item + step < a.items && sh.offs[first_item + step] <= sl.lo) first_item += step;
-  } else {  // part lo of `total` of one item
-    sl.total = CLUSTER ? a.split : 1;
-    sl.ctas = 0;
-    sl.lo = CLUSTER ? (int)cta_rank() : 0;
-    sl.hi = sl.lo + 1;
-    if (CLUSTER) first_item = blockIdx.x / a.split;
-    __syncthreads();
-  }
-  // segment k of the slice: its item's units v0 .. v1 of v
-  auto segment = [&](int it, int &v0, int &v1, int &v) {
-    if (mode != kAtSliced) {
-      v0 = sl.lo, v1 = sl.hi, v = sl.total;
-      return it == first_item;
-    }
-    if (it >= a.items || sh.offs[it] >= sl.hi) return false;
-    v0 = max(sl.lo, sh.offs[it]) - sh.offs[it];
-    v1 = min(sl.hi, sh.offs[it + 1]) - sh.offs[it];
-    v = sh.offs[it + 1] - sh.offs[it];
-    return true;
-  };
-
+  const AttnSlice sl = attn_slice<kAtWarps>(a, sh, mode);
+  if (sl.none) return;
   if (warp >= kAtWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtProducerRegs));
-    if (warp > kAtWarps + 1) return;
-    if (warp == kAtWarps) {
-      // ------------------------------------------------------------ the copies
-      // one thread: an item's queries when its first batch comes, then a
-      // stage a block
-      if (lane != 0) return;
-      int j = 0, nq = 0;  // stages filled, items begun
-      bool ok = true;
-      auto acquire = [&]() {
-        return mbar_wait(&sh.empty[j % kStages], ((uint32_t)(j / kStages) & 1) ^ 1, a.status, a.lim);
-      };
-      int v0, v1, v, it = first_item;
-      for (int nbt = 0; ok && segment(it, v0, v1, v); ++nbt) {
-        const AttnBatch &bt = sh.batch[nbt & 1];
-        if (!(ok = mbar_wait(&sh.batch_full[nbt & 1], (uint32_t)(nbt >> 1) & 1, a.status, a.lim))) break;
-        const AttnItem x = attn_place(a, it);
-        if (bt.first) {
-          if (!(ok = mbar_wait(&sh.q_empty, (uint32_t)(nq & 1) ^ 1, a.status, a.lim))) break;
-          sh.q_item = make_int2(bt.first_pos, bt.seq);
-          const int es = a.q_is_fp8 ? 1 : 2, bytes = a.group * kHeadDim * es;
-          const uint8_t *src = a.q + (((int64_t)x.r * a.q_len + x.row0) * a.q_stride + x.h * a.group * kHeadDim) * es;
-          mbar_expect_tx(&sh.q_full, x.rows * bytes);
-          for (int i = 0; i < x.rows; ++i, src += a.q_stride * es) bulk_g2s(q_smem + i * bytes, src, bytes, &sh.q_full);
-          ++nq;
-        }
-        for (int k = 0; k < bt.n; ++k) {
-          const int64_t id = bt.blk[k];
-          if (id < 0) continue;
-          if (!(ok = acquire())) break;
-          const int s = j % kStages;
-          uint64_t *bar = &sh.full[s];
-          uint8_t *st = ring + s * St::kBytes;
-          sh.info[s] = bt.info[k];
-          mbar_expect_tx(bar, St::kBytes);
-          if constexpr (FMT == 0) {  // the block's 8 pages of the head: K, V, their scales
-            const int page = (int)(id * a.kps);
-            tma_pages(smem_u32(st), &maps.m[0], x.h, page, bar);
-            tma_pages(smem_u32(st + St::kKs), &maps.m[2], x.h, page, bar);
-            tma_pages(smem_u32(st + St::kV), &maps.m[1], x.h, page, bar);
-            tma_pages(smem_u32(st + St::kVs), &maps.m[3], x.h, page, bar);
-          } else if (a.bs <= 128) {  // the head's K and V slots of 128 / bs pages
-            tma_pages(smem_u32(st), &maps.m[0], 2 * x.h * max(a.bs >> 4, 1), (int)(id * (128 / a.bs)), bar);
-          } else {  // 128 tokens within a page: K codes, K scales, V codes, V scales
-            const int64_t page = id * 128 / a.bs;
-            const int t0 = (int)(id * 128 - page * a.bs);
-            const uint8_t *slot = a.kv_cache + page * a.kv_page_bytes + (int64_t)(2 * x.h) * a.bs * 72;
-            for (int v2 = 0; v2 < 2; ++v2, slot += a.bs * 72) {
-              bulk_g2s(st + v2 * 9216, slot + t0 * 64, 8192, bar);
-              bulk_g2s(st + v2 * 9216 + 8192, slot + a.bs * 64 + t0 * 8, 1024, bar);
-            }
-          }
-          ++j;
-        }
-        if (!ok) break;
-        if (bt.last) {
-          if (!(ok = acquire())) break;
-          sh.info[j % kStages] = make_int2(-1, 0);
-          mbar_arrive(&sh.full[j % kStages]);
-          ++j;
-          ++it;
-        }
-        mbar_arrive(&sh.batch_empty[nbt & 1]);
-      }
-      // the copies issued land before the CTA exits
-      for (int k = j - 1; k >= 0 && k >= j - kStages; --k)
-        mbar_wait(&sh.full[k % kStages], (uint32_t)(k / kStages) & 1, a.status, a.lim);
-      if (nq > 0) mbar_wait(&sh.q_full, (uint32_t)(nq - 1) & 1, a.status, a.lim);
-      return;
-    }
-    // -------------------------------------------------- what is to be copied
-    // a batch of up to 32 blocks ahead of the copies, so that the lists' and
-    // block table's latency (behind the copies already asked for) is hidden
-    bool ok = true;
-    int nbt = 0;
-    int v0, v1, v;
-    for (int it = first_item; ok && segment(it, v0, v1, v); ++it) {
-      bool bad = false;
-      const AttnItem x = attn_item(a, it, &bad);
-      if (mode != kAtSliced && bad && lane == 0) set_status(a.status, kDevSlotRange);
-      const int nb = x.blocks_upto(x.rows);
-      int u0 = 0, u1 = 0;  // the segment's blocks (of the union list, or of the request)
-      if (a.topk == 0) {
-        u0 = (int)((int64_t)nb * v0 / v);
-        u1 = (int)((int64_t)nb * v1 / v);
-      } else if (x.rows == 1 && a.topk <= 32) {
-        // one short list, an entry a lane: its distinct blocks in list order
-        if (nb > 0) {
-          const int64_t at = ((int64_t)x.r * a.q_len + x.row0) * a.n_kv + x.h;
-          const int count = __ldg(a.counts + at);
-          int b = lane < a.topk ? __ldg(a.blocks + at * a.topk + lane) : -1;
-          const bool given = lane < min(count, a.topk);
-          const bool fits = given && b >= 0 && b < nb;
-          if (__any_sync(0xffffffffu, given && !fits) && lane == 0) set_status(a.status, kDevSlotRange);
-          if (!fits) b = -1 - lane;
-          const uint32_t same = __match_any_sync(0xffffffffu, b);
-          const uint32_t kept = __ballot_sync(0xffffffffu, fits && (same & ((1u << lane) - 1u)) == 0);
-          const int total = __popc(kept), pos = __popc(kept & ((1u << lane) - 1u));
-          u0 = total * v0 / v;
-          u1 = total * v1 / v;
-          __syncwarp();
-          if (((kept >> lane) & 1u) && pos >= u0 && pos < u1) {
-            sh.list[pos - u0] = (uint16_t)b;
-            sh.bits[0][b >> 5] = 0xffffffffu;  // (the batches ask it for the rows)
-          }
-          __syncwarp();
-        }
-      } else if (nb > 0) {
-        // the rows' lists as bit sets over the request's blocks, then the
-        // union's blocks u0 .. u1 in ascending order
-        const int words = (nb + 31) / 32;
-        __syncwarp();
-        for (int i = 0; i < x.rows; ++i)
-          for (int w = lane; w < words; w += 32) sh.bits[i][w] = 0;
-        const int64_t at = ((int64_t)x.r * a.q_len + x.row0) * a.n_kv + x.h;
-        int count[kAtMaxRows];
-#pragma unroll
-        for (int i = 0; i < kAtMaxRows; ++i) count[i] = i < x.rows ? __ldg(a.counts + at + i * a.n_kv) : 0;
-        bool out_of_range = false;
-        for (int e0 = 0; e0 < a.topk; e0 += 32) {
-          int b[kAtMaxRows];
-          const bool in = e0 + lane < a.topk;
-#pragma unroll
-          for (int i = 0; i < kAtMaxRows; ++i)
-            b[i] = in && i < x.rows ? __ldg(a.blocks + (at + i * a.n_kv) * a.topk + e0 + lane) : 0;
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < kAtMaxRows; ++i)
-            if (in && e0 + lane < count[i]) {
-              if (b[i] < 0 || b[i] > (x.first + i) / 128) out_of_range = true;
-              else atomicOr(&sh.bits[i][b[i] >> 5], 1u << (b[i] & 31));
-            }
-        }
-        if (__any_sync(0xffffffffu, out_of_range) && lane == 0) set_status(a.status, kDevSlotRange);
-        __syncwarp();
-        int total = 0;
-        for (int w = lane; w < words; w += 32) {
-          uint32_t u = 0;
-          for (int i = 0; i < x.rows; ++i) u |= sh.bits[i][w];
-          total += __popc(u);
-        }
-        total = __reduce_add_sync(0xffffffffu, total);
-        u0 = (int)((int64_t)total * v0 / v);
-        u1 = (int)((int64_t)total * v1 / v);
-        int before = 0;
-        for (int w0 = 0; w0 < words; w0 += 32) {
-          uint32_t u = 0;
-          if (w0 + lane < words)
-            for (int i = 0; i < x.rows; ++i) u |= sh.bits[i][w0 + lane];
-          int incl = __popc(u);
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-          }
-          int at = before + incl - __popc(u);
-          before += __shfl_sync(0xffffffffu, incl, 31);
-          for (; u; u &= u - 1, ++at)
-            if (at >= u0 && at < u1) sh.list[at - u0] = (uint16_t)(32 * (w0 + lane) + __ffs(u) - 1);
-        }
-        __syncwarp();
-      }
-      for (int base = u0; ok && (base < u1 || base == u0); base += 32) {
-        // 32 blocks at a time, one a lane: their ids and the rows they serve
-        int b = -1, rows = 0;
-        int64_t blk = -1;
-        if (base + lane < u1) {
-          b = a.topk ? sh.list[base + lane - u0] : base + lane;
-          for (int i = 0; i < x.rows; ++i)
-            if (a.topk ? (sh.bits[i][b >> 5] >> (b & 31)) & 1u : b <= (x.first + i) / 128) rows |= 1 << i;
-          blk = __ldg(a.block_table + (int64_t)x.r * a.bt_width + b);
-          const bool in = FMT == 0 ? blk >= 0 && blk * a.kps + 8 <= a.num_pages16
-                                   : blk >= 0 && (blk + 1) * 128 <= a.kv_pages * a.bs;
-          if (!in) {
-            blk = -1;
-            set_status(a.status, kDevSlotRange);
-          }
-        }
-        if (lane == 0) ok = mbar_wait(&sh.batch_empty[nbt & 1], ((uint32_t)(nbt >> 1) & 1) ^ 1, a.status, a.lim);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        AttnBatch &bt = sh.batch[nbt & 1];
-        bt.blk[lane] = blk < 0 ? -1 : (int)blk;
-        bt.info[lane] = make_int2(b, rows);
-        if (lane == 0) {
-          bt.n = min(32, u1 - base);
-          bt.first_pos = x.first, bt.seq = x.seq;
-          bt.first = base == u0, bt.last = base + 32 >= u1;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.batch_full[nbt & 1]);
-        ++nbt;
-      }
-    }
+    if (warp == kAtWarps && lane == 0) attn_copies<FMT, kStages, true>(a, maps, sh, sl, ring, q_smem);
+    if (warp == kAtWarps + 1) attn_resolve<FMT>(a, sh, sl, mode);
     return;
   }
 
@@ -557,7 +165,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     return __all_sync(0xffffffffu, got) != 0;
   };
   int v0, v1, v;
-  for (int it = first_item; segment(it, v0, v1, v); ++it) {
+  for (int it = sl.first; sl.segment(a, sh, it, v0, v1, v); ++it) {
     AttnItem x = attn_place(a, it);
     {
       const bool got = mbar_wait(&sh.q_full, nq & 1, a.status, a.lim);
@@ -627,7 +235,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
       bool got = mbar_wait(&sh.full[s], (uint32_t)(j / kStages) & 1, a.status, a.lim);
       if (got && a.test_timeout) got = mbar_wait(&sh.never, 0, a.status, a.lim);
       if (!__all_sync(0xffffffffu, got)) return;  // the warp gives up; the others' waits are bounded too
-      const int2 info = sh.info[s];
+      const int2 info = sh.info[j % kAtInfo];
       ++j;
       if (info.x >= 0 && ((info.y >> row) & 1) && (kGroups == 1 || (j & (kGroups - 1)) == part / kParts)) {
         const uint8_t *st = ring + s * St::kBytes;
@@ -987,7 +595,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
 // partial is its slot 1 (the item starts there), the others' their slot 0.
 constexpr int kJoinWarps = 8;
 template <int W>
-__global__ void __launch_bounds__(32 * kJoinWarps) pa_attn_join_kernel(const __grid_constant__ AttnParams a, int grid) {
+__global__ void __launch_bounds__(32 * kJoinWarps) pa_attn_join_kernel(const __grid_constant__ CacheAttnParams a, int grid) {
   __shared__ float4 acc_s[kJoinWarps][32];
   __shared__ float2 ml_s[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1055,7 +663,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) pa_attn_join_kernel(const __g
       make_uint2(bf16x2_bits(acc.x * inv, acc.y * inv), bf16x2_bits(acc.z * inv, acc.w * inv));
 }
 
-static bool attn_maps(AttnMaps *maps, const AttnParams &a, int fmt) {
+static bool attn_maps(AttnMaps *maps, const CacheAttnParams &a, int fmt) {
   if (fmt == 0) {
     const uint64_t kv = (uint64_t)a.n_kv, pages = (uint64_t)a.num_pages16;
     return map_page_rows(&maps->m[0], a.k_cache, 2048, kv, kv * 2048, pages, 1, 8) &&
@@ -1070,11 +678,11 @@ static bool attn_maps(AttnMaps *maps, const AttnParams &a, int fmt) {
 }
 
 template <int FMT>
-static cudaError_t launch_attn(const AttnParams &a0, int sms, bool pdl, cudaStream_t stream) {
+static cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cudaStream_t stream) {
   AttnMaps maps;
   if (!attn_maps(&maps, a0, FMT)) return cudaErrorInvalidValue;
-  AttnParams a = a0;
-  using Kern = void (*)(const AttnMaps, const AttnParams);
+  CacheAttnParams a = a0;
+  using Kern = void (*)(const AttnMaps, const CacheAttnParams);
   Kern kern = pa_attn_kernel<FMT, 1, false>, clustered = pa_attn_kernel<FMT, 1, true>;
   int smem = AttnSmem<FMT, 1>::kBytes;
   if (a.rows_per == 1) kern = pa_attn_kernel<FMT, 8, false>, clustered = pa_attn_kernel<FMT, 8, true>, smem = AttnSmem<FMT, 8>::kBytes;
@@ -1135,7 +743,9 @@ static cudaError_t launch_attn(const AttnParams &a0, int sms, bool pdl, cudaStre
     cfg.gridDim = dim3(sms);
     cfg.numAttrs = 1;
   }
-  e = cudaLaunchKernelEx(&cfg, kern, maps, a);
+  // several rows an item: the kernel that converts a block once for all rows
+  if (a.rows_per > 1 && a.bt_width <= kTcMaxWidth) e = launch_attn_tc(FMT, maps, a, (int)cfg.gridDim.x, pdl, stream);
+  else e = cudaLaunchKernelEx(&cfg, kern, maps, a);
   if (e != cudaSuccess || a.mode != kAtSliced || a.test_timeout) return e;
   // few items: many partials each, a CTA a head; else a warp a head
   const bool many = a.items * 8 <= sms;
@@ -1207,7 +817,7 @@ extern "C" int pre_attn_attention(const pa_attention_args *in, void *stream) {
   if (!x.workspace || x.workspace_bytes < pre_attn_attention_workspace_bytes(x.R, x.q_len, x.n_kv_heads, sms))
     return PA_ERR_WORKSPACE;
   if (!aligned(x.workspace, 256)) return PA_ERR_ALIGN;
-  pa::AttnParams a = {};
+  pa::CacheAttnParams a = {};
   a.q = static_cast<const uint8_t *>(x.q ? x.q : x.q_fp8);
   a.q_is_fp8 = x.q ? 0 : 1;
   a.q_stride = x.q_stride;
