@@ -37,12 +37,14 @@
 namespace pa {
 
 constexpr int kTcThreads = 640;  // 8 softmax, 8 converting, 4 other warps
-constexpr int kTcSoftRegs = 136, kTcConvRegs = 72, kTcCtlRegs = 56;  // a thread, after the split
+constexpr int kTcSoftRegs = 112, kTcConvRegs = 88, kTcCtlRegs = 80;  // a thread, after the split
 constexpr int kTcTile = 128 * 256;  // bytes of an f16 tile of 128 x 128
 
 template <int FMT>
 struct TcShared : AttnRing<kAtMaxRows, kTcMaxWidth> {
-  uint64_t k_full, k_empty, v_full, v_empty;  // the f16 tiles
+  uint64_t k_full, k_empty;        // the f16 tile of keys; entries without a block go through too
+  uint64_t v_full[2], v_empty[2];  // that of values, by halves of 64 keys
+  uint64_t v_end;                  // the V warps have passed a segment's end
   uint64_t s_full[2], s_empty[2];             // S in tensor memory
   uint64_t p_full, pv_done;                   // P written; O += V^T P done
   uint64_t seg_done;                          // a segment's result is out
@@ -51,7 +53,7 @@ struct TcShared : AttnRing<kAtMaxRows, kTcMaxWidth> {
   int dead;                    // a softmax warp's wait ran out
   int first[2];                // by the segment's parity: the first row's position
   float row_scale[2][kAtMaxRows];
-  uint32_t nan_rows[2][kHeadDim];  // rows that see a NaN value in a dim, among the keys not all rows see
+  uint32_t nan_rows[2][2][kHeadDim];  // for each softmax group: rows that see a NaN value in a dim, of keys not all see
   float off[kAtMaxRows][16];   // lift - m of (row, head)
   float m[kAtMaxRows][16];
   float warp_max[2][4][20];    // by group and warp: a row's maxima, and the largest V scale
@@ -61,20 +63,28 @@ struct TcShared : AttnRing<kAtMaxRows, kTcMaxWidth> {
 
 template <int FMT>
 struct TcSmem {  // K, V, P and Q tiles, the stages, the rest
-  static constexpr int kRest = 4 * kTcTile + (int)sizeof(TcShared<FMT>) + 128;
+  static constexpr int kRest = 4 * kTcTile + (int)sizeof(TcShared<FMT>) + 1024;
   static constexpr int kFit = (kAtSmem - kRest) / AttnStage<FMT>::kBytes;
   static constexpr int kStages = kFit < 4 ? kFit : 4;
   static constexpr int kBytes = kRest + kStages * AttnStage<FMT>::kBytes;
 };
 
-// Descriptor of an operand without swizzle: core matrices of 8 x 16 bytes,
-// 128 contiguous bytes.  K-major: lbo from 8 elements of K to the next 8, sbo
-// from 8 rows to the next 8; MN-major: sbo from 8 rows to the next 8, lbo
-// from 8 elements of K to the next 8.
-__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
-         ((uint64_t)1 << 46);
+// The f16 tiles are rows of 128 bytes (64 elements) with the 128-byte swizzle,
+// two such halves of 16 KB: 16-byte piece c (of 16) of row r.  (Tiles of plain
+// 8 x 16-byte core matrices took the MMAs about four times as long.)
+__device__ __forceinline__ uint32_t tile_at(int r, int c) {
+  return (uint32_t)((c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
+// MN-major operand: rows are elements of K, 8 of them 1024 bytes on (SBO), the
+// next 64 elements of M or N 16 KB on (LBO).
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(16384 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// 16 elements of K on, in a descriptor's 16-byte units: along the 128-byte
+// rows and into the other half (K-major), 16 rows (MN-major).
+__device__ __forceinline__ uint32_t step_k(int k) { return (uint32_t)((k & 3) * 2 + (k >> 2) * 1024); }
+__device__ __forceinline__ uint32_t step_mn(int k) { return (uint32_t)(k * 128); }
 // kind::f16, f16 operands, f32 accumulator; ta, tb: A, B MN-major.
 __device__ __forceinline__ uint32_t idesc_f16(int m, int n, int ta, int tb) {
   return (1u << 4) | ((uint32_t)ta << 15) | ((uint32_t)tb << 16) | ((uint32_t)(n >> 3) << 17) |
@@ -131,35 +141,41 @@ __device__ __forceinline__ uint4 keep_bytes(uint4 w, int n) {
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
+// E2M1 codes of 32 dims of a token and their two scales as the tile's pieces
+// 4 t .. 4 t + 3 of row tok.
+__device__ __forceinline__ void e2m1x32_tile(uint4 w, uint32_t sf2, uint8_t *tile, int tok, int t) {
+  const uint32_t fh = e4m3x4_f16(sf2).x;
+  const uint32_t f[2] = {__byte_perm(fh, fh, 0x1010), __byte_perm(fh, fh, 0x3232)};
+  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    uint32_t h[4];
+    e2m1x8_f16(ww[y], h);
+    *reinterpret_cast<uint4 *>(tile + tile_at(tok, 4 * t + y)) =
+        make_uint4(mul_f16x2(h[0], f[y >> 1]), mul_f16x2(h[1], f[y >> 1]), mul_f16x2(h[2], f[y >> 1]),
+                   mul_f16x2(h[3], f[y >> 1]));
+  }
+}
+
+// The keys of a block, by 128 threads: a token each.
 template <int FMT>
-__device__ __forceinline__ void convert_k(const uint8_t *st, uint8_t *tile, int pt, int ct) {
+__device__ __forceinline__ void convert_k(const uint8_t *st, uint8_t *tile, int pt, int tok) {
   if constexpr (FMT == 0) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int idx = k * 256 + ct, c = idx >> 7, tok = idx & 127;
+    for (int c = 0; c < 8; ++c) {
       uint4 lo, hi;
       e4m3x16_f16(*reinterpret_cast<const uint4 *>(st + (tok >> 4) * 2048 + c * 256 + (tok & 15) * 16), lo, hi);
-      *reinterpret_cast<uint4 *>(tile + (2 * c) * 2048 + tok * 16) = lo;
-      *reinterpret_cast<uint4 *>(tile + (2 * c + 1) * 2048 + tok * 16) = hi;
+      *reinterpret_cast<uint4 *>(tile + tile_at(tok, 2 * c)) = lo;
+      *reinterpret_cast<uint4 *>(tile + tile_at(tok, 2 * c + 1)) = hi;
     }
   } else {
+    const int in = tok & (pt - 1);
+    const uint8_t *base = st + (tok - in) * 144;
+    const uint2 sf = *reinterpret_cast<const uint2 *>(base + pt * 64 + in * 8);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int idx = k * 256 + ct, t = idx >> 7, tok = idx & 127, in = tok & (pt - 1);
-      const uint8_t *base = st + (tok - in) * 144;
-      const uint4 w = *reinterpret_cast<const uint4 *>(base + in * 64 + 16 * t);
-      const uint32_t fh = e4m3x4_f16(*reinterpret_cast<const uint16_t *>(base + pt * 64 + in * 8 + 2 * t)).x;
-      const uint32_t f[2] = {__byte_perm(fh, fh, 0x1010), __byte_perm(fh, fh, 0x3232)};
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        uint32_t h[4];
-        e2m1x8_f16(ww[y], h);
-        *reinterpret_cast<uint4 *>(tile + (4 * t + y) * 2048 + tok * 16) =
-            make_uint4(mul_f16x2(h[0], f[y >> 1]), mul_f16x2(h[1], f[y >> 1]), mul_f16x2(h[2], f[y >> 1]),
-                       mul_f16x2(h[3], f[y >> 1]));
-      }
-    }
+    for (int t = 0; t < 4; ++t)
+      e2m1x32_tile(*reinterpret_cast<const uint4 *>(base + in * 64 + 16 * t), (t < 2 ? sf.x : sf.y) >> (16 * (t & 1)) & 0xffffu,
+                   tile, tok, t);
   }
 }
 
@@ -169,13 +185,19 @@ __device__ __forceinline__ void convert_k(const uint8_t *st, uint8_t *tile, int 
 __device__ __forceinline__ uint32_t rows_that_see(int key, int first, uint32_t rows) {
   return key <= first ? rows : rows & ~((1u << min(key - first, 31)) - 1u);
 }
+__device__ __forceinline__ void note_nan(uint32_t (&nan_rows)[2][kHeadDim], int d, uint32_t rows) {
+  atomicOr(&nan_rows[0][d], rows);
+  atomicOr(&nan_rows[1][d], rows);
+}
+// Half (64 keys) of a block's values, by 128 threads: FP8 a dim each, NVFP4 two
+// of the four 32-dim parts of a token each.
 template <int FMT>
-__device__ __forceinline__ void convert_v(const uint8_t *st, uint8_t *tile, int pt, int ct, int first, int last,
-                                          uint32_t rows, bool all, uint32_t *nan_rows) {
+__device__ __forceinline__ void convert_v(const uint8_t *st, uint8_t *tile, int pt, int ct, int half, int first, int last,
+                                          uint32_t rows, bool all, uint32_t (&nan_rows)[2][kHeadDim]) {
   if constexpr (FMT == 0) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int idx = k * 256 + ct, pg = idx >> 7, d = idx & 127;
+      const int pg = 4 * half + k, d = ct;
       uint4 w = *reinterpret_cast<const uint4 *>(st + AttnStage<0>::kV + pg * 2048 + d * 16);
       if (!all) {
         if (last < 127) w = keep_bytes(w, last + 1 - 16 * pg);
@@ -188,21 +210,22 @@ __device__ __forceinline__ void convert_v(const uint8_t *st, uint8_t *tile, int 
             for (int q = 0; q < 4; ++q)
               if ((e >> 2) == q && ((x[q] >> (8 * (e & 3))) & 0x7fu) == 0x7fu) {
                 x[q] &= ~(0xffu << (8 * (e & 3)));
-                atomicOr(&nan_rows[d], rows_that_see(16 * pg + e, first, rows));
+                note_nan(nan_rows, d, rows_that_see(16 * pg + e, first, rows));
               }
           w = make_uint4(x[0], x[1], x[2], x[3]);
         }
       }
       uint4 lo, hi;
       e4m3x16_f16(w, lo, hi);
-      *reinterpret_cast<uint4 *>(tile + (2 * pg) * 2048 + d * 16) = lo;
-      *reinterpret_cast<uint4 *>(tile + (2 * pg + 1) * 2048 + d * 16) = hi;
+      *reinterpret_cast<uint4 *>(tile + tile_at(d, 2 * pg)) = lo;
+      *reinterpret_cast<uint4 *>(tile + tile_at(d, 2 * pg + 1)) = hi;
     }
   } else {
+    const int tok = 64 * half + (ct & 63), in = tok & (pt - 1);
+    const uint8_t *base = st + (tok - in) * 144 + pt * 72;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int idx = k * 256 + ct, t = idx >> 7, tok = idx & 127, in = tok & (pt - 1);
-      const uint8_t *base = st + (tok - in) * 144 + pt * 72;
+      const int t = 2 * (ct >> 6) + k;
       uint4 w = *reinterpret_cast<const uint4 *>(base + in * 64 + 16 * t);
       const uint8_t *sf = base + pt * 64 + (in >> 2) * 32 + 8 * t + (in & 3);
       uint32_t sf2 = (uint32_t)sf[0] | ((uint32_t)sf[4] << 8);
@@ -212,21 +235,10 @@ __device__ __forceinline__ void convert_v(const uint8_t *st, uint8_t *tile, int 
         for (int g = 0; g < 2; ++g)
           if (((sf2 >> (8 * g)) & 0x7fu) == 0x7fu) {
             sf2 &= ~(0xffu << (8 * g));
-            for (int d = 32 * t + 16 * g; d < 32 * t + 16 * g + 16; ++d)
-              atomicOr(&nan_rows[d], rows_that_see(tok, first, rows));
+            for (int d = 32 * t + 16 * g; d < 32 * t + 16 * g + 16; ++d) note_nan(nan_rows, d, rows_that_see(tok, first, rows));
           }
       }
-      const uint32_t fh = e4m3x4_f16(sf2).x;
-      const uint32_t f[2] = {__byte_perm(fh, fh, 0x1010), __byte_perm(fh, fh, 0x3232)};
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        uint32_t h[4];
-        e2m1x8_f16(ww[y], h);
-        *reinterpret_cast<uint4 *>(tile + (4 * t + y) * 2048 + tok * 16) =
-            make_uint4(mul_f16x2(h[0], f[y >> 1]), mul_f16x2(h[1], f[y >> 1]), mul_f16x2(h[2], f[y >> 1]),
-                       mul_f16x2(h[3], f[y >> 1]));
-      }
+      e2m1x32_tile(w, sf2, tile, tok, t);
     }
   }
 }
@@ -239,7 +251,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
   static_assert(Sm::kBytes <= kAtSmem && Sm::kStages >= 2, "shared memory of a CTA");
   constexpr int kStages = Sm::kStages;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t *k_tile = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
+  uint8_t *k_tile = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t *v_tile = k_tile + kTcTile, *p_tile = v_tile + kTcTile, *q_tile = p_tile + kTcTile, *ring = q_tile + kTcTile;
   TcShared<FMT> &sh = *reinterpret_cast<TcShared<FMT> *>(ring + kStages * St::kBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -256,10 +268,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
       mbar_init(&sh.s_full[s], 1);
       mbar_init(&sh.s_empty[s], 8);
     }
-    mbar_init(&sh.k_full, 8);
+    mbar_init(&sh.k_full, 4);
     mbar_init(&sh.k_empty, 1);
-    mbar_init(&sh.v_full, 8);
-    mbar_init(&sh.v_empty, 1);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&sh.v_full[h], 4);
+      mbar_init(&sh.v_empty[h], 1);
+    }
+    mbar_init(&sh.v_end, 4);
     mbar_init(&sh.p_full, 8);
     mbar_init(&sh.pv_done, 1);
     mbar_init(&sh.seg_done, 8);
@@ -268,6 +283,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
     sh.dead = 0;
     fence_mbar_init();
   }
+  if (tid < 4 * kHeadDim) (&sh.nan_rows[0][0][0])[tid] = 0;
   const AttnSlice sl = attn_slice<8>(a, sh, a.mode);
   if (sl.none) return;
   if (warp == 19) tc_alloc(&sh.tmem, 512);
@@ -275,7 +291,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  constexpr uint32_t kOCol = 256;  // S: columns 0 and 128; O: 256 .. 383
+  // S: columns 0 and 128; O, 16 columns a row; each key's thread's sums of the weights, as many
+  constexpr uint32_t kOCol = 256, kLCol = 384;
   const int pt = min(a.bs, 128);
 
   if (warp >= 16) {
@@ -284,43 +301,65 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
     if (warp == 17) attn_resolve<FMT>(a, sh, sl, a.mode);
     if (warp == 18 && lane == 0) {
       // ------------------------------------------------------------ the MMAs
-      const uint64_t kd = sdesc_plain(smem_u32(k_tile), 2048, 128), qd = sdesc_plain(smem_u32(q_tile), 2048, 128);
-      // V: FP8 tiles are [8 keys][128 dims][8 keys' values], NVFP4 ones [8 dims][128 keys][8 dims' values]
-      const uint64_t vd = FMT == 0 ? sdesc_plain(smem_u32(v_tile), 2048, 128) : sdesc_plain(smem_u32(v_tile), 128, 2048);
-      const uint64_t pd = sdesc_plain(smem_u32(p_tile), 128, 2048);
-      constexpr int kVStep = FMT == 0 ? 256 : 16;  // 16 keys on, in units of 16 bytes
+      // K and Q: rows are keys, (row, head)s.  V: rows are dims (FP8: pages hold
+      // a dim's keys together) or keys (NVFP4).  P: rows are keys
+      const uint64_t kd = sdesc_sw128(smem_u32(k_tile)), qd = sdesc_sw128(smem_u32(q_tile)), pd = sdesc_mn(smem_u32(p_tile));
+      const uint64_t vd = FMT == 0 ? sdesc_sw128(smem_u32(v_tile)) : sdesc_mn(smem_u32(v_tile));
       bool ok = true;
-      uint32_t n = 0, np = 0;  // entries, blocks whose PV is issued
+      uint32_t n = 0, np = 0, ends = 0;  // entries, blocks whose PV is issued, segments ended
       int v0, v1, v;
       for (int it = sl.first; ok && sl.segment(a, sh, it, v0, v1, v); ++it) {
         const int rows = attn_place(a, it).rows;
         const uint32_t ids = idesc_f16(128, 16 * rows, 0, 0), idp = idesc_f16(128, 16 * rows, FMT == 0 ? 0 : 1, 1);
+        // S of entry n and O of the block before it, whichever can go first; O
+        // by halves of 64 keys
         bool pending = false, begun = false, more = true;
         while (ok && more) {
-          if (!(ok = mbar_wait(&sh.k_full, n & 1, a.status, a.lim))) break;
-          more = sh.info[n % kAtInfo].x >= 0;
-          if (!(ok = mbar_wait(&sh.s_empty[n & 1], ((n >> 1) & 1) ^ 1, a.status, a.lim))) break;
-          tc_fence_after();
-          if (more) {
+          bool s_out = false;
+          int halves = pending ? 0 : 2;
+          const uint64_t t0 = globaltimer();
+          while (!s_out || halves < 2) {
+            bool moved = false;
+            if (halves < 2 && mbar_try_wait(smem_u32(&sh.v_full[halves]), np & 1) &&
+                (halves == 1 || mbar_try_wait(smem_u32(&sh.p_full), np & 1))) {
+              tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 8; ++k) mma_f16_ss(tmem + (n & 1) * 128, kd + 256 * k, qd + 256 * k, ids, k > 0);
-            tc_commit(&sh.s_full[n & 1]);
-            tc_commit(&sh.k_empty);
-          }
-          if (pending) {
-            ok = mbar_wait(&sh.p_full, np & 1, a.status, a.lim) && mbar_wait(&sh.v_full, np & 1, a.status, a.lim);
-            if (!ok) break;
-            tc_fence_after();
+              for (int k = 0; k < 4; ++k) {
+                const int kk = 4 * halves + k;
+                mma_f16_ss(tmem + kOCol, vd + (FMT == 0 ? step_k(kk) : step_mn(kk)), pd + step_mn(kk), idp,
+                           (begun || k > 0) ? 1u : 0u);
+              }
+              begun = true;
+              if (halves == 1) tc_commit(&sh.pv_done);
+              tc_commit(&sh.v_empty[halves]);
+              ++halves;
+              moved = true;
+            }
+            if (!s_out && mbar_try_wait(smem_u32(&sh.k_full), n & 1) &&
+                mbar_try_wait(smem_u32(&sh.s_empty[n & 1]), ((n >> 1) & 1) ^ 1)) {
+              more = sh.info[n % kAtInfo].x >= 0;
+              if (more) {
+                tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_f16_ss(tmem + kOCol, vd + kVStep * k, pd + 16 * k, idp, (begun || k > 0) ? 1u : 0u);
-            tc_commit(&sh.pv_done);
-            tc_commit(&sh.v_empty);
-            begun = true;
-            ++np;
+                for (int k = 0; k < 8; ++k) mma_f16_ss(tmem + (n & 1) * 128, kd + step_k(k), qd + step_k(k), ids, k > 0);
+                tc_commit(&sh.s_full[n & 1]);
+                tc_commit(&sh.k_empty);
+              }
+              s_out = true;
+              moved = true;
+            }
+            if (!moved && globaltimer() - t0 > a.lim) {
+              set_status(a.status, kDevWaitTimeout);
+              ok = false;
+              break;
+            }
           }
+          if (!ok) break;
+          if (pending) ++np;
           pending = more;
           if (!more) {  // the end of the segment: the softmax groups read O
+            if (!(ok = mbar_wait(&sh.v_end, ends & 1, a.status, a.lim))) break;
+            ++ends;
             tc_commit(&sh.s_full[n & 1]);
             tc_commit(&sh.k_empty);
           }
@@ -335,121 +374,147 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
   } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcConvRegs));
     // ---------------------------------------------------------- converters
-    const int ct = tid - 256, cw = warp - 8;
-    uint32_t j = 0, nv = 0, seg = 0;  // entries, blocks, segments
-    // the queries of an item, 64 dims of a (row, head) a thread (a row a
-    // warp), asked for a segment ahead and kept in registers
-    uint4 qr[8];
-    AttnItem nx;
-    const int qrow = cw, qhead = lane >> 1, qd0 = 64 * (lane & 1);
-    auto ask = [&](int it) {
-      bool bad = false;
-      nx = attn_item(a, it, &bad);
-      const bool have = qrow < nx.rows && qhead < a.group;
-      const int64_t at = ((int64_t)nx.r * a.q_len + nx.row0 + qrow) * a.q_stride + (int64_t)(nx.h * a.group + qhead) * kHeadDim + qd0;
-      const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (a.q_is_fp8 ? at : 2 * at));
-#pragma unroll
-      for (int k = 0; k < 8; ++k) qr[k] = have && (k < 4 || !a.q_is_fp8) ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-    };
-    // and their f16 values in the tile [8 dims][row, head][8 dims' values]
-    auto lay_out = [&]() {
-      float top = 0.f;
-      auto values = [&](int k, float (&x)[8]) {  // dims qd0 + 8 k .. + 7
-        if (a.q_is_fp8) {
-          const uint4 w = qr[k >> 1];
-          const uint2 h0 = e4m3x4_f16(k & 1 ? w.z : w.x), h1 = e4m3x4_f16(k & 1 ? w.w : w.y);
-          const uint32_t h[4] = {h0.x, h0.y, h1.x, h1.y};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
-            x[2 * e] = f.x, x[2 * e + 1] = f.y;
-          }
-        } else {
-          const uint32_t h[4] = {qr[k].x, qr[k].y, qr[k].z, qr[k].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[2 * e] = bf16_to_f32(h[e] & 0xffffu), x[2 * e + 1] = bf16_to_f32(h[e] >> 16);
-        }
-      };
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float x[8];
-        values(k, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int ex = max(exponent_of(top), -110) - 14;
-      const float down = pow2i(-ex);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float x[8];
-        values(k, x);
-        *reinterpret_cast<uint4 *>(q_tile + ((qd0 >> 3) + k) * 2048 + (qrow * 16 + qhead) * 16) =
-            make_uint4(f16x2_bits(x[0] * down, x[1] * down), f16x2_bits(x[2] * down, x[3] * down),
-                       f16x2_bits(x[4] * down, x[5] * down), f16x2_bits(x[6] * down, x[7] * down));
-      }
-      if (lane == 0) sh.row_scale[seg & 1][cw] = a.score_scale * pow2i(ex);
-      if (ct < kHeadDim) sh.nan_rows[seg & 1][ct] = 0;
-      if (ct == 0) sh.first[seg & 1] = nx.first;
-    };
+    const int ct = tid & 127, cw = warp & 3;
+    uint32_t j = 0, seg = 0;  // entries, segments
+    bool ok = true;
+    auto all_got = [&](bool got) { return ok = __all_sync(0xffffffffu, got) != 0; };
     int v0, v1, v;
-    bool ok = sl.segment(a, sh, sl.first, v0, v1, v);
-    if (ok) ask(sl.first);
-    for (int it = sl.first; ok && sl.segment(a, sh, it, v0, v1, v); ++it, ++seg) {
-      if (seg == 0) lay_out();
-      const int first_pos = nx.first, last_pos = nx.first + nx.rows - 1;
-      const int every = (1 << nx.rows) - 1;
-      int w0, w1, w;
-      const bool next = sl.segment(a, sh, it + 1, w0, w1, w);
-      if (next) ask(it + 1);
-      bool more = true;
-      while (more) {
-        const int s = j % kStages;
-        ok = mbar_wait(&sh.full[s], (j / kStages) & 1, a.status, a.lim) &&
-             mbar_wait(&sh.k_empty, (j & 1) ^ 1, a.status, a.lim);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        const int2 info = sh.info[j % kAtInfo];
-        const int b = info.x;
-        more = b >= 0;
-        const uint8_t *st = ring + s * St::kBytes;
-        if (more) {
-          convert_k<FMT>(st, k_tile, pt, ct);
-          if constexpr (FMT == 0)
-            sh.scales[j & 3][ct >> 7][ct & 127] = *reinterpret_cast<const float *>(st + (ct < 128 ? St::kKs : St::kVs) + 4 * (ct & 127));
-        } else if (next) {
-          // the segment before this one is out: what it noted may be replaced
-          if (seg > 0) ok = mbar_wait(&sh.seg_done, (seg - 1) & 1, a.status, a.lim);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
+    if (warp < 12) {
+      // keys and queries.  A (row, head)'s 64 dims a thread, two threads each:
+      // rows cw and cw + 4, the first asked for a segment ahead
+      uint4 qr[8];
+      AttnItem nx;
+      const int qhead = lane >> 1, qd0 = 64 * (lane & 1);
+      auto ask = [&](int row) {
+        const bool have = row < nx.rows && qhead < a.group;
+        const int64_t at = ((int64_t)nx.r * a.q_len + nx.row0 + row) * a.q_stride + (int64_t)(nx.h * a.group + qhead) * kHeadDim + qd0;
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (a.q_is_fp8 ? at : 2 * at));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) qr[k] = have && (k < 4 || !a.q_is_fp8) ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+      };
+      auto look_up = [&](int it) {
+        bool bad = false;
+        nx = attn_item(a, it, &bad);
+        ask(cw);
+        if (cw + 4 < nx.rows && qhead < a.group)
+          prefetch_l2(a.q + (((int64_t)nx.r * a.q_len + nx.row0 + cw + 4) * a.q_stride +
+                             (int64_t)(nx.h * a.group + qhead) * kHeadDim + qd0) * (a.q_is_fp8 ? 1 : 2));
+      };
+      // f16 values into the tile: a (row, head) a row of it
+      auto lay_out_row = [&](int row, uint32_t sg) {
+        float top = 0.f;
+        auto values = [&](int k, float (&x)[8]) {  // dims qd0 + 8 k .. + 7
+          if (a.q_is_fp8) {
+            const uint4 w = qr[k >> 1];
+            const uint2 h0 = e4m3x4_f16(k & 1 ? w.z : w.x), h1 = e4m3x4_f16(k & 1 ? w.w : w.y);
+            const uint32_t h[4] = {h0.x, h0.y, h1.x, h1.y};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
+              x[2 * e] = f.x, x[2 * e + 1] = f.y;
+            }
+          } else {
+            const uint32_t h[4] = {qr[k].x, qr[k].y, qr[k].z, qr[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[2 * e] = bf16_to_f32(h[e] & 0xffffu), x[2 * e + 1] = bf16_to_f32(h[e] >> 16);
           }
-          ++seg;
-          lay_out();
-          --seg;
+        };
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float x[8];
+          values(k, x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.k_full);
-        if (more) {
-          ok = mbar_wait(&sh.v_empty, (nv & 1) ^ 1, a.status, a.lim);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int ex = max(exponent_of(top), -110) - 14;
+        const float down = pow2i(-ex);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float x[8];
+          values(k, x);
+          *reinterpret_cast<uint4 *>(q_tile + tile_at(row * 16 + qhead, (qd0 >> 3) + k)) =
+              make_uint4(f16x2_bits(x[0] * down, x[1] * down), f16x2_bits(x[2] * down, x[3] * down),
+                         f16x2_bits(x[4] * down, x[5] * down), f16x2_bits(x[6] * down, x[7] * down));
+        }
+        if (lane == 0) sh.row_scale[sg & 1][row] = a.score_scale * pow2i(ex);
+      };
+      auto lay_out = [&](uint32_t sg) {
+#pragma unroll 1
+        for (int row = cw; row < nx.rows; row += 4) {
+          if (row >= 4) ask(row);
+          lay_out_row(row, sg);
+        }
+        if (ct == 0) sh.first[sg & 1] = nx.first;
+      };
+      if (sl.segment(a, sh, sl.first, v0, v1, v)) {
+        look_up(sl.first);
+        lay_out(0);
+      }
+      for (int it = sl.first; ok && sl.segment(a, sh, it, v0, v1, v); ++it, ++seg) {
+        int w0, w1, w;
+        const bool next = sl.segment(a, sh, it + 1, w0, w1, w);
+        if (next) look_up(it + 1);
+        for (bool more = true; more; ++j) {
+          const int s = j % kStages;
+          if (!all_got(mbar_wait(&sh.full[s], (j / kStages) & 1, a.status, a.lim) &&
+                       mbar_wait(&sh.k_empty, (j & 1) ^ 1, a.status, a.lim)))
             break;
+          more = sh.info[j % kAtInfo].x >= 0;
+          if (more) {
+            const uint8_t *st = ring + s * St::kBytes;
+            convert_k<FMT>(st, k_tile, pt, ct);
+            if constexpr (FMT == 0) {
+              sh.scales[j & 3][0][ct] = *reinterpret_cast<const float *>(st + St::kKs + 4 * ct);
+              sh.scales[j & 3][1][ct] = *reinterpret_cast<const float *>(st + St::kVs + 4 * ct);
+            }
+          } else if (next) {
+            // the segment before this one is out: its scales may be replaced
+            if (seg > 0 && !all_got(mbar_wait(&sh.seg_done, (seg - 1) & 1, a.status, a.lim))) break;
+            lay_out(seg + 1);
           }
-          convert_v<FMT>(st, v_tile, pt, ct, first_pos - b * 128, last_pos - b * 128, (uint32_t)info.y,
-                         info.y == every && first_pos - b * 128 >= 127, sh.nan_rows[seg & 1]);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.v_full);
-          ++nv;
+          if (lane == 0) {
+            mbar_arrive(&sh.k_full);
+            mbar_arrive(&sh.empty[s]);
+          }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty[s]);
-        ++j;
+      }
+    } else {
+      // values
+      uint32_t nv = 0;  // blocks
+      for (int it = sl.first; ok && sl.segment(a, sh, it, v0, v1, v); ++it, ++seg) {
+        bool bad = false;
+        const AttnItem x = attn_item(a, it, &bad);
+        const int every = (1 << x.rows) - 1;
+        for (bool more = true; more; ++j) {
+          const int s = j % kStages;
+          if (!all_got(mbar_wait(&sh.full[s], (j / kStages) & 1, a.status, a.lim))) break;
+          const int2 info = sh.info[j % kAtInfo];
+          more = info.x >= 0;
+          if (more) {
+            const int first = x.first - info.x * 128;
+            for (int half = 0; ok && half < 2; ++half) {
+              if (!all_got(mbar_wait(&sh.v_empty[half], (nv & 1) ^ 1, a.status, a.lim))) break;
+              convert_v<FMT>(ring + s * St::kBytes, v_tile, pt, ct, half, first, first + x.rows - 1, (uint32_t)info.y,
+                             info.y == every && first >= 127, sh.nan_rows[seg & 1]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh.v_full[half]);
+            }
+            if (!ok) break;
+            ++nv;
+          } else if (seg > 0 && !all_got(mbar_wait(&sh.seg_done, (seg - 1) & 1, a.status, a.lim))) {
+            break;
+          }
+          __syncwarp();
+          if (lane == 0) {
+            if (!more) mbar_arrive(&sh.v_end);
+            mbar_arrive(&sh.empty[s]);
+          }
+        }
       }
     }
   } else {
@@ -465,11 +530,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
     int v0, v1, v;
     for (int it = sl.first; live && sl.segment(a, sh, it, v0, v1, v); ++it, ++seg) {
       const AttnItem x = attn_place(a, it);
-      float l[4][16];
+      {
+        float zero[16];
 #pragma unroll
-      for (int rr = 0; rr < 4; ++rr)
-#pragma unroll
-        for (int h = 0; h < 16; ++h) l[rr][h] = 0.f;
+        for (int h = 0; h < 16; ++h) zero[h] = 0.f;
+        for (int row = grp; row < x.rows; row += 2) tc_st16(lanes + kLCol + 16 * row, zero);
+        tc_wait_st();
+      }
       if ((tid & 127) < 64) {
         const int row = 2 * ((tid & 127) >> 4) + grp;
         sh.off[row][tid & 15] = 1e30f;  // any score is above the limit: the first sets m
@@ -493,19 +560,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
         float ks = 1.f, vs = 1.f;
         if constexpr (FMT == 0) ks = sh.scales[n & 3][0][key], vs = sh.scales[n & 3][1][key];
         bool waited = false;
-#pragma unroll
-        for (int rr = 0; rr < 4; ++rr) {
-          const int row = 2 * rr + grp;
-          if (row >= x.rows) continue;
-          uint8_t *pr = p_tile + 2 * row * 2048 + key * 16;
+#pragma unroll 1
+        for (int row = grp; row < x.rows; row += 2) {
+          uint4 *p0 = reinterpret_cast<uint4 *>(p_tile + tile_at(key, 2 * row)), *p1 = reinterpret_cast<uint4 *>(p_tile + tile_at(key, 2 * row + 1));
           if (!((info.y >> row) & 1)) {  // the row does not attend the block
             if (!waited) wait(&sh.pv_done, (np & 1) ^ 1), waited = true;
-            *reinterpret_cast<uint4 *>(pr) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(pr + 2048) = make_uint4(0, 0, 0, 0);
+            *p0 = *p1 = make_uint4(0, 0, 0, 0);
             continue;
           }
-          float s[16], y[16];
+          float s[16], y[16], l[16];
           tc_ld16(lanes + (n & 1) * 128 + 16 * row, s);
+          tc_ld16(lanes + kLCol + 16 * row, l);
           const bool seen = kj <= first + row;
           const float kk = ks * sh.row_scale[seg & 1][row];
           tc_wait_ld();
@@ -553,13 +618,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
             float o[16];
             if (f != 1.f) {  // the group's other rows
 #pragma unroll 1
-              for (int r2 = 0; r2 < 4; ++r2) {
-                if (r2 == rr || 2 * r2 + grp >= x.rows) continue;
-                tc_ld16(lanes + kOCol + 16 * (2 * r2 + grp), o);
+              for (int r2 = grp; r2 < x.rows; r2 += 2) {
+                if (r2 == row) continue;
+                tc_ld16(lanes + kOCol + 16 * r2, o);
                 tc_wait_ld();
 #pragma unroll
                 for (int h = 0; h < 16; ++h) o[h] *= f;
-                tc_st16(lanes + kOCol + 16 * (2 * r2 + grp), o);
+                tc_st16(lanes + kOCol + 16 * r2, o);
               }
             }
             tc_ld16(lanes + kOCol + 16 * row, o);
@@ -572,7 +637,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
 #pragma unroll
               for (int w = 0; w < 4; ++w) t = fmaxf(t, sh.warp_max[grp][w][h]);
               const float al = t == was ? 1.f : ex2_approx(was - t);
-              l[rr][h] *= al;
+              l[h] *= al;
               o[h] *= al * f;
               if ((tid & 127) == h) nm = t;
             }
@@ -594,12 +659,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             const float e0 = ex2_approx(y[2 * q]), e1 = ex2_approx(y[2 * q + 1]);
-            l[rr][2 * q] += e0, l[rr][2 * q + 1] += e1;
+            l[2 * q] += e0, l[2 * q + 1] += e1;
             w[q] = f16x2_bits(FMT == 0 ? e0 * wu : e0, FMT == 0 ? e1 * wu : e1);
           }
-          *reinterpret_cast<uint4 *>(pr) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4 *>(pr + 2048) = make_uint4(w[4], w[5], w[6], w[7]);
+          *p0 = make_uint4(w[0], w[1], w[2], w[3]);
+          *p1 = make_uint4(w[4], w[5], w[6], w[7]);
+          tc_st16(lanes + kLCol + 16 * row, l);
         }
+        tc_wait_st();
         if (!waited) wait(&sh.pv_done, (np & 1) ^ 1);
         fence_proxy_async_smem();
         tc_fence_before();
@@ -624,14 +691,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
         a.shares[it] = make_int2(0, 0);
       }
       const float up = FMT == 0 ? pow2i(ev) : 1.f;
-      const uint32_t nan_rows = sh.nan_rows[seg & 1][key];  // this thread's dim is `key`
-#pragma unroll
-      for (int rr = 0; rr < 4; ++rr) {
-        const int row = 2 * rr + grp;
-        if (row >= x.rows) continue;
+      const uint32_t nan_rows = sh.nan_rows[seg & 1][grp][key];  // this thread's dim is `key`
+      sh.nan_rows[seg & 1][grp][key] = 0;
+#pragma unroll 1
+      for (int row = grp; row < x.rows; row += 2) {
+        float l[16];
+        tc_ld16(lanes + kLCol + 16 * row, l);
+        tc_wait_ld();
 #pragma unroll
         for (int h = 0; h < 16; ++h) {
-          float t = l[rr][h];
+          float t = l[h];
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
           if (lane == h) sh.warp_sum[grp][gw][h] = t;
