@@ -34,14 +34,14 @@
 
 #include "../../include/pre_attn.h"
 #include "pa_attn.cuh"
-#include "pa_attn_tc.h"
 
 namespace pa {
 
-constexpr int kAtThreads = 32 * (kAtWarps + 4);    // and the producer's warpgroup (one warp of it works)
+constexpr int kAtThreads = 32 * (kAtWarps + 4);  // and the producers' warpgroup, of which two warps work
 // Registers a thread after the split (setmaxnreg): the compute warps hold o,
-// the queries and the codes of 32 keys.  Their sum must not exceed what the
-// CTA was launched with, which launch_attn checks.
+// the queries and the step's scores and codes (twelve compute warps of 144
+// registers were slower).  The sum must not exceed what the CTA was launched
+// with, which launch_attn checks.
 constexpr int kAtComputeRegs = 200, kAtProducerRegs = 96;
 
 template <int ROWS>
@@ -113,9 +113,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
   using Sm = AttnSmem<FMT, WPR>;
   static_assert(Sm::kBytes <= kAtSmem && Sm::kStages >= 3, "shared memory of a CTA");
   constexpr int kStages = Sm::kStages;
-  // a warp takes 32 keys at least: with eight warps a row, two groups of four
-  // take alternate blocks
-  constexpr int kParts = WPR > 4 ? 4 : WPR, kGroups = WPR / kParts, kKeys = 128 / kParts;
+  // a warp takes 16 Y keys at a time and at least those of a block: a row's
+  // warps beyond that take alternate blocks
+  constexpr int Y = CLUSTER || FMT == 1 ? 2 : 4, kMost = 128 / (16 * Y);
+  constexpr bool kEarly = Y == 2;
+  constexpr int kParts = WPR > kMost ? kMost : WPR, kGroups = WPR / kParts, kKeys = 128 / kParts;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
   uint8_t *q_smem = ring + kStages * St::kBytes;  // [row][group][128], as q holds them
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
   if (sl.none) return;
   if (warp >= kAtWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtProducerRegs));
-    if (warp == kAtWarps && lane == 0) attn_copies<FMT, kStages, true>(a, maps, sh, sl, ring, q_smem);
+    if (warp == kAtWarps && lane == 0) attn_copies<FMT, kStages>(a, maps, sh, sl, ring, q_smem);
     if (warp == kAtWarps + 1) attn_resolve<FMT>(a, sh, sl, mode);
     return;
   }
@@ -237,20 +239,17 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
       if (!__all_sync(0xffffffffu, got)) return;  // the warp gives up; the others' waits are bounded too
       const int2 info = sh.info[j % kAtInfo];
       ++j;
-      if (info.x >= 0 && ((info.y >> row) & 1) && (kGroups == 1 || (j & (kGroups - 1)) == part / kParts)) {
+      if (info.x >= 0 && ((info.y >> row) & 1) && (kGroups == 1 || j % kGroups == part / kParts)) {
         const uint8_t *st = ring + s * St::kBytes;
         const bool cut = info.x * 128 + 127 > p;  // keys after the row's position
 #pragma unroll 1
-        for (int k0 = key0; k0 < key0 + kKeys; k0 += 32) {
-          // scores of 32 keys: this thread's are keys k0 + 16 y + 4 t + (e + rot) % 4, y = 0, 1, e = 0 .. 3
-          float c[4][4];
+        for (int k0 = key0; k0 < key0 + kKeys; k0 += 16 * Y) {
+          // scores of 16 Y keys: of each 16, this thread's are 4 t + (e + rot) % 4, e = 0 .. 3
+          float c[2 * Y][4];
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt)
+          for (int nt = 0; nt < 2 * Y; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) c[nt][e] = 0.f;
-          float sv[2][8];     // [head g, g + 8][4 y + e]
-          uint32_t vraw[32];  // the value codes of those keys, read before the softmax needs its results
-          uint32_t vsf[2];
           if constexpr (FMT == 0) {
             // a page is [8 chunks of 16 dims][16 tokens][16 bytes].  Column n
             // of tile nt is key 4 (n / 2) + 2 nt + n % 2 (the rows of an 8x8
@@ -261,37 +260,28 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
             const uint32_t at = smem_u32(st) + (k0 >> 4) * 2048 + (lane >> 4) * 256 + tok * 16;
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc) {
-              uint32_t w[2][4];
-              ldsm_x4(at + cc * 512, w[0]);
-              ldsm_x4(at + 2048 + cc * 512, w[1]);
+              uint32_t w[Y][4];
+#pragma unroll
+              for (int y = 0; y < Y; ++y) ldsm_x4(at + y * 2048 + cc * 512, w[y]);
 #pragma unroll
               for (int z = 0; z < 2; ++z)
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
+                for (int y = 0; y < Y; ++y)
 #pragma unroll
                   for (int u = 0; u < 2; ++u) {
                     const uint2 k2 = e4m3x4_f16(w[y][2 * z + u]);
                     mma_f16(c[2 * y + u], qf[2 * cc + z], k2.x, k2.y);
                   }
             }
-            // a page of values is [128 dims][16 tokens]
-            const uint32_t vat = smem_u32(st) + St::kV + (k0 >> 4) * 2048 + lane * 16;
-#pragma unroll
-            for (int q4 = 0; q4 < 8; ++q4) {
-              uint32_t w[4];
-              ldsm_x4(vat + q4 * 512, w);
-#pragma unroll
-              for (int y = 0; y < 4; ++y) vraw[4 * q4 + y] = w[y];
-            }
           } else {
             // a token is 64 bytes of codes; thread t takes the 16 of dims
             // 32 t .. + 31 (two scale groups).  Column n of tile nt is key
             // 4 (n / 2) + (2 nt + n % 2 + n / 2) % 4: with that rotation the
             // value reads below meet in a bank two at a time, not four
-            uint32_t f0[4], f1[4];
-            uint4 kw[4];
+            uint32_t f0[2 * Y], f1[2 * Y];
+            uint4 kw[2 * Y];
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
+            for (int nt = 0; nt < 2 * Y; ++nt) {
               const int quad = k0 + 16 * (nt >> 1) + 4 * (g >> 1), in = quad & (pt - 1);
               const int tok = in + ((2 * (nt & 1) + (g & 1) + (g >> 1)) & 3);
               const uint8_t *kp = st + (quad - in) * 144;
@@ -302,101 +292,115 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
 #pragma unroll
             for (int y = 0; y < 4; ++y)
 #pragma unroll
-              for (int nt = 0; nt < 4; ++nt) {
+              for (int nt = 0; nt < 2 * Y; ++nt) {
                 uint32_t h[4];
                 e2m1x8_f16(y == 0 ? kw[nt].x : y == 1 ? kw[nt].y : y == 2 ? kw[nt].z : kw[nt].w, h);
                 const uint32_t f = y < 2 ? f0[nt] : f1[nt];
                 mma_f16(c[nt], qf[2 * y], mul_f16x2(h[0], f), mul_f16x2(h[1], f));
                 mma_f16(c[nt], qf[2 * y + 1], mul_f16x2(h[2], f), mul_f16x2(h[3], f));
               }
-            // values: thread g takes dims 16 g .. + 15 (one scale group) of its tokens
+          }
+          // the value codes, where registers allow before the softmax needs
+          // the scores: as the products below take them
+          uint32_t vraw[kEarly ? 16 * Y : 1], vsf[kEarly ? Y : 1];
+          auto read_v = [&](int y, uint32_t *w, uint32_t &f4) {
+            if constexpr (FMT == 0) {  // a page of values is [128 dims][16 tokens]
+              const uint32_t vat = smem_u32(st) + St::kV + ((k0 >> 4) + y) * 2048 + lane * 16;
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
+              for (int q4 = 0; q4 < 4; ++q4) {
+                uint32_t r[4];
+                ldsm_x4(vat + q4 * 512, r);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) w[4 * q4 + n] = r[n];
+              }
+            } else {  // thread g takes dims 16 g .. + 15 (one scale group) of its tokens
               const int quad = k0 + 16 * y + 4 * t, in = quad & (pt - 1);
               const uint8_t *vp = st + (quad - in) * 144 + pt * 72;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const uint2 w2 = *reinterpret_cast<const uint2 *>(vp + (in + ((e + t) & 3)) * 64 + 8 * g);
-                vraw[16 * y + 2 * e] = w2.x, vraw[16 * y + 2 * e + 1] = w2.y;
+                w[2 * e] = w2.x, w[2 * e + 1] = w2.y;
               }
-              const uint32_t f4 = *reinterpret_cast<const uint32_t *>(vp + pt * 64 + in * 8 + 4 * g);
-              vsf[y] = __funnelshift_r(f4, f4, 8 * t);
-            }
-          }
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                sv[hh][4 * y + e] = c[2 * y][2 * hh + e], sv[hh][4 * y + 2 + e] = c[2 * y + 1][2 * hh + e];
-          // x = score - reference (in log2 units, lifted by kAtLift): at most
-          // kAtLift + kAtSlack while the reference holds
-          f32x2 ksc[2][4], vs2[4];  // the score's factor of [head][pair of keys]; the pair's V scales
-          if constexpr (FMT == 0) {
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const float4 k4 = *reinterpret_cast<const float4 *>(st + St::kKs + (k0 + 16 * y + 4 * t) * 4);
-              const float4 v4 = *reinterpret_cast<const float4 *>(st + St::kVs + (k0 + 16 * y + 4 * t) * 4);
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-                ksc[hh][2 * y] = mul2(pack2(k4.x, k4.y), pack2(sc[hh], sc[hh]));
-                ksc[hh][2 * y + 1] = mul2(pack2(k4.z, k4.w), pack2(sc[hh], sc[hh]));
-              }
-              vs2[2 * y] = pack2(v4.x, v4.y), vs2[2 * y + 1] = pack2(v4.z, v4.w);
-            }
-          } else {
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) ksc[hh][k] = pack2(sc[hh], sc[hh]);
-          }
-          if (cut) {  // keys after the row's position: no score, no value (whatever the cache holds there)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int left = p - info.x * 128 - k0 - 16 * y - 4 * t;  // the last of the four keys that counts
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if ((FMT == 0 ? e : (e + t) & 3) > left) {
-                  sv[0][4 * y + e] = sv[1][4 * y + e] = -INFINITY;
-                  if constexpr (FMT == 0) {
-                    auto put = [&](f32x2 &d, float x) {
-                      const float2 u = unpack2(d);
-                      d = e & 1 ? pack2(u.x, x) : pack2(x, u.y);
-                    };
-                    put(ksc[0][2 * y + (e >> 1)], 1.f), put(ksc[1][2 * y + (e >> 1)], 1.f);
-                    put(vs2[2 * y + (e >> 1)], 0.f);
-#pragma unroll
-                    for (int n = 0; n < 16; ++n) vraw[16 * y + n] &= ~(0xffu << (8 * e));
-                  } else {
-                    vraw[16 * y + 2 * e] = vraw[16 * y + 2 * e + 1] = 0u;
-                    vsf[y] &= ~(0xffu << (8 * e));
-                  }
-                }
-            }
-          }
-          f32x2 x[2][4];
-          float top[2], vtop = 0.f;
-          auto scores = [&]() {
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const float off = mref[hh] == -INFINITY ? 0.f : kAtLift - mref[hh];
-              top[hh] = -INFINITY;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                x[hh][k] = fma2(pack2(sv[hh][2 * k], sv[hh][2 * k + 1]), ksc[hh][k], pack2(off, off));
-                const float2 u = unpack2(x[hh][k]);
-                top[hh] = fmaxf(top[hh], fmaxf(u.x, u.y));
-              }
+              f4 = *reinterpret_cast<const uint32_t *>(vp + pt * 64 + in * 8 + 4 * g);
             }
           };
-          scores();
+          if constexpr (kEarly)
+#pragma unroll
+            for (int y = 0; y < Y; ++y) read_v(y, vraw + 16 * y, vsf[y]);
+          // x = score - reference (in log2 units, lifted by kAtLift: at most
+          // kAtLift + kAtSlack while the reference holds; the score itself
+          // while there is none), pairs of keys
+          f32x2 x[2][2 * Y], vs2[2 * Y];
+          float off[2];
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) off[hh] = mref[hh] == -INFINITY ? 0.f : kAtLift - mref[hh];
+#pragma unroll
+          for (int y = 0; y < Y; ++y) {
+            f32x2 ks[2];
+            if constexpr (FMT == 0) {
+              const float4 k4 = *reinterpret_cast<const float4 *>(st + St::kKs + (k0 + 16 * y + 4 * t) * 4);
+              const float4 v4 = *reinterpret_cast<const float4 *>(st + St::kVs + (k0 + 16 * y + 4 * t) * 4);
+              ks[0] = pack2(k4.x, k4.y), ks[1] = pack2(k4.z, k4.w);
+              vs2[2 * y] = pack2(v4.x, v4.y), vs2[2 * y + 1] = pack2(v4.z, v4.w);
+            }
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                f32x2 f = pack2(sc[hh], sc[hh]);
+                if constexpr (FMT == 0) f = mul2(f, ks[u]);
+                x[hh][2 * y + u] = fma2(pack2(c[2 * y + u][2 * hh], c[2 * y + u][2 * hh + 1]), f, pack2(off[hh], off[hh]));
+              }
+          }
+          auto last_of = [&](int y) { return p - info.x * 128 - k0 - 16 * y - 4 * t; };  // of four keys, the last that counts
+          auto mask_v = [&](int left, uint32_t *w, uint32_t &f4) {
+            const uint32_t keep = left >= 3 ? 0xffffffffu : left < 0 ? 0u : (256u << (8 * left)) - 1u;
+            if constexpr (FMT == 0) {
+#pragma unroll
+              for (int n = 0; n < 16; ++n) w[n] &= keep;
+            } else {
+              f4 &= keep;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (((e + t) & 3) > left) w[2 * e] = w[2 * e + 1] = 0u;
+            }
+          };
+          if (cut) {  // keys after the row's position: no weight, no value (whatever the cache holds there)
+#pragma unroll
+            for (int y = 0; y < Y; ++y) {
+              const int left = last_of(y);
+              if constexpr (kEarly) mask_v(left, vraw + 16 * y, vsf[y]);
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const bool ok0 = (FMT == 0 ? 2 * u : (2 * u + t) & 3) <= left, ok1 = (FMT == 0 ? 2 * u + 1 : (2 * u + 1 + t) & 3) <= left;
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                  const float2 z = unpack2(x[hh][2 * y + u]);
+                  x[hh][2 * y + u] = pack2(ok0 ? z.x : -INFINITY, ok1 ? z.y : -INFINITY);
+                }
+                if constexpr (FMT == 0) {
+                  const float2 z = unpack2(vs2[2 * y + u]);
+                  vs2[2 * y + u] = pack2(ok0 ? z.x : 0.f, ok1 ? z.y : 0.f);
+                }
+              }
+            }
+          }
+          float top[2], vtop = 0.f;
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            top[hh] = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 2 * Y; ++k) {
+              const float2 u = unpack2(x[hh][k]);
+              top[hh] = fmaxf(top[hh], fmaxf(u.x, u.y));
+            }
+          }
           // the reference (and the V unit) move only when a score (a V scale)
           // has outgrown them, or there is none yet
           bool grow = top[0] > glimit[0] || top[1] > glimit[1];
           if constexpr (FMT == 0) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 2 * Y; ++k) {
               const float2 u = unpack2(vs2[k]);
               vtop = fmaxf(vtop, fmaxf(fabsf(u.x), fabsf(u.y)));
             }
@@ -412,28 +416,31 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
             }
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              const float was = mref[hh], tm = quad_max(top[hh]);  // the quad's largest score is tm, less the lift
+              const float was = mref[hh], tm = quad_max(top[hh]);
               const float now = was == -INFINITY ? tm : was + (tm - kAtLift);
               const float nm = fmaxf(was, now);
               const float al = nm == was ? 1.f : ex2_approx(was - nm);
+              const float by = nm == was ? 0.f : was == -INFINITY ? kAtLift - nm : was - nm;
+#pragma unroll
+              for (int k = 0; k < 2 * Y; ++k) x[hh][k] = add2(x[hh][k], pack2(by, by));
               mref[hh] = nm;
               glimit[hh] = nm == -INFINITY ? -INFINITY : kAtLift + kAtSlack;
               l[hh] *= al;
 #pragma unroll
               for (int n = 0; n < 16; ++n) o[n][2 * hh] *= al * f, o[n][2 * hh + 1] *= al * f;
             }
-            scores();
           }
-          uint32_t pa[2][4];
+          uint32_t pa[Y][4];
+          const float unit = FMT == 0 ? pow2i(-ev) : 1.f;
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             f32x2 sum = pack2(0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 2 * Y; ++k) {
               const float2 u = unpack2(x[hh][k]);
               f32x2 w = pack2(ex2_approx(u.x), ex2_approx(u.y));
               sum = add2(sum, w);
-              if constexpr (FMT == 0) w = mul2(w, mul2(vs2[k], pack2(pow2i(-ev), pow2i(-ev))));
+              if constexpr (FMT == 0) w = mul2(w, mul2(vs2[k], pack2(unit, unit)));
               const float2 r = unpack2(w);
               pa[k >> 1][(k & 1) * 2 + hh] = f16x2_bits(r.x, r.y);
             }
@@ -442,17 +449,22 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
           }
           // o += weights . values
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
+          for (int y = 0; y < Y; ++y) {
+            uint32_t late[kEarly ? 1 : 16], late_sf = 0;
+            if constexpr (!kEarly) read_v(y, late, late_sf);
+            uint32_t *w = kEarly ? vraw + 16 * y : late;
+            uint32_t f4 = kEarly ? vsf[y] : late_sf;
+            if constexpr (!kEarly)
+              if (cut) mask_v(last_of(y), w, f4);
             if constexpr (FMT == 0) {
 #pragma unroll
               for (int n = 0; n < 16; ++n) {
-                const uint2 v2 = e4m3x4_f16(vraw[16 * y + n]);
+                const uint2 v2 = e4m3x4_f16(w[n]);
                 mma_f16(o[n], pa[y], v2.x, v2.y);
               }
             } else {
               // nibbles of two tokens are paired before the conversion
-              const uint2 f = e4m3x4_f16(vsf[y]);
-              const uint32_t *w = vraw + 16 * y;
+              const uint2 f = e4m3x4_f16(__funnelshift_r(f4, f4, 8 * t));
 #pragma unroll
               for (int z = 0; z < 2; ++z) {
                 constexpr uint32_t kLow = 0x0f0f0f0fu;
@@ -683,35 +695,42 @@ static cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cud
   if (!attn_maps(&maps, a0, FMT)) return cudaErrorInvalidValue;
   CacheAttnParams a = a0;
   using Kern = void (*)(const AttnMaps, const CacheAttnParams);
-  Kern kern = pa_attn_kernel<FMT, 1, false>, clustered = pa_attn_kernel<FMT, 1, true>;
-  int smem = AttnSmem<FMT, 1>::kBytes;
-  if (a.rows_per == 1) kern = pa_attn_kernel<FMT, 8, false>, clustered = pa_attn_kernel<FMT, 8, true>, smem = AttnSmem<FMT, 8>::kBytes;
-  else if (a.rows_per == 2) kern = pa_attn_kernel<FMT, 4, false>, clustered = pa_attn_kernel<FMT, 4, true>, smem = AttnSmem<FMT, 4>::kBytes;
-  else if (a.rows_per <= 4) kern = pa_attn_kernel<FMT, 2, false>, clustered = pa_attn_kernel<FMT, 2, true>, smem = AttnSmem<FMT, 2>::kBytes;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), smem);
-  if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void *>(clustered), smem);
-  if (e != cudaSuccess) return e;
+  struct Variant {
+    Kern kern;
+    int smem;
+  };
+  static const Variant kSliced[4] = {{pa_attn_kernel<FMT, 8, false>, AttnSmem<FMT, 8>::kBytes},
+                                     {pa_attn_kernel<FMT, 4, false>, AttnSmem<FMT, 4>::kBytes},
+                                     {pa_attn_kernel<FMT, 2, false>, AttnSmem<FMT, 2>::kBytes},
+                                     {pa_attn_kernel<FMT, 1, false>, AttnSmem<FMT, 1>::kBytes}};
+  static const Variant kClustered[4] = {{pa_attn_kernel<FMT, 8, true>, AttnSmem<FMT, 8>::kBytes},
+                                        {pa_attn_kernel<FMT, 4, true>, AttnSmem<FMT, 4>::kBytes},
+                                        {pa_attn_kernel<FMT, 2, true>, AttnSmem<FMT, 2>::kBytes},
+                                        {pa_attn_kernel<FMT, 1, true>, AttnSmem<FMT, 1>::kBytes}};
   const int variant = a.rows_per == 1 ? 0 : a.rows_per == 2 ? 1 : a.rows_per <= 4 ? 2 : 3;
-  static int regs[4] = {0, 0, 0, 0};  // of the four kernels at launch
-  if (regs[variant] == 0) {
-    cudaFuncAttributes at, ac;
-    e = cudaFuncGetAttributes(&at, reinterpret_cast<const void *>(kern));
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&ac, reinterpret_cast<const void *>(clustered));
-    if (e != cudaSuccess) return e;
-    regs[variant] = std::min(at.numRegs, ac.numRegs);
-  }
-  if (regs[variant] * kAtThreads < 32 * kAtWarps * kAtComputeRegs + (kAtThreads - 32 * kAtWarps) * kAtProducerRegs)
-    return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
+  auto use = [&](const Variant &v, int &launch_regs) {  // its shared memory, and that it holds the registers it splits
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(v.kern), v.smem);
+    if (e == cudaSuccess && launch_regs == 0) {
+      cudaFuncAttributes at;
+      e = cudaFuncGetAttributes(&at, reinterpret_cast<const void *>(v.kern));
+      if (e == cudaSuccess) launch_regs = at.numRegs;
+    }
+    if (e == cudaSuccess &&
+        launch_regs * kAtThreads < 32 * kAtWarps * kAtComputeRegs + (kAtThreads - 32 * kAtWarps) * kAtProducerRegs)
+      e = cudaErrorInvalidConfiguration;
+    cfg.blockDim = dim3(kAtThreads);
+    cfg.dynamicSmemBytes = v.smem;
+    return e;
+  };
+  static int regs[2][4];  // of the kernels at launch
+  cudaError_t e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  cfg.gridDim = dim3(a.mode == kAtSliced ? sms : a.items);
-  cfg.blockDim = dim3(kAtThreads);
-  cfg.dynamicSmemBytes = smem;
   if (a.mode == kAtSliced) {
     // a cluster an item where all of them are resident at once and a CTA's
     // share of an item is short: then the scan and the second kernel cost
@@ -722,6 +741,8 @@ static cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cud
     static int resident[4][64][kAtMaxSplit + 1];  // clusters of a size, by device; -1: none
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    const Variant &v = kClustered[variant];
+    if ((e = use(v, regs[1][variant])) != cudaSuccess) return e;
     for (int n = std::min(kAtMaxSplit, longest); n >= 2 && dev < 64; --n) {
       if (a.items * n > sms || (longest + n - 1) / n > kAtClusterBlocks) continue;
       int &held = resident[variant][dev][n];
@@ -730,22 +751,21 @@ static cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cud
         cfg.gridDim = dim3(n);
         cfg.numAttrs = 2;
         int k = 0;
-        held = cudaOccupancyMaxActiveClusters(&k, clustered, &cfg) == cudaSuccess && k > 0 ? k : -1;
+        held = cudaOccupancyMaxActiveClusters(&k, v.kern, &cfg) == cudaSuccess && k > 0 ? k : -1;
       }
       if (held >= a.items) {
         a.mode = kAtCluster;
         a.split = n;
         cfg.gridDim = dim3(a.items * n);
         cfg.numAttrs = 2;
-        return cudaLaunchKernelEx(&cfg, clustered, maps, a);
+        return cudaLaunchKernelEx(&cfg, v.kern, maps, a);
       }
     }
-    cfg.gridDim = dim3(sms);
     cfg.numAttrs = 1;
   }
-  // several rows an item: the kernel that converts a block once for all rows
-  if (a.rows_per > 1 && a.bt_width <= kTcMaxWidth) e = launch_attn_tc(FMT, maps, a, (int)cfg.gridDim.x, pdl, stream);
-  else e = cudaLaunchKernelEx(&cfg, kern, maps, a);
+  if ((e = use(kSliced[variant], regs[0][variant])) != cudaSuccess) return e;
+  cfg.gridDim = dim3(a.mode == kAtSliced ? sms : a.items);
+  e = cudaLaunchKernelEx(&cfg, kSliced[variant].kern, maps, a);
   if (e != cudaSuccess || a.mode != kAtSliced || a.test_timeout) return e;
   // few items: many partials each, a CTA a head; else a warp a head
   const bool many = a.items * 8 <= sms;
