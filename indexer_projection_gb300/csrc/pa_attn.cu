@@ -51,13 +51,26 @@ struct AttnShared : AttnRing<ROWS> {
   float2 ml[kAtWarps / 2][16];
 };
 
-template <int FMT, int WPR>
+// A warp takes 16 Y keys at a time and at least those of a block; a row's
+// warps beyond that take alternate entries of the ring, in kGroups groups.
+// (64 keys a step were 7% faster than 32 for FP8 rows that share a CTA, slower
+// for NVFP4, whose codes then cannot be read ahead of the softmax.)
+template <int FMT, int WPR, bool CLUSTER>
+struct AttnSplit {
+  static constexpr int Y = FMT == 0 && !CLUSTER && WPR < 8 ? 4 : 2, kMost = 128 / (16 * Y);
+  static constexpr int kParts = WPR > kMost ? kMost : WPR, kGroups = WPR / kParts, kKeys = 128 / kParts;
+};
+
+template <int FMT, int WPR, bool CLUSTER>
 struct AttnSmem {  // stages, then the queries, the buffer where a row's warps meet, the rest
   static constexpr int kRows = kAtWarps / WPR, kQ = kRows * 16 * kHeadDim * 2, kJoint = WPR > 1 ? 4 * 8192 : 0;
   using Shared = AttnShared<kRows>;
   static constexpr int kRest = kQ + kJoint + (int)sizeof(Shared) + 128;
   static constexpr int kFit = (kAtSmem - kRest) / AttnStage<FMT>::kBytes;
-  static constexpr int kStages = kFit < kAtMaxStages ? kFit : kAtMaxStages;
+  // a stage belongs to one group, which sees each of its phases (a wait names
+  // a phase by its parity alone)
+  static constexpr int kGroups = AttnSplit<FMT, WPR, CLUSTER>::kGroups;
+  static constexpr int kStages = (kFit < kAtMaxStages ? kFit : kAtMaxStages) / kGroups * kGroups;
   static constexpr int kBytes = kStages * AttnStage<FMT>::kBytes + kRest;
 };
 
@@ -110,14 +123,13 @@ template <int FMT, int WPR, bool CLUSTER>  // CLUSTER: mode kAtCluster
 __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_constant__ AttnMaps maps,
                                                                 const __grid_constant__ CacheAttnParams a) {
   using St = AttnStage<FMT>;
-  using Sm = AttnSmem<FMT, WPR>;
+  using Sm = AttnSmem<FMT, WPR, CLUSTER>;
+  using Sp = AttnSplit<FMT, WPR, CLUSTER>;
   static_assert(Sm::kBytes <= kAtSmem && Sm::kStages >= 3, "shared memory of a CTA");
   constexpr int kStages = Sm::kStages;
-  // a warp takes 16 Y keys at a time and at least those of a block: a row's
-  // warps beyond that take alternate blocks
-  constexpr int Y = CLUSTER || FMT == 1 ? 2 : 4, kMost = 128 / (16 * Y);
+  constexpr int Y = Sp::Y, kParts = Sp::kParts, kGroups = Sp::kGroups, kKeys = Sp::kKeys;
   constexpr bool kEarly = Y == 2;
-  constexpr int kParts = WPR > kMost ? kMost : WPR, kGroups = WPR / kParts, kKeys = 128 / kParts;
+  static_assert(Sm::kStages >= 2 * kGroups, "two stages a group");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
   uint8_t *q_smem = ring + kStages * St::kBytes;  // [row][group][128], as q holds them
@@ -130,7 +142,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.empty[s], kAtWarps);
+      mbar_init(&sh.empty[s], kAtWarps / kGroups);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh.batch_full[s], 1);
@@ -147,7 +159,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
   if (sl.none) return;
   if (warp >= kAtWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtProducerRegs));
-    if (warp == kAtWarps && lane == 0) attn_copies<FMT, kStages>(a, maps, sh, sl, ring, q_smem);
+    if (warp == kAtWarps && lane == 0) attn_copies<FMT, kStages, kGroups>(a, maps, sh, sl, ring, q_smem);
     if (warp == kAtWarps + 1) attn_resolve<FMT>(a, sh, sl, mode);
     return;
   }
@@ -157,7 +169,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
   const int row = warp / WPR, part = warp % WPR;
   const int key0 = part % kParts * kKeys;
   const int pt = min(a.bs, 128);  // NVFP4: tokens a piece of a stage
-  int j = 0;
+  // the warp's next entry: its number, stage and phase, and whether it is
+  // known to be there (asked for while the one before is worked on)
+  int next = kGroups > 1 ? part / kParts : 0, stage = next;
+  uint32_t phase = 0;
+  bool ready = false;
+  auto peek = [&]() { ready = __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.full[stage]), phase)); };
   uint32_t nq = 0, fin_phase = 0;
   auto fin_sync = [&]() {  // all compute warps; bounded
     __syncwarp();
@@ -232,14 +249,22 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     float glimit[2] = {-INFINITY, -INFINITY};  // the reference moves when a lifted score is above
     int ev = -126;  // FP8: o is in units of 2^ev, V scales up to 2^(ev + 1) = vlimit
     float vlimit = pow2i(-125);
+    if (a.test_timeout) {
+      const bool got = mbar_wait(&sh.never, 0, a.status, a.lim);
+      if (!__all_sync(0xffffffffu, got)) return;
+    }
     while (true) {
-      const int s = j % kStages;
-      bool got = mbar_wait(&sh.full[s], (uint32_t)(j / kStages) & 1, a.status, a.lim);
-      if (got && a.test_timeout) got = mbar_wait(&sh.never, 0, a.status, a.lim);
-      if (!__all_sync(0xffffffffu, got)) return;  // the warp gives up; the others' waits are bounded too
-      const int2 info = sh.info[j % kAtInfo];
-      ++j;
-      if (info.x >= 0 && ((info.y >> row) & 1) && (kGroups == 1 || j % kGroups == part / kParts)) {
+      if (!ready) {
+        const bool got = mbar_wait(&sh.full[stage], phase, a.status, a.lim);
+        if (!__all_sync(0xffffffffu, got)) return;  // the warp gives up; the others' waits are bounded too
+      }
+      ready = false;
+      const int s = stage;
+      const int2 info = sh.info[next % kAtInfo];
+      next += kGroups;
+      stage += kGroups;
+      if (stage >= kStages) stage -= kStages, phase ^= 1u;
+      if (info.x >= 0 && ((info.y >> row) & 1)) {
         const uint8_t *st = ring + s * St::kBytes;
         const bool cut = info.x * 128 + 127 > p;  // keys after the row's position
 #pragma unroll 1
@@ -447,6 +472,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
             const float2 u = unpack2(sum);
             l[hh] += u.x + u.y;
           }
+          peek();
           // o += weights . values
 #pragma unroll
           for (int y = 0; y < Y; ++y) {
@@ -699,14 +725,14 @@ static cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cud
     Kern kern;
     int smem;
   };
-  static const Variant kSliced[4] = {{pa_attn_kernel<FMT, 8, false>, AttnSmem<FMT, 8>::kBytes},
-                                     {pa_attn_kernel<FMT, 4, false>, AttnSmem<FMT, 4>::kBytes},
-                                     {pa_attn_kernel<FMT, 2, false>, AttnSmem<FMT, 2>::kBytes},
-                                     {pa_attn_kernel<FMT, 1, false>, AttnSmem<FMT, 1>::kBytes}};
-  static const Variant kClustered[4] = {{pa_attn_kernel<FMT, 8, true>, AttnSmem<FMT, 8>::kBytes},
-                                        {pa_attn_kernel<FMT, 4, true>, AttnSmem<FMT, 4>::kBytes},
-                                        {pa_attn_kernel<FMT, 2, true>, AttnSmem<FMT, 2>::kBytes},
-                                        {pa_attn_kernel<FMT, 1, true>, AttnSmem<FMT, 1>::kBytes}};
+  static const Variant kSliced[4] = {{pa_attn_kernel<FMT, 8, false>, AttnSmem<FMT, 8, false>::kBytes},
+                                     {pa_attn_kernel<FMT, 4, false>, AttnSmem<FMT, 4, false>::kBytes},
+                                     {pa_attn_kernel<FMT, 2, false>, AttnSmem<FMT, 2, false>::kBytes},
+                                     {pa_attn_kernel<FMT, 1, false>, AttnSmem<FMT, 1, false>::kBytes}};
+  static const Variant kClustered[4] = {{pa_attn_kernel<FMT, 8, true>, AttnSmem<FMT, 8, true>::kBytes},
+                                        {pa_attn_kernel<FMT, 4, true>, AttnSmem<FMT, 4, true>::kBytes},
+                                        {pa_attn_kernel<FMT, 2, true>, AttnSmem<FMT, 2, true>::kBytes},
+                                        {pa_attn_kernel<FMT, 1, true>, AttnSmem<FMT, 1, true>::kBytes}};
   const int variant = a.rows_per == 1 ? 0 : a.rows_per == 2 ? 1 : a.rows_per <= 4 ? 2 : 3;
   cudaLaunchConfig_t cfg = {};
   auto use = [&](const Variant &v, int &launch_regs) {  // its shared memory, and that it holds the registers it splits

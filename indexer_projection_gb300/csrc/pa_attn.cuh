@@ -369,9 +369,10 @@ __device__ __forceinline__ void attn_resolve(const CacheAttnParams &a, S &sh, co
   }
 }
 
-// One thread: an item's queries when its first batch comes, then a
-// stage a block, each segment ended by an entry without a block.
-template <int FMT, int kStages, class S>
+// One thread: an item's queries when its first batch comes, then a stage a
+// block; kGroups groups of readers take the entries in turn, and each segment
+// ends with an entry without a block for each of them.
+template <int FMT, int kStages, int kGroups, class S>
 __device__ __forceinline__ void attn_copies(const CacheAttnParams &a, const AttnMaps &maps, S &sh, const AttnSlice &sl,
                                             uint8_t *ring, uint8_t *q_smem) {
   using St = AttnStage<FMT>;
@@ -424,10 +425,13 @@ __device__ __forceinline__ void attn_copies(const CacheAttnParams &a, const Attn
     }
     if (!ok) break;
     if (bt.last) {
-      if (!(ok = acquire())) break;
-      sh.info[j % kAtInfo] = make_int2(-1, 0);
-      mbar_arrive(&sh.full[j % kStages]);
-      ++j;
+      for (int k = 0; k < kGroups && ok; ++k) {  // an entry for each group of readers
+        if (!(ok = acquire())) break;
+        sh.info[j % kAtInfo] = make_int2(-1, 0);
+        mbar_arrive(&sh.full[j % kStages]);
+        ++j;
+      }
+      if (!ok) break;
       ++it;
     }
     mbar_arrive(&sh.batch_empty[nbt & 1]);

@@ -45,7 +45,7 @@ struct Index4Params {
 };
 
 template <int NT>  // n8 tiles of query rows: q_len <= 8 * NT
-__global__ void __launch_bounds__(32 * kI4Warps, NT == 1 ? 6 : 4) pa_index_scores_nvfp4_kernel(const __grid_constant__ Index4Params a) {
+__global__ void __launch_bounds__(32 * kI4Warps, NT == 1 ? 5 : 4) pa_index_scores_nvfp4_kernel(const __grid_constant__ Index4Params a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int r = blockIdx.y, unit = blockIdx.x * kI4Warps + warp;

@@ -40,7 +40,7 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) pa_select_kernel(const __grid_constant__ SelectParams a) {
+__global__ void __launch_bounds__(kSelThreads, 6) pa_select_kernel(const __grid_constant__ SelectParams a) {
   extern __shared__ uint32_t keys[];  // [bt_width], of the cluster's first CTA
   __shared__ uint32_t hist[2][256];
   __shared__ int3 pick;               // the digit found, what remains to take in it, what it holds
