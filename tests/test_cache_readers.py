@@ -299,6 +299,94 @@ def test_offsets_beyond_32_bits():
     close(got, want)
 
 
+@pytest.mark.parametrize("fmt,R,q_len,nkv,topk", [("fp8", 48, 1, 2, 0), ("nvfp4", 24, 1, 4, 0), ("fp8", 12, 7, 2, 0),
+                                                  ("nvfp4", 12, 4, 2, 0), ("fp8", 64, 7, 2, 16), ("nvfp4", 64, 6, 2, 16),
+                                                  ("fp8", 200, 2, 1, 12)])
+def test_many_blocks_a_cta(fmt, R, q_len, nkv, topk):
+    """Enough blocks that every CTA's ring goes round many times, ragged requests; the reference in 64 bits on the GPU."""
+    from indexer_projection_gb300 import binding as B
+    from indexer_projection_gb300.runner import CacheReader, PreAttn
+
+    g = torch.Generator(device="cuda").manual_seed(R + q_len)
+    dev, D = "cuda", 128
+    seq = torch.randint(q_len, 20000, (R,), generator=g, device=dev, dtype=torch.int32)
+    W = (20000 + 127) // 128
+    nb = (seq + 127) // 128
+    pool = int(nb.sum())
+    perm = torch.randperm(pool, generator=g, device=dev).to(torch.int32)
+    bt = torch.full((R, W), -1, dtype=torch.int32, device=dev)
+    bt[torch.arange(W, device=dev) < nb[:, None]] = perm
+    q = (torch.randn(R * q_len, nkv * 16 * D, generator=g, device=dev) * 0.5).to(torch.bfloat16)
+    e4m3 = torch.from_numpy(np.nan_to_num(ref.E4M3)).to(dev)
+    slots = pool * 128
+    s_ = torch.arange(slots, device=dev)[:, None]
+    d = torch.arange(D, device=dev)
+    if fmt == "fp8":
+        code = [torch.randint(0, 0x70, (slots // 16 * nkv * 2048,), generator=g, device=dev, dtype=torch.uint8) for _ in "kv"]
+        for x in code:
+            x |= torch.randint(0, 2, x.shape, generator=g, device=dev, dtype=torch.uint8) << 7
+        scale = [torch.rand(slots // 16 * nkv * 16, generator=g, device=dev) * 0.02 + 0.001 for _ in "kv"]
+        caches, form, bs = PreAttn.fp8_caches(*code, *scale, None, slots // 16, 0), B.PA_CACHE_FP8, 16
+
+        def kv(h, slot):
+            p, t = (slot // 16 * nkv + h)[:, None], (slot % 16)[:, None]
+            k = e4m3[code[0][p * 2048 + d // 16 * 256 + t * 16 + d % 16].long()] * scale[0][p * 16 + t].double()
+            return k, e4m3[code[1][p * 2048 + d * 16 + t].long()] * scale[1][p * 16 + t].double()
+    else:
+        bs = 32
+        page = 2 * nkv * bs * 72
+        cache = torch.randint(0, 256, (slots // bs, page), generator=g, device=dev, dtype=torch.uint8)
+        sf = cache.view(slots // bs, 2 * nkv, bs * 72)[:, :, bs * 64:]
+        sf.copy_(torch.randint(0x20, 0x38, sf.shape, generator=g, device=dev, dtype=torch.uint8))
+        caches, form = PreAttn.nvfp4_caches(cache, slots // bs, page, None, 0, 0), B.PA_CACHE_NVFP4
+        flat, e2m1 = cache.view(-1), torch.from_numpy(ref.E2M1).to(dev)
+
+        def kv(h, slot):
+            out = []
+            for sl in (2 * h, 2 * h + 1):
+                base, t, grp = (slot // bs * page + sl * bs * 72)[:, None], (slot % bs)[:, None], d // 16
+                byte = flat[base + t * 64 + d // 2].long()
+                at = (t // 4 * 4 + grp // 2) * 8 + grp % 2 * 4 + t % 4 if sl % 2 else t * 8 + grp
+                out.append(e2m1[torch.where(d % 2 == 0, byte & 15, byte >> 4)] * e4m3[flat[base + bs * 64 + at].long()])
+            return out
+    rd = CacheReader(16 * nkv, nkv, cache_format=form, caches=caches, max_requests=R, q_len=q_len, bt_width=W, topk=topk,
+                     block_size=bs)
+    kw = {}
+    if topk:
+        pos = (seq.long()[:, None] - q_len + torch.arange(q_len, device=dev)).view(-1, 1, 1)
+        order = torch.rand(R * q_len, nkv, W, generator=g, device=dev)
+        order[:, :, :4] += 1  # blocks that most rows share
+        order = torch.where(torch.arange(W, device=dev) <= pos // 128, order, -1.0)
+        val, top = order.topk(topk, dim=-1)
+        kw["blocks"] = torch.where(val >= 0, top, -1).to(torch.int32)
+        kw["counts"] = (val >= 0).sum(-1).to(torch.int32)
+    outs = []
+    for _ in range(3):
+        out = torch.full((R * q_len, nkv * 16 * D), float("nan"), dtype=torch.bfloat16, device=dev)
+        rd.attend(q, bt, seq, out, **kw)
+        outs.append(out)
+    torch.cuda.synchronize()
+    assert rd.device_status() == 0
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    for r in range(R):
+        n = int(seq[r])
+        j = torch.arange(n, device=dev)
+        slot = bt[r, j // 128].long() * 128 + j % 128
+        for h in range(nkv):
+            k, v = kv(h, slot)
+            for i in range(q_len):
+                m = r * q_len + i
+                live = j <= n - q_len + i
+                if topk:
+                    live = live & torch.isin(j // 128, kw["blocks"][m, h].long())
+                w = torch.softmax(q[m].view(nkv, 16, D)[h].double() @ k[live].T * D ** -0.5, -1)
+                want, mass = w @ v[live], w @ v[live].abs()
+                # as ref.Case.attention's bound: 2^-11 a weight's rounding, 2^-8 the output's, the scores' errors below 2^-12
+                tol = 2.0 ** -10 * mass + 2.0 ** -8 * want.abs() + 1e-6 * v.abs().max()
+                got = outs[0][m].view(nkv, 16, D)[h].double()
+                assert ((got - want).abs() <= tol).all(), (r, h, i, float(((got - want).abs() - tol).max()))
+
+
 # ------------------------------------------------------------- the selection
 
 def run_select(scores, seq, q_len, init, local, topk, W):
