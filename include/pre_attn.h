@@ -571,7 +571,8 @@ typedef struct pa_attention_args {
   int block_size;             /* NVFP4: tokens a page (see above); FP8: 16 */
   int kv_page_stride;         /* FP8: page-16 pages a 128-token block, as in pa_config: 0 (8) or >= 8 */
   const pa_caches *caches;    /* host struct: the K / V fields of the format are read.  FP8: k_cache, v_cache, k_scale
-                                 and v_scale 16-byte aligned; NVFP4: kv_cache and kv_page_bytes multiples of 32 */
+                                 and v_scale 16-byte aligned; NVFP4: kv_cache and kv_page_bytes multiples of 32,
+                                 global scales > 0 and finite */
   const int32_t *block_table; /* [R, bt_width] page-128 block ids */
   const int32_t *seq_lens;    /* [R] keys of each request, its q_len rows' own included */
   const int32_t *blocks;      /* [R * q_len, n_kv_heads, topk], or NULL: every block */
@@ -581,7 +582,8 @@ typedef struct pa_attention_args {
   int q_len;                  /* 1 .. 16 */
   int bt_width;               /* 1 .. 16384 */
   float sm_scale;             /* > 0, finite */
-  void *out;                  /* [R * q_len, out_stride] bf16, 16-byte aligned; no overlap with q */
+  void *out;                  /* [R * q_len, out_stride] bf16, 16-byte aligned; the span of its rows
+                                 (first to last element) does not overlap that of q's */
   int64_t out_stride;         /* elements a row: a multiple of 8, >= n_q_heads * 128 */
   void *workspace;            /* pre_attn_attention_workspace_bytes() of scratch, 256-byte aligned; no initial
                                  contents needed; calls that share it must be ordered on the GPU */

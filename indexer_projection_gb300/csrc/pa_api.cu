@@ -135,7 +135,7 @@ const char *pre_attn_strerror(int s) {
     case PA_ERR_ALIGN: return "a pointer or stride violates its alignment rule";
     case PA_ERR_NO_Q_OUTPUT: return "no q output requested (need q and/or q_fp8)";
     case PA_ERR_NO_IQ_OUTPUT: return "no index_q output requested (need iq and/or iq_fp8)";
-    case PA_ERR_ALIAS: return "residual partially overlaps ar or res";
+    case PA_ERR_ALIAS: return "an output overlaps an input (residual: ar or res in part; attention: q)";
     case PA_ERR_WORKSPACE: return "workspace NULL or too small";
     case PA_ERR_CUDA: return "a CUDA runtime call failed";
     case PA_ERR_UNSUPPORTED: return "valid request not implemented by this build";

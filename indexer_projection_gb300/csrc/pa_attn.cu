@@ -29,6 +29,7 @@
 // stays in f16's normal range for keys whose weight is up to 2^-23 of the
 // largest.  The sum of the weights is taken in f32 before that rounding.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -183,12 +184,20 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     fin_phase ^= 1;
     return __all_sync(0xffffffffu, got) != 0;
   };
+  // A wait ran out: what this warp leaves out, the status tells.  The CTA stays
+  // until no other CTA of its cluster reads its shared memory.
+  auto give_up = [&]() {
+    if constexpr (CLUSTER) {
+      cluster_sync();
+      cluster_sync();
+    }
+  };
   int v0, v1, v;
   for (int it = sl.first; sl.segment(a, sh, it, v0, v1, v); ++it) {
     AttnItem x = attn_place(a, it);
     {
       const bool got = mbar_wait(&sh.q_full, nq & 1, a.status, a.lim);
-      if (!__all_sync(0xffffffffu, got)) return;
+      if (!__all_sync(0xffffffffu, got)) return give_up();
       ++nq;
     }
     x.first = sh.q_item.x, x.seq = sh.q_item.y;
@@ -251,12 +260,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     float vlimit = pow2i(-125);
     if (a.test_timeout) {
       const bool got = mbar_wait(&sh.never, 0, a.status, a.lim);
-      if (!__all_sync(0xffffffffu, got)) return;
+      if (!__all_sync(0xffffffffu, got)) return give_up();
     }
     while (true) {
       if (!ready) {
         const bool got = mbar_wait(&sh.full[stage], phase, a.status, a.lim);
-        if (!__all_sync(0xffffffffu, got)) return;  // the warp gives up; the others' waits are bounded too
+        if (!__all_sync(0xffffffffu, got)) return give_up();  // the warp gives up; the others' waits are bounded too
       }
       ready = false;
       const int s = stage;
@@ -550,7 +559,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
             for (int hh = 0; hh < 2; ++hh) box[(2 * n + hh) * 32] = make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
           if (t == 0) sh.ml[slot][g] = make_float2(mref[0], l[0]), sh.ml[slot][g + 8] = make_float2(mref[1], l[1]);
         }
-        if (!fin_sync()) return;
+        if (!fin_sync()) return give_up();
         if (part < half) {
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
@@ -568,14 +577,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
             }
           }
         }
-        if (!fin_sync()) return;
+        if (!fin_sync()) return give_up();
       }
     }
     const int64_t m = (int64_t)x.r * a.q_len + x.row0 + row;
     float *own = reinterpret_cast<float *>(ring);  // kAtCluster: [row][head][128], then (m, l); the stages are free
     if constexpr (CLUSTER) {
       if constexpr (WPR == 1)
-        if (!fin_sync()) return;  // (with more warps a row they have met above)
+        if (!fin_sync()) return give_up();  // (with more warps a row they have met above)
       pp = own;
     }
     if (part == 0 && row < x.rows) {
@@ -735,21 +744,22 @@ static cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cud
                                         {pa_attn_kernel<FMT, 1, true>, AttnSmem<FMT, 1, true>::kBytes}};
   const int variant = a.rows_per == 1 ? 0 : a.rows_per == 2 ? 1 : a.rows_per <= 4 ? 2 : 3;
   cudaLaunchConfig_t cfg = {};
-  auto use = [&](const Variant &v, int &launch_regs) {  // its shared memory, and that it holds the registers it splits
+  auto use = [&](const Variant &v, std::atomic<int> &launch_regs) {  // its shared memory, and that it holds the registers it splits
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(v.kern), v.smem);
-    if (e == cudaSuccess && launch_regs == 0) {
+    int regs = launch_regs.load(std::memory_order_relaxed);
+    if (e == cudaSuccess && regs == 0) {
       cudaFuncAttributes at;
       e = cudaFuncGetAttributes(&at, reinterpret_cast<const void *>(v.kern));
-      if (e == cudaSuccess) launch_regs = at.numRegs;
+      if (e == cudaSuccess) launch_regs.store(regs = at.numRegs, std::memory_order_relaxed);
     }
     if (e == cudaSuccess &&
-        launch_regs * kAtThreads < 32 * kAtWarps * kAtComputeRegs + (kAtThreads - 32 * kAtWarps) * kAtProducerRegs)
+        regs * kAtThreads < 32 * kAtWarps * kAtComputeRegs + (kAtThreads - 32 * kAtWarps) * kAtProducerRegs)
       e = cudaErrorInvalidConfiguration;
     cfg.blockDim = dim3(kAtThreads);
     cfg.dynamicSmemBytes = v.smem;
     return e;
   };
-  static int regs[2][4];  // of the kernels at launch
+  static std::atomic<int> regs[2][4];  // of the kernels at launch
   cudaError_t e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -764,20 +774,21 @@ static cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cud
     const int longest = a.topk ? std::min(a.bt_width, a.topk * a.rows_per) : a.bt_width;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    static int resident[4][64][kAtMaxSplit + 1];  // clusters of a size, by device; -1: none
+    static std::atomic<int> resident[4][64][kAtMaxSplit + 1];  // clusters of a size, by device; -1: none
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     const Variant &v = kClustered[variant];
     if ((e = use(v, regs[1][variant])) != cudaSuccess) return e;
     for (int n = std::min(kAtMaxSplit, longest); n >= 2 && dev < 64; --n) {
       if (a.items * n > sms || (longest + n - 1) / n > kAtClusterBlocks) continue;
-      int &held = resident[variant][dev][n];
+      int held = resident[variant][dev][n].load(std::memory_order_relaxed);
       attr[1].val.clusterDim.x = n;
       if (held == 0) {
         cfg.gridDim = dim3(n);
         cfg.numAttrs = 2;
         int k = 0;
         held = cudaOccupancyMaxActiveClusters(&k, v.kern, &cfg) == cudaSuccess && k > 0 ? k : -1;
+        resident[variant][dev][n].store(held, std::memory_order_relaxed);
       }
       if (held >= a.items) {
         a.mode = kAtCluster;
@@ -844,7 +855,9 @@ extern "C" int pre_attn_attention(const pa_attention_args *in, void *stream) {
     if (bs < 4 || bs % 4 || bs > 1024 || c.kv_pages < 1 || c.kv_pages > INT32_MAX) return PA_ERR_CONFIG;
     if (128 % bs && bs % 128) return PA_ERR_UNSUPPORTED;
     if (c.kv_page_bytes < (int64_t)2 * x.n_kv_heads * bs * 72) return PA_ERR_CONFIG;
-    if (!(c.k_global_scale > 0.0f) || !(c.v_global_scale > 0.0f)) return PA_ERR_CONFIG;
+    if (!(c.k_global_scale > 0.0f) || !(c.v_global_scale > 0.0f) || !std::isfinite(c.k_global_scale) ||
+        !std::isfinite(c.v_global_scale))
+      return PA_ERR_CONFIG;
     if (c.kv_page_bytes % 32 || !aligned(c.kv_cache, 32)) return PA_ERR_ALIGN;
   }
   if ((x.q && !aligned(x.q, 16)) || (x.q_fp8 && !aligned(x.q_fp8, 16)) || x.q_stride % 16 || !aligned(x.out, 16) ||
@@ -852,10 +865,11 @@ extern "C" int pre_attn_attention(const pa_attention_args *in, void *stream) {
       !aligned(x.counts, 4) || !aligned(x.status, 4))
     return PA_ERR_ALIGN;
   if (x.R == 0) return PA_OK;
-  const int64_t M = (int64_t)x.R * x.q_len;
+  const int64_t M = (int64_t)x.R * x.q_len, cols = (int64_t)x.n_q_heads * 128;
   {
     const uintptr_t q0 = reinterpret_cast<uintptr_t>(x.q ? x.q : x.q_fp8), o0 = reinterpret_cast<uintptr_t>(x.out);
-    const uintptr_t q1 = q0 + (uintptr_t)(M * x.q_stride) * (x.q ? 2 : 1), o1 = o0 + (uintptr_t)(M * x.out_stride) * 2;
+    const uintptr_t q1 = q0 + (uintptr_t)((M - 1) * x.q_stride + cols) * (x.q ? 2 : 1);
+    const uintptr_t o1 = o0 + (uintptr_t)((M - 1) * x.out_stride + cols) * 2;
     if (q0 < o1 && o0 < q1) return PA_ERR_ALIAS;
   }
   const int sms = pa::current_device_sms();

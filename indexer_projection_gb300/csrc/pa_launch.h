@@ -1,6 +1,8 @@
 // Host-side launchers of the pre-attention kernels (one per translation unit).
 #pragma once
 
+#include <mutex>
+
 #include <cuda_runtime.h>
 
 namespace pa {
@@ -21,9 +23,11 @@ inline cudaError_t ensure_smem_attr(const void *kern, int bytes) {
   };
   static Entry table[64];
   static int n = 0;
+  static std::mutex held;  // host threads may call at once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> guard(held);
   for (int i = 0; i < n; ++i)
     if (table[i].k == kern && table[i].dev == dev && table[i].bytes >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);

@@ -86,14 +86,16 @@ class CacheReader:
     selection and the attention, for up to ``max_requests`` requests of
     ``q_len`` rows whose block tables hold ``bt_width`` page-128 blocks.
 
-    ``caches`` is PreAttn.fp8_caches(...) or PreAttn.nvfp4_caches(...): the
-    fields that a call reads have to be set (the index cache for
-    ``index_scores``, the K / V ones for ``attend``) and their tensors kept
+    ``caches`` is PreAttn.fp8_caches(...) or PreAttn.nvfp4_caches(...), read at
+    every call: the fields that a call reads have to be set (the index cache
+    for ``index_scores``, the K / V ones for ``attend``) and their tensors kept
     alive by the caller.  Owns a workspace, a status word and the calls'
-    argument structs: one host thread uses a reader at a time, and its calls
-    are ordered on the GPU by their stream, or by the caller.  Every tensor is on
-    ``device``; seq_lens, block tables, block lists and counts are contiguous
-    int32, scores and query rows have contiguous columns.
+    argument structs: one host thread uses a reader at a time, and its calls,
+    replays of captured ones among them, are ordered on the GPU by their
+    stream, or by the caller (calls that may run together take a reader each).
+    Every tensor is on ``device``; seq_lens, block tables, block lists and
+    counts are contiguous int32, scores and query rows have contiguous columns.
+    A call without requests does nothing.
     """
 
     def __init__(self, n_q_heads: int, n_kv_heads: int, *, cache_format: int, caches: B.pa_caches, max_requests: int,
@@ -104,6 +106,7 @@ class CacheReader:
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self.index = self.device.index
         self.n_q_heads, self.n_kv_heads, self.cache_format, self.caches = n_q_heads, n_kv_heads, cache_format, caches
         self.max_requests, self.q_len, self.bt_width, self.topk = max_requests, q_len, bt_width, topk
         self.init_blocks, self.local_blocks, self.block_size = init_blocks, local_blocks, block_size
@@ -135,10 +138,9 @@ class CacheReader:
 
     def _on(self, stream):
         """The stream of a call: the reader's device has to be the current one."""
-        index = self.device.index
-        if torch.cuda.current_device() != index:
+        if torch.cuda.current_device() != self.index:
             raise ValueError(f"the current device is not the reader's ({self.device})")
-        return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream
+        return torch._C._cuda_getCurrentRawStream(self.index) if stream is None else stream
 
     def _requests(self, seq_lens, block_table=None) -> int:
         R = seq_lens.shape[0]
@@ -150,13 +152,15 @@ class CacheReader:
         return R
 
     def _ints(self, x, shape, name):
-        if x.dtype is not torch.int32 or x.shape != shape or not x.is_contiguous():
-            raise ValueError(f"{name}: a contiguous int32 tensor of shape {shape} is wanted")
+        if x.dtype is not torch.int32 or x.shape != shape or not x.is_contiguous() or x.get_device() != self.index:
+            raise ValueError(f"{name}: a contiguous int32 tensor of shape {shape} on {self.device} is wanted")
 
     def _rows(self, x, dtype_ok, rows, cols, name):
         shape, stride = x.shape, x.stride()
-        if not dtype_ok or len(shape) != 2 or shape[0] != rows or shape[1] < cols or stride[1] != 1:
-            raise ValueError(f"{name}: [{rows}, >= {cols}] with contiguous columns is wanted, not {x.dtype} {tuple(shape)}")
+        if (not dtype_ok or len(shape) != 2 or shape[0] != rows or shape[1] < cols or stride[1] != 1
+                or x.get_device() != self.index):
+            raise ValueError(f"{name}: [{rows}, >= {cols}] with contiguous columns on {self.device} is wanted, not "
+                             f"{x.dtype} {tuple(shape)} on {x.device}")
         return stride[0] if rows > 1 else cols  # elements a row (a single row's stride says nothing)
 
     def index_scores(self, iq, head: int, block_table, seq_lens, scores, *, scale: float | None = None, stream=None,
@@ -169,6 +173,13 @@ class CacheReader:
         a.iq, a.head, a.block_table, a.seq_lens = iq.data_ptr(), head, block_table.data_ptr(), seq_lens.data_ptr()
         a.R, a.scores = R, scores.data_ptr()
         a.index_scale = self.index_scale if scale is None else scale
+        c = self.caches
+        if self.cache_format == B.PA_CACHE_FP8:
+            a.index_cache, a.num_index_slots = c.index_cache, c.num_index_slots
+        else:
+            a.idx_cache, a.idx_pages, a.idx_page_bytes = c.idx_cache, c.idx_pages, c.idx_page_bytes
+        if R == 0:
+            return B.PA_OK
         return self._run_scores(a, self._on(stream), check)
 
     def select_blocks(self, scores, seq_lens, blocks, counts, *, stream=None, check: bool = True) -> int:
@@ -177,8 +188,8 @@ class CacheReader:
         M, shape, stride, a = R * self.q_len, scores.shape, scores.stride(), self._select
         width = self.bt_width * 128
         if (scores.dtype is not torch.float32 or len(shape) != 3 or shape[0] < 1 or shape[1] != M or shape[2] < width
-                or stride[2] != 1):
-            raise ValueError(f"scores: f32 [heads, {M}, >= {width}] with contiguous columns is wanted")
+                or stride[2] != 1 or scores.get_device() != self.index):
+            raise ValueError(f"scores: f32 [heads, {M}, >= {width}] with contiguous columns on {self.device} is wanted")
         heads = shape[0]
         self._ints(blocks, (M, heads, self.topk), "blocks")
         self._ints(counts, (M, heads), "counts")
@@ -186,6 +197,8 @@ class CacheReader:
         a.score_head_stride = stride[0] if heads > 1 else M * a.score_stride
         a.scores, a.n_heads, a.seq_lens, a.R = scores.data_ptr(), heads, seq_lens.data_ptr(), R
         a.blocks, a.counts = blocks.data_ptr(), counts.data_ptr()
+        if R == 0:
+            return B.PA_OK
         return B.pre_attn_select_blocks(a, self._on(stream), check)
 
     def attend(self, q, block_table, seq_lens, out, *, blocks=None, counts=None, q_fp8_scale: float = 1.0, stream=None,
@@ -203,13 +216,17 @@ class CacheReader:
             a.q, a.q_fp8, a.q_fp8_scale = None, q.data_ptr(), q_fp8_scale
         a.out, a.R, a.block_table, a.seq_lens = out.data_ptr(), R, block_table.data_ptr(), seq_lens.data_ptr()
         if blocks is None:
+            if counts is not None:
+                raise ValueError("counts come with their blocks")
             a.blocks = a.counts = None
         else:
-            if counts is None:
-                raise ValueError("blocks come with their counts")
+            if counts is None or self.topk < 1:
+                raise ValueError("blocks come with their counts, and a reader of lists has topk > 0")
             self._ints(blocks, (M, self.n_kv_heads, self.topk), "blocks")
             self._ints(counts, (M, self.n_kv_heads), "counts")
             a.blocks, a.counts = blocks.data_ptr(), counts.data_ptr()
+        if R == 0:
+            return B.PA_OK
         return B.pre_attn_attention(a, self._on(stream), check)
 
     def device_status(self, stream=None) -> int:

@@ -278,6 +278,88 @@ def test_a_wait_that_runs_out_is_reported(fmt, q_len):
     close(got, c.attention())
 
 
+def test_two_readers_at_once():
+    # two host threads, a reader and a stream each: what one does is not seen by the other
+    import threading
+    cases = [ref.Case(f, [3000, 900], q, 2, 16, seed=90 + q).upload() for f, q in (("fp8", 1), ("nvfp4", 3))]
+    outs = [torch.zeros(c.M, 32 * 128, dtype=torch.bfloat16, device="cuda") for c in cases]
+    torch.cuda.synchronize()
+
+    def work(c, out):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            rd = c.reader()
+            for _ in range(20):
+                rd.attend(c.dev["q"], c.dev["bt"], c.dev["seq"], out)
+            assert rd.device_status() == 0
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(c, o)) for c, o in zip(cases, outs)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    for c, out in zip(cases, outs):
+        close(out.double().cpu().numpy(), c.attention())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_what_the_reader_refuses(fmt):
+    c = ref.Case(fmt, [300, 20], 2, 1, 16, seed=95).upload()
+    rd = c.reader(topk=2)
+    out = torch.zeros(c.M, 2048, dtype=torch.bfloat16, device="cuda")
+    lists, counts = (torch.zeros(*s, dtype=torch.int32, device="cuda") for s in ((c.M, 1, 2), (c.M, 1)))
+    q, bt, seq = c.dev["q"], c.dev["bt"], c.dev["seq"]
+    for bad in (dict(q=q.cpu()), dict(q=q.float()), dict(q=q[1:]), dict(q=q[:, :-128]), dict(bt=bt.cpu()), dict(bt=bt.long()),
+                dict(bt=bt[:, 1:]), dict(seq=seq.cpu()), dict(seq=seq.long()), dict(out=out.cpu()), dict(out=out.float()),
+                dict(blocks=lists), dict(counts=counts), dict(blocks=lists.cpu(), counts=counts),
+                dict(blocks=lists, counts=counts.cpu()), dict(blocks=lists[:, :, :1], counts=counts)):
+        a = dict(dict(q=q, bt=bt, seq=seq, out=out), **bad)
+        with pytest.raises(ValueError):
+            rd.attend(a["q"], a["bt"], a["seq"], a["out"], blocks=a.get("blocks"), counts=a.get("counts"))
+    with pytest.raises(ValueError):  # a reader of every block alone
+        c.reader().attend(q, bt, seq, out, blocks=lists[:, :, :0], counts=counts)
+    scores = torch.zeros(1, c.M, c.W * 128, device="cuda")
+    for bad in (dict(scores=scores.cpu()), dict(seq=seq.cpu()), dict(blocks=lists.cpu()), dict(counts=counts.cpu()),
+                dict(scores=scores.half()), dict(scores=scores[0])):
+        a = dict(dict(scores=scores, seq=seq, blocks=lists, counts=counts), **bad)
+        with pytest.raises(ValueError):
+            rd.select_blocks(a["scores"], a["seq"], a["blocks"], a["counts"])
+    iq = torch.zeros(c.M, 128, dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(iq=iq.cpu()), dict(head=1), dict(bt=bt.cpu()), dict(scores=scores[0].cpu())):
+        a = dict(dict(iq=iq, head=0, bt=bt, seq=seq, scores=scores[0]), **bad)
+        with pytest.raises(ValueError):
+            rd.index_scores(a["iq"], a["head"], a["bt"], a["seq"], a["scores"])
+    assert rd.device_status() == 0 and not out.any()
+
+
+def test_a_call_without_requests_does_nothing():
+    c = ref.Case("fp8", [300], 1, 1, 16, seed=96).upload()
+    rd = c.reader(topk=2)
+    none = {k: c.dev[k][:0] for k in ("q", "bt", "seq")}
+    out = torch.zeros(0, 2048, dtype=torch.bfloat16, device="cuda")
+    lists, counts = (torch.zeros(*s, dtype=torch.int32, device="cuda") for s in ((0, 1, 2), (0, 1)))
+    assert rd.attend(none["q"], none["bt"], none["seq"], out) == 0
+    assert rd.attend(none["q"], none["bt"], none["seq"], out, blocks=lists, counts=counts) == 0
+    scores = torch.zeros(1, 0, c.W * 128, device="cuda")
+    assert rd.index_scores(none["q"][:, :128], 0, none["bt"], none["seq"], scores[0]) == 0
+    assert rd.select_blocks(scores, none["seq"], lists, counts) == 0
+    assert rd.device_status() == 0
+
+
+def test_the_caches_are_read_at_the_call():
+    # a reader whose caches' struct is given its fields after the reader was made
+    c = ref.Case("nvfp4", [300, 130], 1, 1, 16, seed=97).upload()
+    fields = [f for f, _ in c.caches._fields_]
+    kept = {f: getattr(c.caches, f) for f in fields}
+    for f in fields:
+        setattr(c.caches, f, None if "cache" in f else 0)
+    rd = c.reader()
+    for f in fields:
+        setattr(c.caches, f, kept[f])
+    got, status = attend(c, reader=rd)
+    assert status == 0
+    close(got, c.attention())
+
+
 def test_offsets_beyond_32_bits():
     # pages past 2^31 bytes of a cache, and past 2^32
     c = ref.Case("nvfp4", [200, 130], 1, 1, 16, bs=128, seed=23, stale="zero")

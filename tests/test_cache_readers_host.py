@@ -124,6 +124,21 @@ def test_out_over_q_is_refused(B):
         assert B.pre_attn_attention(a, check=False) == B.PA_ERR_ALIAS
 
 
+def test_out_right_behind_a_slice_of_columns_is_not_an_overlap(B):
+    # q: the columns 4096 .. 8191 of rows of 8192, its last row ends where out begins
+    a = attention_args(B, R=2, q=P + 4096 * 2, q_stride=8192, out=P + 4 * 8192 * 2, workspace=None)
+    assert B.pre_attn_attention(a, check=False) in (B.PA_ERR_WORKSPACE, B.PA_ERR_CUDA)  # the next refusal, or no GPU
+    a.out -= 16
+    assert B.pre_attn_attention(a, check=False) == B.PA_ERR_ALIAS
+
+
+@pytest.mark.parametrize("field", ["k_global_scale", "v_global_scale"])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_attention_refuses_global_scales_without_a_value(B, field, value):
+    a = attention_args(B, {field: value}, cache_format=B.PA_CACHE_NVFP4)
+    assert B.pre_attn_attention(a, check=False) == B.PA_ERR_CONFIG
+
+
 def test_workspace_bytes(B):
     n = B.pre_attn_attention_workspace_bytes(64, 7, 2, 152)
     assert n > 0 and B.pre_attn_attention_workspace_bytes(0, 1, 1, 152) > 0
