@@ -10,13 +10,16 @@
 //
 // Work.  An item is (request, up to 8 of its rows, KV head): the rows share
 // the key blocks, so a block is read from memory once for all rows that
-// attend it.  A persistent grid (a CTA an SM) walks the list of all items'
-// blocks in even contiguous slices; an item that several CTAs share leaves
-// partial sums in the workspace and pa_attn_join_kernel adds them up.  A
-// producer warp keeps a ring of 128-key blocks in flight with bulk copies;
-// a query row's (up to 16) heads are the 16 rows of mma.sync m16n8k16, and
-// the eight compute warps are dealt to the item's rows: WPR = 8, 4, 2 or 1
-// warps a row, each with its part of the keys.
+// attend it.  Three ways to deal items to CTAs (launch_attn): a cluster of
+// CTAs an item, joined through distributed shared memory (small calls); a
+// persistent grid that walks the list of all items' blocks in even contiguous
+// slices, an item that several CTAs share leaving partial sums in the
+// workspace for pa_attn_join_kernel; a CTA an item where there are more items
+// than the slices' list holds.  In a CTA one warp resolves the lists and block
+// tables ahead, one thread keeps a ring of 128-key blocks in flight with
+// tensor-map copies (pa_attn.cuh); a query row's (up to 16) heads are the 16
+// rows of mma.sync m16n8k16, and the eight compute warps are dealt to the
+// item's rows: WPR = 8, 4, 2 or 1 warps a row, each with its part of the keys.
 //
 // Arithmetic.  E4M3 codes and E2M1 code x E4M3 scale are f16 values, so keys
 // and values are converted exactly in registers and multiplied on the f16
@@ -24,10 +27,27 @@
 // a maximum in [2^14, 2^15) first, so its bf16 values are f16 values too
 // unless they are 2^-29 of that maximum or less.  The per-token K scale
 // multiplies the score, the per-token V scale the weight.  A weight rounds to
-// f16 (2^-12 relative) for the second product: it is 2^9 exp2(s - m) times
+// f16 (2^-11 relative) for the second product: it is 2^9 exp2(s - m) times
 // the V scale over a power of two near the largest V scale so far, so it
 // stays in f16's normal range for keys whose weight is up to 2^-23 of the
 // largest.  The sum of the weights is taken in f32 before that rounding.
+//
+// Bound and figures (one GB300, calls back to back; the floor is the bytes at
+// the measured copy rate).  Dense decode, ragged lengths up to 32768: FP8, 32
+// requests x 2 KV heads, 276 MB of blocks in 59.7 us (4.6 TB/s, 0.68 of the
+// copy rate); NVFP4, 64 x 4, 625 MB in 179 us (3.5 TB/s, 0.51).  FP8 is bound
+// by the stream and the ends of its slices; NVFP4 and several rows an item by
+// the compute warps: 750 instructions a warp for 32 keys (340 of them convert
+// codes), where two warps a scheduler reach 1.7 to 2 a clock against
+// fixed-latency waits and the ALU (35%) and tensor (34%) pipes.  Small calls
+// (8 requests on 16 blocks each: 8.9 us) are a chain of latencies: list and
+// table, first block, its products, the join.
+//
+// Measured and kept out: the rows of an item as one tcgen05 tile (FP8 spec
+// rows 128 us against 77: softmax latency, instruction cache); two rows a warp
+// sharing converted codes (114 against 77 where rows pick blocks of their own,
+// 70 against 77 on every block); the value products of a step issued behind
+// the next step's scores (179 to 186); twelve compute warps of 144 registers.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -769,8 +789,13 @@ static cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cud
   cfg.stream = stream;
   if (a.mode == kAtSliced) {
     // a cluster an item where all of them are resident at once and a CTA's
-    // share of an item is short: then the scan and the second kernel cost
-    // more than even slices save
+    // share of an item is short: then the scan and the second kernel cost more
+    // than even slices save.  One FP8 row on 16 blocks: 8.9 us, sliced 12.1;
+    // NVFP4, 24 blocks: 10.6, sliced 19.0.  Rows of every block, blocks a CTA
+    // at which the two break even: 14 for one row, 7 for two, 3 to 4 for four,
+    // 1 to 2 for seven (4 and 16 blocks a CTA, one row, 2 items: 9.0 against
+    // 11.0 and 13.2 against 12.0 us; 16 items: 10.3 against 15.6 and 19.2
+    // against 22.4)
     const int longest = a.topk ? std::min(a.bt_width, a.topk * a.rows_per) : a.bt_width;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
@@ -780,7 +805,7 @@ static cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cud
     const Variant &v = kClustered[variant];
     if ((e = use(v, regs[1][variant])) != cudaSuccess) return e;
     for (int n = std::min(kAtMaxSplit, longest); n >= 2 && dev < 64; --n) {
-      if (a.items * n > sms || (longest + n - 1) / n > kAtClusterBlocks) continue;
+      if (a.items * n > sms || (longest + n - 1) / n * a.rows_per > kAtClusterWork) continue;
       int held = resident[variant][dev][n].load(std::memory_order_relaxed);
       attr[1].val.clusterDim.x = n;
       if (held == 0) {
@@ -804,8 +829,11 @@ static cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cud
   cfg.gridDim = dim3(a.mode == kAtSliced ? sms : a.items);
   e = cudaLaunchKernelEx(&cfg, kSliced[variant].kern, maps, a);
   if (e != cudaSuccess || a.mode != kAtSliced || a.test_timeout) return e;
-  // few items: many partials each, a CTA a head; else a warp a head
-  const bool many = a.items * 8 <= sms;
+  // few (item, row)s: many partials each, a CTA a head; else a warp a head.
+  // Dense, whole calls with a CTA a head / a warp a head: 1 item x 4 rows of
+  // 4 heads 77 / 92 us, 32 items x 1 row 37.4 / 38.3, 64 x 1 60.8 / 59.7, 32 x
+  // 4 523 / 518
+  const bool many = a.items * a.rows_per * 4 <= sms;
   cfg.gridDim = dim3(a.items * a.rows_per, many ? a.group : (a.group + kJoinWarps - 1) / kJoinWarps);
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
