@@ -10,6 +10,11 @@
 // a pass from the highest bit in which the keys differ, until a digit is
 // taken whole) and writes the blocks above it, and the first of those equal
 // to it, in block order.
+//
+// One GB300, calls back to back: 64 requests x 7 rows x 2 heads, lengths up to
+// 32767, 61 MB in 13.6 us (4.4 TB/s, 0.66 of the measured copy rate; the
+// selection behind the last loads is what is left); 3 rows x 4 heads of 131072
+// keys 6.7 us, 8 rows of up to 32768 3.7 us, latency.
 #include <cstdint>
 
 #include "../../include/pre_attn.h"
@@ -206,7 +211,10 @@ static cudaError_t launch_select(const SelectParams &a, cudaStream_t stream) {
   if (e0 != cudaSuccess) return e0;
   const int64_t items = (int64_t)a.R * a.q_len * a.n_heads;
   const int sms = current_device_sms();
-  int ctas = 1;  // a (row, head): while the grid is less than two CTAs an SM and each has 16 blocks to read
+  // CTAs a (row, head): more while the grid is less than two CTAs an SM and
+  // each has 16 blocks to read (1, 2, 4, 8 CTAs: 12 (row, head)s of 1024
+  // blocks 13.6, 9.6, 7.7, 6.7 us; 8 of up to 256 5.1, 4.2, 3.8, 3.6)
+  int ctas = 1;
   while (ctas < 8 && items * ctas < 2 * sms && a.bt_width >= 32 * ctas) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
