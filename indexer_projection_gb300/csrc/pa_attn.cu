@@ -158,8 +158,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
   typename Sm::Shared &sh = *reinterpret_cast<typename Sm::Shared *>(q_smem + Sm::kQ + Sm::kJoint);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  pdl_wait();  // queries, caches and lists come from the previous kernels
-  pdl_trigger();
+  const int mode = CLUSTER ? (int)kAtCluster : a.mode;
+  if (warp == kAtWarps && (FMT == 0 ? lane < 4 : lane == 0 && a.bs <= 128))
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.m[lane])) : "memory");
+  if (warp == kAtWarps + 1) attn_prefetch(a, mode);
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sh.full[s], 1);
@@ -175,7 +177,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     mbar_init(&sh.never, 1);
     fence_mbar_init();
   }
-  const int mode = CLUSTER ? (int)kAtCluster : a.mode;
+  pdl_wait();  // queries, caches and lists come from the previous kernels
+  pdl_trigger();
   const AttnSlice sl = attn_slice<kAtWarps>(a, sh, mode);
   if (sl.none) return;
   if (warp >= kAtWarps) {

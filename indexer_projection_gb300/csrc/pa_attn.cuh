@@ -240,6 +240,39 @@ __device__ __forceinline__ AttnSlice attn_slice(const CacheAttnParams &a, S &sh,
   return sl;
 }
 
+// One warp, before the wait on the previous kernels: into L2 what the CTA's
+// first loads will find there (lengths, lists, the block table, queries, each
+// a latency of the chain in front of the first block).  No value is used, so
+// it does not matter that those kernels may still write them.
+__device__ __forceinline__ void attn_prefetch(const CacheAttnParams &a, int mode) {
+  const int lane = threadIdx.x & 31;
+  auto line = [](const void *p, int64_t bytes, int64_t k) {  // 128-byte line k of a span
+    if (128 * k < bytes) prefetch_l2(static_cast<const uint8_t *>(p) + 128 * k);
+  };
+  if (mode == kAtSliced) {  // every CTA a share of the whole
+    const int64_t k = (int64_t)blockIdx.x * 32 + lane, M = (int64_t)a.R * a.q_len;
+    line(a.seq_lens, (int64_t)a.R * 4, k);
+    line(a.block_table, (int64_t)a.R * a.bt_width * 4, k);
+    if (a.topk) {
+      line(a.counts, M * a.n_kv * 4, k);
+      line(a.blocks, M * a.n_kv * a.topk * 4, k);
+    }
+    return;
+  }
+  const int it = mode == kAtCluster ? blockIdx.x / a.split : blockIdx.x;
+  const AttnItem x = attn_place(a, it);
+  const int64_t m = (int64_t)x.r * a.q_len + x.row0;
+  if (lane == 0) prefetch_l2(a.seq_lens + x.r);
+  line(a.block_table + (int64_t)x.r * a.bt_width, (int64_t)a.bt_width * 4, lane);
+  if (a.topk) {
+    line(a.counts + m * a.n_kv, (int64_t)x.rows * a.n_kv * 4, lane);
+    line(a.blocks + m * a.n_kv * a.topk, (int64_t)x.rows * a.n_kv * a.topk * 4, lane);
+  }
+  const int es = a.q_is_fp8 ? 1 : 2;
+  for (int i = 0; i < x.rows; ++i)
+    line(a.q + ((m + i) * a.q_stride + x.h * a.group * kHeadDim) * es, a.group * kHeadDim * es, lane);
+}
+
 // One warp: what is to be copied, a batch of up to 32 blocks ahead of the
 // copies, so that the latency of the lists and the block table (behind the
 // copies already asked for) is hidden.
@@ -251,6 +284,13 @@ __device__ __forceinline__ void attn_resolve(const CacheAttnParams &a, S &sh, co
   int v0, v1, v;
   for (int it = sl.first; ok && sl.segment(a, sh, it, v0, v1, v); ++it) {
     bool bad = false;
+    int b1 = -1, count1 = 0;  // a single row's short list, an entry a lane: asked for together with the length
+    if (a.topk > 0 && a.topk <= 32 && a.rows_per == 1) {
+      const AttnItem y = attn_place(a, it);
+      const int64_t at = ((int64_t)y.r * a.q_len + y.row0) * a.n_kv + y.h;
+      count1 = __ldg(a.counts + at);
+      if (lane < a.topk) b1 = __ldg(a.blocks + at * a.topk + lane);
+    }
     const AttnItem x = attn_item(a, it, &bad);
     if (mode != kAtSliced && bad && lane == 0) set_status(a.status, kDevSlotRange);
     const int nb = x.blocks_upto(x.rows);
@@ -258,13 +298,11 @@ __device__ __forceinline__ void attn_resolve(const CacheAttnParams &a, S &sh, co
     if (a.topk == 0) {
       u0 = (int)((int64_t)nb * v0 / v);
       u1 = (int)((int64_t)nb * v1 / v);
-    } else if (x.rows == 1 && a.topk <= 32) {
-      // one short list, an entry a lane: its distinct blocks in list order
+    } else if (a.rows_per == 1 && a.topk <= 32) {
+      // one short list: its distinct blocks in list order
       if (nb > 0) {
-        const int64_t at = ((int64_t)x.r * a.q_len + x.row0) * a.n_kv + x.h;
-        const int count = __ldg(a.counts + at);
-        int b = lane < a.topk ? __ldg(a.blocks + at * a.topk + lane) : -1;
-        const bool given = lane < min(count, a.topk);
+        int b = b1;
+        const bool given = lane < min(count1, a.topk);
         const bool fits = given && b >= 0 && b < nb;
         if (__any_sync(0xffffffffu, given && !fits) && lane == 0) set_status(a.status, kDevSlotRange);
         if (!fits) b = -1 - lane;
