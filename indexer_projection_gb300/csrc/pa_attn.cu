@@ -67,9 +67,10 @@ constexpr int kAtComputeRegs = 200, kAtProducerRegs = 96;
 
 template <int ROWS>
 struct AttnShared : AttnRing<ROWS> {
-  uint64_t fin;    // the compute warps among themselves
+  uint64_t fin;    // the compute warps among themselves: partial results are there
+  uint64_t read;   // .. have been read
   uint64_t never;  // testing: nothing arrives on it
-  float2 ml[kAtWarps / 2][16];
+  float2 ml[kAtWarps][16];  // .. with WPR > 1, as joint
 };
 
 // A warp takes 16 Y keys at a time and at least those of a block; a row's
@@ -84,7 +85,7 @@ struct AttnSplit {
 
 template <int FMT, int WPR, bool CLUSTER>
 struct AttnSmem {  // stages, then the queries, the buffer where a row's warps meet, the rest
-  static constexpr int kRows = kAtWarps / WPR, kQ = kRows * 16 * kHeadDim * 2, kJoint = WPR > 1 ? 4 * 8192 : 0;
+  static constexpr int kRows = kAtWarps / WPR, kQ = kRows * 16 * kHeadDim * 2, kJoint = WPR > 1 ? kAtWarps * 8192 : 0;
   using Shared = AttnShared<kRows>;
   static constexpr int kRest = kQ + kJoint + (int)sizeof(Shared) + 128;
   static constexpr int kFit = (kAtSmem - kRest) / AttnStage<FMT>::kBytes;
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
   uint8_t *q_smem = ring + kStages * St::kBytes;  // [row][group][128], as q holds them
-  float2 *joint = reinterpret_cast<float2 *>(q_smem + Sm::kQ);  // [4 warps][32][lane]
+  float *joint = reinterpret_cast<float *>(q_smem + Sm::kQ);  // [warp][16 heads][128], in chunks of 4 as joint_at says
   typename Sm::Shared &sh = *reinterpret_cast<typename Sm::Shared *>(q_smem + Sm::kQ + Sm::kJoint);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -174,6 +175,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, kAtWarps);
     mbar_init(&sh.fin, kAtWarps);
+    mbar_init(&sh.read, kAtWarps);
     mbar_init(&sh.never, 1);
     fence_mbar_init();
   }
@@ -199,14 +201,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
   uint32_t phase = 0;
   bool ready = false;
   auto peek = [&]() { ready = __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.full[stage]), phase)); };
-  uint32_t nq = 0, fin_phase = 0;
-  auto fin_sync = [&]() {  // all compute warps; bounded
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.fin);
-    const bool got = mbar_wait(&sh.fin, fin_phase, a.status, a.lim);
-    fin_phase ^= 1;
-    return __all_sync(0xffffffffu, got) != 0;
-  };
+  uint32_t nq = 0, nfin = 0;  // items begun; segments whose warps have met
   // A wait ran out: what this warp leaves out, the status tells.  The CTA stays
   // until no other CTA of its cluster reads its shared memory.
   auto give_up = [&]() {
@@ -568,88 +563,131 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     } else if (mode == kAtSliced && tid == 0) {
       a.shares[it] = make_int2(0, 0);
     }
-    if constexpr (WPR > 1) {
-      // a row's warps meet pairwise: the upper half of them hand o, m and l to
-      // the lower half through shared memory, until one is left
+    float *own = reinterpret_cast<float *>(ring);  // kAtCluster: [row][head][128], then (m, l); the stages are free
+    if constexpr (CLUSTER) pp = own;
+    if constexpr (WPR == 1) {  // a warp's own result, as it holds it
+      if constexpr (CLUSTER) {  // (the warps are done with the stages)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.fin);
+        const bool got = mbar_wait(&sh.fin, 0, a.status, a.lim);
+        if (!__all_sync(0xffffffffu, got)) return give_up();
+      }
+      const int64_t m = (int64_t)x.r * a.q_len + x.row0 + row;
+      if (row < x.rows) {
 #pragma unroll
-      for (int half = WPR / 2; half > 0; half /= 2) {
-        const int slot = row * half + (part & (half - 1));
-        float2 *box = joint + slot * 1024 + lane;
-        if (part >= half && part < 2 * half) {
+        for (int hh = 0; hh < 2; ++hh) {
+          const int head = g + 8 * hh;
+          if (head >= a.group) continue;
+          if (!CLUSTER && whole) {
+            const float inv = l[hh] == 0.f ? 0.f : a.out_scale / l[hh];
+            __nv_bfloat16 *dst = a.out + m * a.out_stride + (int64_t)(x.h * a.group + head) * kHeadDim;
+            if constexpr (FMT == 0) {
 #pragma unroll
-          for (int n = 0; n < 16; ++n)
+              for (int n = 0; n < 16; ++n)
+                *reinterpret_cast<uint32_t *>(dst + 8 * n + 2 * t) = bf16x2_bits(o[n][2 * hh] * inv, o[n][2 * hh + 1] * inv);
+            } else {
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) box[(2 * n + hh) * 32] = make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
-          if (t == 0) sh.ml[slot][g] = make_float2(mref[0], l[0]), sh.ml[slot][g + 8] = make_float2(mref[1], l[1]);
-        }
-        if (!fin_sync()) return give_up();
-        if (part < half) {
+              for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const float2 ml = sh.ml[slot][g + 8 * hh];
-            const float top = fmaxf(mref[hh], ml.x);
-            const float f0 = mref[hh] == top ? 1.f : ex2_approx(mref[hh] - top);
-            const float f1 = ml.x == top ? 1.f : ex2_approx(ml.x - top);
-            mref[hh] = top;
-            l[hh] = f0 * l[hh] + f1 * ml.y;
-#pragma unroll
-            for (int n = 0; n < 16; ++n) {
-              const float2 y = box[(2 * n + hh) * 32];
-              o[n][2 * hh] = f0 * o[n][2 * hh] + f1 * y.x;
-              o[n][2 * hh + 1] = f0 * o[n][2 * hh + 1] + f1 * y.y;
+                for (int n = 0; n < 16; n += 8) {
+                  auto two = [&](int k) { return bf16x2_bits(o[k][2 * hh + e] * inv, o[k + 1][2 * hh + e] * inv); };
+                  *reinterpret_cast<uint4 *>(dst + 16 * (2 * t + e) + n) = make_uint4(two(n), two(n + 2), two(n + 4), two(n + 6));
+                }
             }
+          } else {
+            float *dst = pp + (row * 16 + head) * kHeadDim;
+            if constexpr (FMT == 0) {
+#pragma unroll
+              for (int n = 0; n < 16; ++n)
+                *reinterpret_cast<float2 *>(dst + 8 * n + 2 * t) = make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int n = 0; n < 16; n += 4)
+                  *reinterpret_cast<float4 *>(dst + 16 * (2 * t + e) + n) =
+                      make_float4(o[n][2 * hh + e], o[n + 1][2 * hh + e], o[n + 2][2 * hh + e], o[n + 3][2 * hh + e]);
+            }
+            if (t == 0)
+              *reinterpret_cast<float2 *>(pp + kAtMaxRows * 16 * kHeadDim + (row * 16 + head) * 2) =
+                  make_float2(mref[hh], l[hh]);
           }
         }
-        if (!fin_sync()) return give_up();
       }
-    }
-    const int64_t m = (int64_t)x.r * a.q_len + x.row0 + row;
-    float *own = reinterpret_cast<float *>(ring);  // kAtCluster: [row][head][128], then (m, l); the stages are free
-    if constexpr (CLUSTER) {
-      if constexpr (WPR == 1)
-        if (!fin_sync()) return give_up();  // (with more warps a row they have met above)
-      pp = own;
-    }
-    if (part == 0 && row < x.rows) {
+    } else {
+      // a (row, head)'s result, lane's dims 4 lane .. + 3
+      auto put = [&](int i, int head, float m, float sum, float4 y) {
+        if (!CLUSTER && whole) {
+          const float inv = sum == 0.f ? 0.f : a.out_scale / sum;
+          const int64_t mi = (int64_t)x.r * a.q_len + x.row0 + i;
+          *reinterpret_cast<uint2 *>(a.out + mi * a.out_stride + (int64_t)(x.h * a.group + head) * kHeadDim + 4 * lane) =
+              make_uint2(bf16x2_bits(y.x * inv, y.y * inv), bf16x2_bits(y.z * inv, y.w * inv));
+        } else {
+          *reinterpret_cast<float4 *>(pp + (i * 16 + head) * kHeadDim + 4 * lane) = y;
+          if (lane == 0)
+            *reinterpret_cast<float2 *>(pp + kAtMaxRows * 16 * kHeadDim + (i * 16 + head) * 2) = make_float2(m, sum);
+        }
+      };
+      // o, m and l go to the warp's slot in shared memory; chunk c (4 dims) of a
+      // head sits at c ^ key, so that neither the fragments' writes nor the rows'
+      // reads meet in a bank
+      auto joint_at = [&](int slot, int head, int c) {
+        const int key = FMT == 0 ? (head & 3) << 1 : ((c >> 3) & 3) | (head & 1) << 2;
+        return joint + (slot * 16 + head) * kHeadDim + 4 * (c ^ key);
+      };
+      if (nfin > 0) {  // the segment before has been read
+        const bool got = mbar_wait(&sh.read, (nfin - 1) & 1, a.status, a.lim);
+        if (!__all_sync(0xffffffffu, got)) return give_up();
+      }
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const int head = g + 8 * hh;
-        if (head >= a.group) continue;
-        if (!CLUSTER && whole) {
-          const float inv = l[hh] == 0.f ? 0.f : a.out_scale / l[hh];
-          __nv_bfloat16 *dst = a.out + m * a.out_stride + (int64_t)(x.h * a.group + head) * kHeadDim;
-          if constexpr (FMT == 0) {
+        if constexpr (FMT == 0) {
 #pragma unroll
-            for (int n = 0; n < 16; ++n)
-              *reinterpret_cast<uint32_t *>(dst + 8 * n + 2 * t) = bf16x2_bits(o[n][2 * hh] * inv, o[n][2 * hh + 1] * inv);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int n = 0; n < 16; n += 8) {
-                auto two = [&](int k) { return bf16x2_bits(o[k][2 * hh + e] * inv, o[k + 1][2 * hh + e] * inv); };
-                *reinterpret_cast<uint4 *>(dst + 16 * (2 * t + e) + n) = make_uint4(two(n), two(n + 2), two(n + 4), two(n + 6));
-              }
-          }
+          for (int n = 0; n < 16; ++n)
+            *reinterpret_cast<float2 *>(joint_at(warp, head, 2 * n + (t >> 1)) + 2 * (t & 1)) =
+                make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
         } else {
-          float *dst = pp + (row * 16 + head) * kHeadDim;
-          if constexpr (FMT == 0) {
 #pragma unroll
-            for (int n = 0; n < 16; ++n)
-              *reinterpret_cast<float2 *>(dst + 8 * n + 2 * t) = make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
-          } else {
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int n = 0; n < 16; n += 4)
-                *reinterpret_cast<float4 *>(dst + 16 * (2 * t + e) + n) =
-                    make_float4(o[n][2 * hh + e], o[n + 1][2 * hh + e], o[n + 2][2 * hh + e], o[n + 3][2 * hh + e]);
-          }
-          if (t == 0)
-            *reinterpret_cast<float2 *>(pp + kAtMaxRows * 16 * kHeadDim + (row * 16 + head) * 2) =
-                make_float2(mref[hh], l[hh]);
+            for (int n = 0; n < 16; n += 4)
+              *reinterpret_cast<float4 *>(joint_at(warp, head, 8 * t + 4 * e + n / 4)) =
+                  make_float4(o[n][2 * hh + e], o[n + 1][2 * hh + e], o[n + 2][2 * hh + e], o[n + 3][2 * hh + e]);
         }
+        if (t == 0) sh.ml[warp][head] = make_float2(mref[hh], l[hh]);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.fin);
+      {
+        const bool got = mbar_wait(&sh.fin, nfin & 1, a.status, a.lim);
+        if (!__all_sync(0xffffffffu, got)) return give_up();
+      }
+      // a warp a (row, head): its warps' parts added up in order
+      for (int k = warp; k < x.rows * 16; k += kAtWarps) {
+        const int i = k >> 4, head = k & 15;
+        if (head >= a.group) continue;
+        float2 ml[WPR];
+        float4 y[WPR];
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < WPR; ++c) {
+          ml[c] = sh.ml[i * WPR + c][head];
+          y[c] = *reinterpret_cast<const float4 *>(joint_at(i * WPR + c, head, lane));
+          top = fmaxf(top, ml[c].x);
+        }
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < WPR; ++c) {
+          const float f = ml[c].x == top ? 1.f : ex2_approx(ml[c].x - top);
+          sum += f * ml[c].y;
+          acc.x += f * y[c].x, acc.y += f * y[c].y, acc.z += f * y[c].z, acc.w += f * y[c].w;
+        }
+        put(i, head, top, sum, acc);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.read);
+      ++nfin;
     }
     if constexpr (CLUSTER) {
       cluster_sync();
