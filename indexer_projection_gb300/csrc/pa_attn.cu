@@ -67,6 +67,7 @@ constexpr int kAtComputeRegs = 200, kAtProducerRegs = 96;
 
 template <int ROWS>
 struct AttnShared : AttnRing<ROWS> {
+  uint64_t recv;   // kAtCluster: the other CTAs' partial results are here
   uint64_t fin;    // the compute warps among themselves: partial results are there
   uint64_t read;   // .. have been read
   uint64_t never;  // testing: nothing arrives on it
@@ -85,9 +86,16 @@ struct AttnSplit {
 
 template <int FMT, int WPR, bool CLUSTER>
 struct AttnSmem {  // stages, then the queries, the buffer where a row's warps meet, the rest
-  static constexpr int kRows = kAtWarps / WPR, kQ = kRows * 16 * kHeadDim * 2, kJoint = WPR > 1 ? kAtWarps * 8192 : 0;
+  static constexpr int kRows = kAtWarps / WPR, kQ = kRows * 16 * kHeadDim * 2, kMeet = kAtWarps * 8192;
+  // where the warps meet: a place of its own, with a cluster and few warps a
+  // row the stages, which are free by then (a warp a row, no cluster: nowhere)
+  static constexpr bool kMeetInRing = CLUSTER && WPR <= 2;
+  static constexpr int kJoint = WPR > 1 && !kMeetInRing ? kMeet : 0;
+  // kAtCluster: partial results of the (row, head)s that this CTA joins, from
+  // up to eight CTAs, o then (m, l)
+  static constexpr int kRecvs = CLUSTER ? kRows * 16 + kAtMaxSplit : 0, kRecv = kRecvs * (kHeadDim * 4 + 16);
   using Shared = AttnShared<kRows>;
-  static constexpr int kRest = kQ + kJoint + (int)sizeof(Shared) + 128;
+  static constexpr int kRest = kQ + kJoint + kRecv + (int)sizeof(Shared) + 128;
   static constexpr int kFit = (kAtSmem - kRest) / AttnStage<FMT>::kBytes;
   // a stage belongs to one group, which sees each of its phases (a wait names
   // a phase by its parity alone)
@@ -96,58 +104,14 @@ struct AttnSmem {  // stages, then the queries, the buffer where a row's warps m
   static constexpr int kBytes = kStages * AttnStage<FMT>::kBytes + kRest;
 };
 
-__device__ __forceinline__ float2 ld_cluster_f2(uint32_t a) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
-  return v;
-}
-
-// Every CTA of a cluster joins a share of its item's (row, head)s from all
-// CTAs' partial results, in CTA order: a warp each, four dims a lane.
-__device__ __forceinline__ void cluster_join(const CacheAttnParams &a, const AttnItem &x, const float *own, int rank, int warp,
-                                             int lane) {
-  const int pairs = x.rows * a.group;
-  for (int k = rank + a.split * warp; k < pairs; k += a.split * kAtWarps) {
-    const int i = k / a.group, head = k - i * a.group, at = i * 16 + head;
-    const uint32_t ml_at = smem_u32(own + kAtMaxRows * 16 * kHeadDim + 2 * at);
-    const uint32_t o_at = smem_u32(own + at * kHeadDim + 4 * lane);
-    float2 ml[kAtMaxSplit];
-    float4 y[kAtMaxSplit];
-    float top = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int c = 0; c < kAtMaxSplit; ++c)
-      if (c < a.split) {
-        ml[c] = ld_cluster_f2(mapa(ml_at, c));
-        y[c] = ld_cluster_f4(mapa(o_at, c));
-        top = fmaxf(top, ml[c].x);
-      }
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int c = 0; c < kAtMaxSplit; ++c)
-      if (c < a.split) {
-        const float f = ml[c].x == top ? 1.f : ex2_approx(ml[c].x - top);
-        sum += f * ml[c].y;
-        acc.x += f * y[c].x, acc.y += f * y[c].y, acc.z += f * y[c].z, acc.w += f * y[c].w;
-      }
-    const float inv = sum == 0.f ? 0.f : a.out_scale / sum;
-    const int64_t mi = (int64_t)x.r * a.q_len + x.row0 + i;
-    *reinterpret_cast<uint2 *>(a.out + mi * a.out_stride + (int64_t)(x.h * a.group + head) * kHeadDim + 4 * lane) =
-        make_uint2(bf16x2_bits(acc.x * inv, acc.y * inv), bf16x2_bits(acc.z * inv, acc.w * inv));
-  }
-}
-
 template <int FMT, int WPR, bool CLUSTER>  // CLUSTER: mode kAtCluster
 __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_constant__ AttnMaps maps,
                                                                 const __grid_constant__ CacheAttnParams a) {
   using St = AttnStage<FMT>;
   using Sm = AttnSmem<FMT, WPR, CLUSTER>;
   using Sp = AttnSplit<FMT, WPR, CLUSTER>;
-  static_assert(Sm::kBytes <= kAtSmem && Sm::kStages >= 3, "shared memory of a CTA");
+  static_assert(Sm::kBytes <= kAtSmem && Sm::kStages >= (CLUSTER ? 2 : 3), "shared memory of a CTA");
+  static_assert(!Sm::kMeetInRing || Sm::kMeet <= Sm::kStages * St::kBytes, "the warps' meeting place");
   constexpr int kStages = Sm::kStages;
   constexpr int Y = Sp::Y, kParts = Sp::kParts, kGroups = Sp::kGroups, kKeys = Sp::kKeys;
   constexpr bool kEarly = Y == 2;
@@ -155,8 +119,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
   uint8_t *q_smem = ring + kStages * St::kBytes;  // [row][group][128], as q holds them
-  float *joint = reinterpret_cast<float *>(q_smem + Sm::kQ);  // [warp][16 heads][128], in chunks of 4 as joint_at says
-  typename Sm::Shared &sh = *reinterpret_cast<typename Sm::Shared *>(q_smem + Sm::kQ + Sm::kJoint);
+  // where the warps meet: [warp][16 heads][128], in chunks of 4 as joint_at says
+  float *joint = reinterpret_cast<float *>(Sm::kMeetInRing ? ring : q_smem + Sm::kQ);
+  typename Sm::Shared &sh = *reinterpret_cast<typename Sm::Shared *>(q_smem + Sm::kQ + Sm::kJoint + Sm::kRecv);
+  float *recv = reinterpret_cast<float *>(q_smem + Sm::kQ + Sm::kJoint);  // [CTA][its share of the (row, head)s][128]
+  float4 *recv_ml = reinterpret_cast<float4 *>(recv + Sm::kRecvs * kHeadDim);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int mode = CLUSTER ? (int)kAtCluster : a.mode;
@@ -177,10 +144,21 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     mbar_init(&sh.fin, kAtWarps);
     mbar_init(&sh.read, kAtWarps);
     mbar_init(&sh.never, 1);
+    if constexpr (CLUSTER) mbar_init(&sh.recv, 1);
     fence_mbar_init();
+  }
+  // kAtCluster: CTA c joins the item's (row, head)s c, c + split, ..; what
+  // rank `of` has to join of an item of `rows`
+  auto to_join = [&](int rows, int of) { return (rows * a.group - of + a.split - 1) / a.split; };
+  if constexpr (CLUSTER) {
+    if (tid == 0)
+      mbar_expect_tx(&sh.recv, to_join(attn_place(a, blockIdx.x / a.split).rows, cta_rank()) * a.split * (kHeadDim * 4 + 16));
+    __syncwarp();
+    cluster_arrive_relaxed();  // (a CTA sends when the others' barriers are there)
   }
   pdl_wait();  // queries, caches and lists come from the previous kernels
   pdl_trigger();
+  if constexpr (CLUSTER) cluster_wait();
   const AttnSlice sl = attn_slice<kAtWarps>(a, sh, mode);
   if (sl.none) return;
   if (warp >= kAtWarps) {
@@ -202,13 +180,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
   bool ready = false;
   auto peek = [&]() { ready = __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.full[stage]), phase)); };
   uint32_t nq = 0, nfin = 0;  // items begun; segments whose warps have met
-  // A wait ran out: what this warp leaves out, the status tells.  The CTA stays
-  // until no other CTA of its cluster reads its shared memory.
+  // A wait ran out: what this warp leaves out, the status tells.  Its CTA of a
+  // cluster stays until no other can send to it (those have all they wait for
+  // and are gone, or have given up too).
   auto give_up = [&]() {
-    if constexpr (CLUSTER) {
-      cluster_sync();
-      cluster_sync();
-    }
+    if constexpr (CLUSTER) cluster_sync();
   };
   int v0, v1, v;
   for (int it = sl.first; sl.segment(a, sh, it, v0, v1, v); ++it) {
@@ -563,22 +539,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     } else if (mode == kAtSliced && tid == 0) {
       a.shares[it] = make_int2(0, 0);
     }
-    float *own = reinterpret_cast<float *>(ring);  // kAtCluster: [row][head][128], then (m, l); the stages are free
-    if constexpr (CLUSTER) pp = own;
-    if constexpr (WPR == 1) {  // a warp's own result, as it holds it
-      if constexpr (CLUSTER) {  // (the warps are done with the stages)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.fin);
-        const bool got = mbar_wait(&sh.fin, 0, a.status, a.lim);
-        if (!__all_sync(0xffffffffu, got)) return give_up();
-      }
+    if constexpr (WPR == 1 && !CLUSTER) {  // a warp's own result, as it holds it
       const int64_t m = (int64_t)x.r * a.q_len + x.row0 + row;
       if (row < x.rows) {
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const int head = g + 8 * hh;
           if (head >= a.group) continue;
-          if (!CLUSTER && whole) {
+          if (whole) {
             const float inv = l[hh] == 0.f ? 0.f : a.out_scale / l[hh];
             __nv_bfloat16 *dst = a.out + m * a.out_stride + (int64_t)(x.h * a.group + head) * kHeadDim;
             if constexpr (FMT == 0) {
@@ -615,13 +583,22 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
         }
       }
     } else {
-      // a (row, head)'s result, lane's dims 4 lane .. + 3
+      const int share = CLUSTER ? to_join(x.rows, 0) : 0;  // places a CTA's parts take in another
+      // a (row, head)'s result and its place, dims 4 lane .. + 3
+      auto store = [&](int i, int head, float sum, float4 y) {
+        const float inv = sum == 0.f ? 0.f : a.out_scale / sum;
+        const int64_t mi = (int64_t)x.r * a.q_len + x.row0 + i;
+        *reinterpret_cast<uint2 *>(a.out + mi * a.out_stride + (int64_t)(x.h * a.group + head) * kHeadDim + 4 * lane) =
+            make_uint2(bf16x2_bits(y.x * inv, y.y * inv), bf16x2_bits(y.z * inv, y.w * inv));
+      };
       auto put = [&](int i, int head, float m, float sum, float4 y) {
-        if (!CLUSTER && whole) {
-          const float inv = sum == 0.f ? 0.f : a.out_scale / sum;
-          const int64_t mi = (int64_t)x.r * a.q_len + x.row0 + i;
-          *reinterpret_cast<uint2 *>(a.out + mi * a.out_stride + (int64_t)(x.h * a.group + head) * kHeadDim + 4 * lane) =
-              make_uint2(bf16x2_bits(y.x * inv, y.y * inv), bf16x2_bits(y.z * inv, y.w * inv));
+        if constexpr (CLUSTER) {  // to the CTA that joins it
+          const int k = i * a.group + head, at = sl.lo * share + k / a.split, to = k % a.split;
+          const uint32_t bar = mapa(smem_u32(&sh.recv), to);
+          st_async_v4(mapa(smem_u32(recv + at * kHeadDim + 4 * lane), to), y, bar);
+          if (lane == 0) st_async_v4(mapa(smem_u32(recv_ml + at), to), make_float4(m, sum, 0.f, 0.f), bar);
+        } else if (whole) {
+          store(i, head, sum, y);
         } else {
           *reinterpret_cast<float4 *>(pp + (i * 16 + head) * kHeadDim + 4 * lane) = y;
           if (lane == 0)
@@ -635,7 +612,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
         const int key = FMT == 0 ? (head & 3) << 1 : ((c >> 3) & 3) | (head & 1) << 2;
         return joint + (slot * 16 + head) * kHeadDim + 4 * (c ^ key);
       };
-      if (nfin > 0) {  // the segment before has been read
+      if constexpr (Sm::kMeetInRing) {  // the one segment's stages have been read
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.read);
+        const bool got = mbar_wait(&sh.read, 0, a.status, a.lim);
+        if (!__all_sync(0xffffffffu, got)) return give_up();
+      } else if (nfin > 0) {  // the segment before has been read
         const bool got = mbar_wait(&sh.read, (nfin - 1) & 1, a.status, a.lim);
         if (!__all_sync(0xffffffffu, got)) return give_up();
       }
@@ -685,14 +667,37 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
         }
         put(i, head, top, sum, acc);
       }
+      if constexpr (CLUSTER) {
+        const bool got = mbar_wait_cluster(&sh.recv, 0, a.status, a.lim);
+        if (!__all_sync(0xffffffffu, got)) return give_up();
+        const int mine = to_join(x.rows, sl.lo);
+        for (int k = warp; k < mine; k += kAtWarps) {  // a warp a (row, head), the CTAs' parts in order
+          float2 ml[kAtMaxSplit];
+          float top = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int c = 0; c < kAtMaxSplit; ++c)
+            if (c < a.split) {
+              const float4 u = recv_ml[c * share + k];
+              ml[c] = make_float2(u.x, u.y);
+              top = fmaxf(top, u.x);
+            }
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < kAtMaxSplit; ++c)
+            if (c < a.split) {
+              const float f = ml[c].x == top ? 1.f : ex2_approx(ml[c].x - top);
+              const float4 y = *reinterpret_cast<const float4 *>(recv + (c * share + k) * kHeadDim + 4 * lane);
+              sum += f * ml[c].y;
+              acc.x += f * y.x, acc.y += f * y.y, acc.z += f * y.z, acc.w += f * y.w;
+            }
+          const int pair = sl.lo + k * a.split;
+          store(pair / a.group, pair % a.group, sum, acc);
+        }
+        return;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.read);
       ++nfin;
-    }
-    if constexpr (CLUSTER) {
-      cluster_sync();
-      cluster_join(a, x, own, sl.lo, warp, lane);
-      cluster_sync();  // nobody leaves while its shared memory is read
     }
   }
 }

@@ -59,6 +59,17 @@ def test_rows_and_heads(fmt, q_len, nkv, group):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("q_len,group", [(1, 1), (1, 3), (1, 16), (2, 16), (3, 5), (4, 2), (6, 1), (8, 16)])
+def test_requests_that_few_sms_share(fmt, q_len, group):
+    # tables of two to thirteen blocks: joined by SMs that meet, two to eight of them, or by a kernel of their own
+    for blocks in (2, 3, 5, 7, 8, 9, 13):
+        c = ref.Case(fmt, [128 * blocks - 5, max(q_len, 64 * blocks), 0], q_len, 1, group, seed=100 + blocks).upload()
+        got, status = attend(c)
+        assert status == 0
+        close(got, c.attention())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("q_len,nkv,topk", [(1, 1, 1), (1, 2, 4), (2, 1, 3), (4, 2, 5), (7, 2, 4), (8, 1, 6), (11, 1, 3)])
 def test_selected_blocks(fmt, q_len, nkv, topk):
     c = ref.Case(fmt, [1000, q_len, 0, 260 + q_len, 128 * 9], q_len, nkv, 16, seed=100 + q_len).upload()
