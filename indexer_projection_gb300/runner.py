@@ -102,7 +102,7 @@ class CacheReader:
                  q_len: int, bt_width: int, topk: int = 0, init_blocks: int = 0, local_blocks: int = 0,
                  block_size: int = 16, kv_page_stride: int = 0, sm_scale: float = 128 ** -0.5, flags: int = 0,
                  device: torch.device | str | None = None):
-        B.load()
+        lib = B.load()
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
@@ -129,18 +129,29 @@ class CacheReader:
         if cache_format == B.PA_CACHE_FP8:
             self._scores = B.pa_index_args(None, 0, 0, caches.index_cache, caches.num_index_slots, None, None, 0, q_len,
                                            bt_width, init_blocks, local_blocks, 0.0, None, 0, self.status, 0)
-            self._run_scores = B.pre_attn_index_scores
+            name = "pre_attn_index_scores"
         else:
             self._scores = B.pa_index_nvfp4_args(None, 0, 0, caches.idx_cache, caches.idx_pages, caches.idx_page_bytes,
                                                  block_size, None, None, 0, q_len, bt_width, init_blocks, local_blocks, 0.0,
                                                  None, 0, self.status)
-            self._run_scores = B.pre_attn_index_scores_nvfp4
+            name = "pre_attn_index_scores_nvfp4"
+        self._scores_entry = getattr(lib, name), B.ctypes.byref(self._scores), name
+        self._select_entry = lib.pre_attn_select_blocks, B.ctypes.byref(self._select), "pre_attn_select_blocks"
+        self._attn_entry = lib.pre_attn_attention, B.ctypes.byref(self._attn), "pre_attn_attention"
 
     def _on(self, stream):
         """The stream of a call: the reader's device has to be the current one."""
-        if torch.cuda.current_device() != self.index:
+        if torch._C._cuda_getDevice() != self.index:
             raise ValueError(f"the current device is not the reader's ({self.device})")
-        return torch._C._cuda_getCurrentRawStream(self.index) if stream is None else stream
+        return torch._C._cuda_getCurrentRawStream(self.index) if stream is None else B.stream_ptr(stream)
+
+    def _call(self, entry, stream, check):
+        """Run a C entry point (its function, the reference to its argument struct, its name)."""
+        fn, args, name = entry
+        st = fn(args, self._on(stream))
+        if check and st != B.PA_OK:
+            raise B.PreAttnError(st, name + " " + (B.pre_attn_last_cuda_error() if st == B.PA_ERR_CUDA else ""))
+        return st
 
     def _requests(self, seq_lens, block_table=None) -> int:
         R = seq_lens.shape[0]
@@ -180,7 +191,7 @@ class CacheReader:
             a.idx_cache, a.idx_pages, a.idx_page_bytes = c.idx_cache, c.idx_pages, c.idx_page_bytes
         if R == 0:
             return B.PA_OK
-        return self._run_scores(a, self._on(stream), check)
+        return self._call(self._scores_entry, stream, check)
 
     def select_blocks(self, scores, seq_lens, blocks, counts, *, stream=None, check: bool = True) -> int:
         """The blocks of each row and head from scores [heads, M, >= bt_width * 128] into blocks [M, heads, topk]."""
@@ -199,7 +210,7 @@ class CacheReader:
         a.blocks, a.counts = blocks.data_ptr(), counts.data_ptr()
         if R == 0:
             return B.PA_OK
-        return B.pre_attn_select_blocks(a, self._on(stream), check)
+        return self._call(self._select_entry, stream, check)
 
     def attend(self, q, block_table, seq_lens, out, *, blocks=None, counts=None, q_fp8_scale: float = 1.0, stream=None,
                check: bool = True) -> int:
@@ -227,7 +238,7 @@ class CacheReader:
             a.blocks, a.counts = blocks.data_ptr(), counts.data_ptr()
         if R == 0:
             return B.PA_OK
-        return B.pre_attn_attention(a, self._on(stream), check)
+        return self._call(self._attn_entry, stream, check)
 
     def device_status(self, stream=None) -> int:
         """PA_DEV_* bits of the calls since the last reading (read and cleared; synchronises)."""
