@@ -11,7 +11,7 @@
 // Work.  An item is (request, up to 8 of its rows, KV head): the rows share
 // the key blocks, so a block is read from memory once for all rows that
 // attend it.  Three ways to deal items to CTAs (launch_attn): a cluster of
-// CTAs an item, joined through distributed shared memory (small calls); a
+// CTAs an item, each sending its parts to the CTA that joins them (small calls); a
 // persistent grid that walks the list of all items' blocks in even contiguous
 // slices, an item that several CTAs share leaving partial sums in the
 // workspace for pa_attn_join_kernel; a CTA an item where there are more items
@@ -34,13 +34,13 @@
 //
 // Bound and figures (one GB300, calls back to back; the floor is the bytes at
 // the measured copy rate).  Dense decode, ragged lengths up to 32768: FP8, 32
-// requests x 2 KV heads, 276 MB of blocks in 59.7 us (4.6 TB/s, 0.68 of the
-// copy rate); NVFP4, 64 x 4, 625 MB in 179 us (3.5 TB/s, 0.51).  FP8 is bound
+// requests x 2 KV heads, 276 MB of blocks in 57.5 us (4.8 TB/s, 0.71 of the
+// copy rate); NVFP4, 64 x 4, 625 MB in 172 us (3.6 TB/s, 0.54).  FP8 is bound
 // by the stream and the ends of its slices; NVFP4 and several rows an item by
 // the compute warps: 750 instructions a warp for 32 keys (340 of them convert
 // codes), where two warps a scheduler reach 1.7 to 2 a clock against
 // fixed-latency waits and the ALU (35%) and tensor (34%) pipes.  Small calls
-// (8 requests on 16 blocks each: 8.9 us) are a chain of latencies: list and
+// (8 requests on 16 blocks each: 7.1 us) are a chain of latencies: list and
 // table, first block, its products, the join.
 //
 // Measured and kept out: the rows of an item as one tcgen05 tile (FP8 spec
@@ -65,13 +65,13 @@ constexpr int kAtThreads = 32 * (kAtWarps + 4);  // and the producers' warpgroup
 // with, which launch_attn checks.
 constexpr int kAtComputeRegs = 200, kAtProducerRegs = 96;
 
-template <int ROWS>
+template <int ROWS, int MEET>  // MEET: warps whose parts meet here
 struct AttnShared : AttnRing<ROWS> {
   uint64_t recv;   // kAtCluster: the other CTAs' partial results are here
   uint64_t fin;    // the compute warps among themselves: partial results are there
   uint64_t read;   // .. have been read
   uint64_t never;  // testing: nothing arrives on it
-  float2 ml[kAtWarps][16];  // .. with WPR > 1, as joint
+  float2 ml[MEET][16];
 };
 
 // A warp takes 16 Y keys at a time and at least those of a block; a row's
@@ -88,13 +88,15 @@ template <int FMT, int WPR, bool CLUSTER>
 struct AttnSmem {  // stages, then the queries, the buffer where a row's warps meet, the rest
   static constexpr int kRows = kAtWarps / WPR, kQ = kRows * 16 * kHeadDim * 2, kMeet = kAtWarps * 8192;
   // where the warps meet: a place of its own, with a cluster and few warps a
-  // row the stages, which are free by then (a warp a row, no cluster: nowhere)
+  // row the stages, which are free by then
   static constexpr bool kMeetInRing = CLUSTER && WPR <= 2;
-  static constexpr int kJoint = WPR > 1 && !kMeetInRing ? kMeet : 0;
+  static constexpr bool kDirect = !CLUSTER && WPR <= 2;  // (see the segment's result)
+  static constexpr int kJoint = kMeetInRing || WPR == 1 ? 0 : kDirect ? kMeet / 2 : kMeet;
   // kAtCluster: partial results of the (row, head)s that this CTA joins, from
   // up to eight CTAs, o then (m, l)
   static constexpr int kRecvs = CLUSTER ? kRows * 16 + kAtMaxSplit : 0, kRecv = kRecvs * (kHeadDim * 4 + 16);
-  using Shared = AttnShared<kRows>;
+  // (places for one warp where none meet: a warp a row has its fifth FP8 stage by a few hundred bytes)
+  using Shared = AttnShared<kRows, (kJoint > 0 || kMeetInRing) ? kAtWarps : 1>;
   static constexpr int kRest = kQ + kJoint + kRecv + (int)sizeof(Shared) + 128;
   static constexpr int kFit = (kAtSmem - kRest) / AttnStage<FMT>::kBytes;
   // a stage belongs to one group, which sees each of its phases (a wait names
@@ -539,9 +541,50 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     } else if (mode == kAtSliced && tid == 0) {
       a.shares[it] = make_int2(0, 0);
     }
-    if constexpr (WPR == 1 && !CLUSTER) {  // a warp's own result, as it holds it
+    if constexpr (Sm::kDirect) {
+      // a row has a warp or two: the second hands its part to the first, which
+      // writes the result as it holds it (all rows' parts through shared memory,
+      // as below, took two of nine stages: 5% of a dense call of four NVFP4 rows)
+      if constexpr (WPR == 2) {
+        float2 *box = reinterpret_cast<float2 *>(joint) + warp / 2 * 1024 + lane;  // [32][lane]
+        if (nfin > 0) {  // the segment before has been read
+          const bool got = mbar_wait(&sh.read, (nfin - 1) & 1, a.status, a.lim);
+          if (!__all_sync(0xffffffffu, got)) return give_up();
+        }
+        if (part == 1) {
+#pragma unroll
+          for (int n = 0; n < 16; ++n)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) box[(2 * n + hh) * 32] = make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
+          if (t == 0) sh.ml[warp][g] = make_float2(mref[0], l[0]), sh.ml[warp][g + 8] = make_float2(mref[1], l[1]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.fin);
+        const bool got = mbar_wait(&sh.fin, nfin & 1, a.status, a.lim);
+        if (!__all_sync(0xffffffffu, got)) return give_up();
+        if (part == 0) {
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const float2 ml = sh.ml[warp + 1][g + 8 * hh];
+            const float top = fmaxf(mref[hh], ml.x);
+            const float f0 = mref[hh] == top ? 1.f : ex2_approx(mref[hh] - top);
+            const float f1 = ml.x == top ? 1.f : ex2_approx(ml.x - top);
+            mref[hh] = top;
+            l[hh] = f0 * l[hh] + f1 * ml.y;
+#pragma unroll
+            for (int n = 0; n < 16; ++n) {
+              const float2 y = box[(2 * n + hh) * 32];
+              o[n][2 * hh] = f0 * o[n][2 * hh] + f1 * y.x;
+              o[n][2 * hh + 1] = f0 * o[n][2 * hh + 1] + f1 * y.y;
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.read);
+        ++nfin;
+      }
       const int64_t m = (int64_t)x.r * a.q_len + x.row0 + row;
-      if (row < x.rows) {
+      if (part == 0 && row < x.rows) {
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const int head = g + 8 * hh;
@@ -836,12 +879,12 @@ static cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cud
   if (a.mode == kAtSliced) {
     // a cluster an item where all of them are resident at once and a CTA's
     // share of an item is short: then the scan and the second kernel cost more
-    // than even slices save.  One FP8 row on 16 blocks: 8.9 us, sliced 12.1;
-    // NVFP4, 24 blocks: 10.6, sliced 19.0.  Rows of every block, blocks a CTA
-    // at which the two break even: 14 for one row, 7 for two, 3 to 4 for four,
-    // 1 to 2 for seven (4 and 16 blocks a CTA, one row, 2 items: 9.0 against
-    // 11.0 and 13.2 against 12.0 us; 16 items: 10.3 against 15.6 and 19.2
-    // against 22.4)
+    // than even slices save.  One FP8 row on 16 blocks: 7.2 us, sliced 11.4;
+    // NVFP4, 24 blocks: 8.6, sliced 15.2.  On every block the two break even at
+    // (blocks a CTA) x (rows) of 12 to 16 for 2 items (one row, 16 blocks a
+    // CTA: 11.5 and 11.5 us; four rows, 4: 13.0 against 12.0) and of 25 to 35
+    // for 8 and 16 (one row, 16: 17.2 against 20.9; four rows, 8: 20.9 against
+    // 20.6; seven rows, 4: 22.4 against 26.0)
     const int longest = a.topk ? std::min(a.bt_width, a.topk * a.rows_per) : a.bt_width;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
@@ -851,7 +894,8 @@ static cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cud
     const Variant &v = kClustered[variant];
     if ((e = use(v, regs[1][variant])) != cudaSuccess) return e;
     for (int n = std::min(kAtMaxSplit, longest); n >= 2 && dev < 64; --n) {
-      if (a.items * n > sms || (longest + n - 1) / n * a.rows_per > kAtClusterWork) continue;
+      const int work = (longest + n - 1) / n * a.rows_per;
+      if (a.items * n > sms || work > (a.items * n * 3 >= sms ? 2 : 1) * kAtClusterWork) continue;
       int held = resident[variant][dev][n].load(std::memory_order_relaxed);
       attr[1].val.clusterDim.x = n;
       if (held == 0) {
@@ -876,9 +920,8 @@ static cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cud
   e = cudaLaunchKernelEx(&cfg, kSliced[variant].kern, maps, a);
   if (e != cudaSuccess || a.mode != kAtSliced || a.test_timeout) return e;
   // few (item, row)s: many partials each, a CTA a head; else a warp a head.
-  // Dense, whole calls with a CTA a head / a warp a head: 1 item x 4 rows of
-  // 4 heads 77 / 92 us, 32 items x 1 row 37.4 / 38.3, 64 x 1 60.8 / 59.7, 32 x
-  // 4 523 / 518
+  // Dense, whole calls with a CTA a head / a warp a head: 4 items x 4 rows 78 /
+  // 92 us, 32 items x 1 row 35.9 / 36.9, 64 x 1 58.9 / 57.7, 32 x 4 548 / 543
   const bool many = a.items * a.rows_per * 4 <= sms;
   cfg.gridDim = dim3(a.items * a.rows_per, many ? a.group : (a.group + kJoinWarps - 1) / kJoinWarps);
   cfg.blockDim = dim3(32 * kJoinWarps);
