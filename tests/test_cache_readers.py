@@ -59,7 +59,7 @@ def test_rows_and_heads(fmt, q_len, nkv, group):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("q_len,group", [(1, 1), (1, 3), (1, 16), (2, 16), (3, 5), (4, 2), (6, 1), (8, 16)])
+@pytest.mark.parametrize("q_len,group", [(1, 1), (1, 3), (1, 16), (2, 16), (3, 5), (4, 2), (6, 1), (8, 16), (9, 3), (16, 4)])
 def test_requests_that_few_sms_share(fmt, q_len, group):
     # tables of two to thirteen blocks: joined by SMs that meet, two to eight of them, or by a kernel of their own
     for blocks in (2, 3, 5, 7, 8, 9, 13):
