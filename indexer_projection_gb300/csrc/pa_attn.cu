@@ -34,8 +34,8 @@
 //
 // Bound and figures (one GB300, calls back to back; the floor is the bytes at
 // the measured copy rate).  Dense decode, ragged lengths up to 32768: FP8, 32
-// requests x 2 KV heads, 276 MB of blocks in 57.5 us (4.8 TB/s, 0.71 of the
-// copy rate); NVFP4, 64 x 4, 625 MB in 172 us (3.6 TB/s, 0.54).  FP8 is bound
+// requests x 2 KV heads, 276 MB of blocks in 57.0 us (4.8 TB/s, 0.71 of the
+// copy rate); NVFP4, 64 x 4, 625 MB in 171 us (3.7 TB/s, 0.54).  FP8 is bound
 // by the stream and the ends of its slices; NVFP4 and several rows an item by
 // the compute warps: 750 instructions a warp for 32 keys (340 of them convert
 // codes), where two warps a scheduler reach 1.7 to 2 a clock against
@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
   auto to_join = [&](int rows, int of) { return (rows * a.group - of + a.split - 1) / a.split; };
   if constexpr (CLUSTER) {
     if (tid == 0)
-      mbar_expect_tx(&sh.recv, to_join(attn_place(a, blockIdx.x / a.split).rows, cta_rank()) * a.split * (kHeadDim * 4 + 16));
+      mbar_expect_tx(&sh.recv, to_join(attn_place(a, blockIdx.x / a.split).rows, cta_rank()) * a.split *
+                                   (kHeadDim * 4 + 16));
     __syncwarp();
     cluster_arrive_relaxed();  // (a CTA sends when the others' barriers are there)
   }
@@ -382,7 +383,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
                 x[hh][2 * y + u] = fma2(pack2(c[2 * y + u][2 * hh], c[2 * y + u][2 * hh + 1]), f, pack2(off[hh], off[hh]));
               }
           }
-          auto last_of = [&](int y) { return p - info.x * 128 - k0 - 16 * y - 4 * t; };  // of four keys, the last that counts
+          // of this thread's four keys of 16, the last that counts
+          auto last_of = [&](int y) { return p - info.x * 128 - k0 - 16 * y - 4 * t; };
           auto mask_v = [&](int left, uint32_t *w, uint32_t &f4) {
             const uint32_t keep = left >= 3 ? 0xffffffffu : left < 0 ? 0u : (256u << (8 * left)) - 1u;
             if constexpr (FMT == 0) {
@@ -402,7 +404,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
               if constexpr (kEarly) mask_v(left, vraw + 16 * y, vsf[y]);
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
-                const bool ok0 = (FMT == 0 ? 2 * u : (2 * u + t) & 3) <= left, ok1 = (FMT == 0 ? 2 * u + 1 : (2 * u + 1 + t) & 3) <= left;
+                const bool ok0 = (FMT == 0 ? 2 * u : (2 * u + t) & 3) <= left;
+                const bool ok1 = (FMT == 0 ? 2 * u + 1 : (2 * u + 1 + t) & 3) <= left;
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                   const float2 z = unpack2(x[hh][2 * y + u]);
@@ -759,6 +762,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) pa_attn_join_kernel(const __g
   const int head = blockIdx.y * (kJoinWarps / W) + warp / W;
   const int h = it & (a.n_kv - 1), rg = it >> a.lg_kv, r = rg >> a.lg_groups;
   const int row0 = (rg - (r << a.lg_groups)) * a.rows_per;
+  pdl_trigger();  // the next kernel's CTAs fit beside these; it waits for this grid's end
   pdl_wait();
   const int2 s = a.shares[it];
   const int c0 = max(s.x, 0), c1 = min(s.y, grid - 1);
@@ -853,7 +857,8 @@ static cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cud
                                         {pa_attn_kernel<FMT, 1, true>, AttnSmem<FMT, 1, true>::kBytes}};
   const int variant = a.rows_per == 1 ? 0 : a.rows_per == 2 ? 1 : a.rows_per <= 4 ? 2 : 3;
   cudaLaunchConfig_t cfg = {};
-  auto use = [&](const Variant &v, std::atomic<int> &launch_regs) {  // its shared memory, and that it holds the registers it splits
+  // its shared memory, and that it holds the registers it splits
+  auto use = [&](const Variant &v, std::atomic<int> &launch_regs) {
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(v.kern), v.smem);
     int regs = launch_regs.load(std::memory_order_relaxed);
     if (e == cudaSuccess && regs == 0) {

@@ -29,7 +29,8 @@ constexpr int kAtMaxTopk = 256;
 constexpr float kAtLift = 9.0f;   // weights are 2^9 exp2(s - m)
 constexpr float kAtSlack = 4.0f;  // m follows the maximum once that is 2^4 above it
 constexpr int kAtMaxSplit = 8;    // CTAs a cluster
-constexpr int kAtClusterWork = 12;  // (blocks a CTA) x (rows) of a cluster at most, twice that on a third of the SMs or more
+// (blocks a CTA) x (rows) of a cluster at most; twice that where clusters take a third of the SMs or more
+constexpr int kAtClusterWork = 12;
 constexpr int kAtPartFloats = kAtMaxRows * 16 * (kHeadDim + 2);  // o, then (m, l), of one partial
 
 // How the items meet the CTAs: a CTA an item; even slices of all items'

@@ -9,12 +9,13 @@
 // 4 bytes a (row, key) out).  A warp takes half a 128-key block, straight from
 // global memory into fragments: lane (g, t) reads the 16 code bytes of dims
 // 32 t .. + 31 of keys 4 g .. 4 g + 3, so a load instruction covers whole
-// 64-byte tokens and no byte passes through shared memory.  Row g of tile 0 / row g + 8 of tile 0 / row g of tile 1 / row
-// g + 8 of tile 1 of the two m16n8k16 products are keys 4 g .. 4 g + 3: a
-// thread ends with four consecutive keys of two query rows and stores 16
-// bytes at a time.  Code x scale is an f16 value and the query rows are f16
-// values after a power-of-two scaling to a maximum in [2^14, 2^15) (down to
-// 2^-29 of it), so the products are exact; the sums are f32.
+// 64-byte tokens and no byte passes through shared memory.  Row g of tile 0 /
+// row g + 8 of tile 0 / row g of tile 1 / row g + 8 of tile 1 of the two
+// m16n8k16 products are keys 4 g .. 4 g + 3: a thread ends with four
+// consecutive keys of two query rows and stores 16 bytes at a time.  Code x
+// scale is an f16 value and the query rows are f16 values after a power-of-two
+// scaling to a maximum in [2^14, 2^15) (down to 2^-29 of it), so the products
+// are exact; the sums are f32.
 //
 // One GB300, calls back to back: 64 requests x 7 rows, lengths up to 32767,
 // 106 MB in 25 us (4.2 TB/s, 0.62 of the measured copy rate): each warp is a
@@ -53,7 +54,8 @@ struct Index4Params {
 };
 
 template <int NT>  // n8 tiles of query rows: q_len <= 8 * NT
-__global__ void __launch_bounds__(32 * kI4Warps, NT == 1 ? 5 : 4) pa_index_scores_nvfp4_kernel(const __grid_constant__ Index4Params a) {
+__global__ void __launch_bounds__(32 * kI4Warps, NT == 1 ? 5 : 4)
+    pa_index_scores_nvfp4_kernel(const __grid_constant__ Index4Params a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int r = blockIdx.y, unit = blockIdx.x * kI4Warps + warp;
