@@ -559,8 +559,10 @@ int pre_attn_select_blocks(const pa_select_args *args, void *stream);
  * scale * global scale (PA_CACHE_NVFP4).  A row without keys, or whose every
  * score is -inf, gets zeros; keys after p and unselected blocks are not
  * looked at, whatever they hold.  bf16 q is used exactly up to 2^-29 of its
- * head row's largest value; scores, softmax statistics and sums are f32, the
- * weights enter the second product in f16. */
+ * head row's largest value; scores, softmax statistics and sums are f32.  The
+ * weights (PA_CACHE_FP8: weight x V scale) enter the second product in f16:
+ * 2^-11 relative within 2^-23 of the row's largest, 2^-34 of that largest
+ * below (rows whose V codes are all zero do not count to it). */
 typedef struct pa_attention_args {
   const void *q;              /* [R * q_len, q_stride] bf16, or NULL; 16-byte aligned */
   const void *q_fp8;          /* [R * q_len, q_stride] E4M3, or NULL; 16-byte aligned.  Exactly one of the two */

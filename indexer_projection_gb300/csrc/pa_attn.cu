@@ -26,11 +26,14 @@
 // tensor path with f32 sums.  A query head row is scaled by a power of two to
 // a maximum in [2^14, 2^15) first, so its bf16 values are f16 values too
 // unless they are 2^-29 of that maximum or less.  The per-token K scale
-// multiplies the score, the per-token V scale the weight.  A weight rounds to
-// f16 (2^-11 relative) for the second product: it is 2^9 exp2(s - m) times
-// the V scale over a power of two near the largest V scale so far, so it
-// stays in f16's normal range for keys whose weight is up to 2^-23 of the
-// largest.  The sum of the weights is taken in f32 before that rounding.
+// multiplies the score, the per-token V scale the weight.  For the second
+// product a weight (NVFP4), or a weight times its key's V scale (FP8), rounds
+// to f16: 2^-11 relative while it is within 2^-23 of the largest so far, below
+// that half of f16's smallest step, 2^-34 of the largest.  For FP8 "the
+// largest" is that of weight x V scale, a reference apart from the softmax's:
+// neither a key of large values that has no weight nor a row of zeros (which
+// its writer gives the scale 1) costs the others their bits.  The sum of the
+// weights is taken in f32 before that rounding.
 //
 // Bound and figures (one GB300, calls back to back; the floor is the bytes at
 // the measured copy rate).  Dense decode, ragged lengths up to 32768: FP8, 32
@@ -252,9 +255,13 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
     float mref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float glimit[2] = {-INFINITY, -INFINITY};  // the reference moves when a lifted score is above
-    int ev = -126;  // FP8: o is in units of 2^ev, V scales up to 2^(ev + 1) = vlimit
-    float vlimit = pow2i(-125);
+    // When the reference moves.  NVFP4: a lifted score is above the limit.
+    // FP8: a lane's weights of a step sum to more than it (or none is known)
+    float glimit[2] = {FMT == 0 ? -1.f : -INFINITY, FMT == 0 ? -1.f : -INFINITY};
+    // FP8: o is the sum of weight x V scale x unit x code, and the largest
+    // weight x V scale x unit so far 2^kAtLift or more (2^kAtUnit while that
+    // would take more)
+    float unit[2] = {pow2i(kAtUnit), pow2i(kAtUnit)};
     if (a.test_timeout) {
       const bool got = mbar_wait(&sh.never, 0, a.status, a.lim);
       if (!__all_sync(0xffffffffu, got)) return give_up();
@@ -358,9 +365,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
           if constexpr (kEarly)
 #pragma unroll
             for (int y = 0; y < Y; ++y) read_v(y, vraw + 16 * y, vsf[y]);
-          // x = score - reference (in log2 units, lifted by kAtLift: at most
-          // kAtLift + kAtSlack while the reference holds; the score itself
-          // while there is none), pairs of keys
+          // x = score - reference (in log2 units, lifted by kAtLift; the score
+          // itself while there is none), pairs of keys
           f32x2 x[2][2 * Y], vs2[2 * Y];
           float off[2];
 #pragma unroll
@@ -418,68 +424,118 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
               }
             }
           }
-          float top[2], vtop = 0.f;
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            top[hh] = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 2 * Y; ++k) {
-              const float2 u = unpack2(x[hh][k]);
-              top[hh] = fmaxf(top[hh], fmaxf(u.x, u.y));
-            }
-          }
-          // the reference (and the V unit) move only when a score (a V scale)
-          // has outgrown them, or there is none yet
-          bool grow = top[0] > glimit[0] || top[1] > glimit[1];
-          if constexpr (FMT == 0) {
-#pragma unroll
-            for (int k = 0; k < 2 * Y; ++k) {
-              const float2 u = unpack2(vs2[k]);
-              vtop = fmaxf(vtop, fmaxf(fabsf(u.x), fabsf(u.y)));
-            }
-            grow |= vtop > vlimit;
-          }
-          if (__any_sync(0xffffffffu, grow)) {
-            float f = 1.f;
-            if constexpr (FMT == 0) {
-              const int e2 = max(ev, min(exponent_of(quad_max(vtop)), 126));
-              f = e2 - ev > 125 ? 0.f : pow2i(ev - e2);  // nothing summed yet where it is 0
-              ev = e2;
-              vlimit = pow2i(ev + 1);
-            }
+          uint32_t pa[Y][4];
+          float sum[2];
+          auto weigh = [&]() {
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              const float was = mref[hh], tm = quad_max(top[hh]);
-              const float now = was == -INFINITY ? tm : was + (tm - kAtLift);
-              const float nm = fmaxf(was, now);
-              const float al = nm == was ? 1.f : ex2_approx(was - nm);
-              const float by = nm == was ? 0.f : was == -INFINITY ? kAtLift - nm : was - nm;
+              f32x2 s2 = pack2(0.f, 0.f);
 #pragma unroll
-              for (int k = 0; k < 2 * Y; ++k) x[hh][k] = add2(x[hh][k], pack2(by, by));
-              mref[hh] = nm;
-              glimit[hh] = nm == -INFINITY ? -INFINITY : kAtLift + kAtSlack;
-              l[hh] *= al;
-#pragma unroll
-              for (int n = 0; n < 16; ++n) o[n][2 * hh] *= al * f, o[n][2 * hh + 1] *= al * f;
+              for (int k = 0; k < 2 * Y; ++k) {
+                const float2 u = unpack2(x[hh][k]);
+                f32x2 w = pack2(ex2_approx(u.x), ex2_approx(u.y));
+                s2 = add2(s2, w);
+                if constexpr (FMT == 0) w = mul2(mul2(w, vs2[k]), pack2(unit[hh], unit[hh]));
+                const float2 r = unpack2(w);
+                pa[k >> 1][(k & 1) * 2 + hh] = f16x2_bits(r.x, r.y);
+              }
+              const float2 u = unpack2(s2);
+              sum[hh] = u.x + u.y;
             }
-          }
-          uint32_t pa[Y][4];
-          const float unit = FMT == 0 ? pow2i(-ev) : 1.f;
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            f32x2 sum = pack2(0.f, 0.f);
+          };
+          auto highest = [&](int hh) {
+            float top = -INFINITY;
 #pragma unroll
             for (int k = 0; k < 2 * Y; ++k) {
               const float2 u = unpack2(x[hh][k]);
-              f32x2 w = pack2(ex2_approx(u.x), ex2_approx(u.y));
-              sum = add2(sum, w);
-              if constexpr (FMT == 0) w = mul2(w, mul2(vs2[k], pack2(unit, unit)));
-              const float2 r = unpack2(w);
-              pa[k >> 1][(k & 1) * 2 + hh] = f16x2_bits(r.x, r.y);
+              top = fmaxf(top, fmaxf(u.x, u.y));
             }
-            const float2 u = unpack2(sum);
-            l[hh] += u.x + u.y;
+            return top;
+          };
+          if constexpr (FMT == 0) {
+            // The references move only where a product has outgrown f16 (a NaN
+            // does not count) or the weights their sum; then the step is
+            // weighed again
+#pragma unroll 1
+            for (bool again = false;; again = true) {
+              weigh();
+              uint32_t most = abs_f16x2(pa[0][0]);
+#pragma unroll
+              for (int k = 1; k < 4 * Y; ++k) most = max_f16x2(most, abs_f16x2(pa[k >> 2][k & 3]));
+              // above 2^15 in either half: its bits are above 0x7800
+              const bool grow = ((most + 0x07ff07ffu) & 0x80008000u) != 0u || sum[0] > glimit[0] || sum[1] > glimit[1];
+              if (again || !__any_sync(0xffffffffu, grow)) break;
+              // rows of zeros count for nothing, whatever their scale
+#pragma unroll
+              for (int y = 0; y < Y; ++y) {
+                uint32_t late[kEarly ? 1 : 16], none = 0, some = 0;
+                if constexpr (!kEarly) read_v(y, late, none);
+#pragma unroll
+                for (int n = 0; n < 16; ++n) some |= kEarly ? vraw[16 * y + n] : late[n];
+                some |= __shfl_xor_sync(0xffffffffu, some, 4);
+                some |= __shfl_xor_sync(0xffffffffu, some, 8);
+                some |= __shfl_xor_sync(0xffffffffu, some, 16);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                  const float2 z = unpack2(vs2[2 * y + u]);
+                  const bool zero0 = ((some >> (16 * u)) & 0x7fu) == 0u, zero1 = ((some >> (16 * u)) & 0x7f00u) == 0u;
+                  vs2[2 * y + u] = pack2(zero0 && fabsf(z.x) < INFINITY ? 0.f : z.x, zero1 && fabsf(z.y) < INFINITY ? 0.f : z.y);
+                }
+              }
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                // the softmax's reference: up to the largest score, by whole powers of two
+                const float was = mref[hh], tm = quad_max(highest(hh));
+                const float nm = fmaxf(was, was == -INFINITY ? ceilf(tm) : was + ceilf(tm - kAtLift));
+                const float by = nm == was ? 0.f : was == -INFINITY ? kAtLift - nm : was - nm;
+                const int down = nm == was || was == -INFINITY ? 0 : (int)fminf(nm - was, 1000.f);
+                float pv = 0.f;  // the largest weight x V scale, / 2^10
+#pragma unroll
+                for (int k = 0; k < 2 * Y; ++k) {
+                  x[hh][k] = add2(x[hh][k], pack2(by, by));
+                  const float2 u = unpack2(x[hh][k]), z = unpack2(vs2[k]);
+                  pv = fmaxf(pv, fmaxf(ex2_approx(u.x) * (fabsf(z.x) * pow2i(-10)), ex2_approx(u.y) * (fabsf(z.y) * pow2i(-10))));
+                }
+                pv = quad_max(pv);
+                mref[hh] = nm;
+                glimit[hh] = nm == -INFINITY ? -1.f : kAtMostSum;
+                l[hh] *= down > 126 ? 0.f : pow2i(-down);
+                // the unit: the largest product, of this step or before it
+                // (then 2^down lower than it was), at 2^kAtLift
+                const int at = exponent_of(unit[hh]);
+                int rise = down;
+                if (pv > 0.f) rise = min(rise, (int)kAtLift - 10 - exponent_of(pv) - at);
+                const int to = max(min(at + rise, kAtUnit), -126);
+                unit[hh] = pow2i(to);
+                const int by_o = to - at - down;  // <= 0
+                const float f = by_o < -126 ? 0.f : pow2i(by_o);
+#pragma unroll
+                for (int n = 0; n < 16; ++n) o[n][2 * hh] *= f, o[n][2 * hh + 1] *= f;
+              }
+            }
+          } else {
+            // the reference moves only when a score has outgrown it, or there is none yet
+            const float top[2] = {highest(0), highest(1)};
+            if (__any_sync(0xffffffffu, top[0] > glimit[0] || top[1] > glimit[1])) {
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                const float was = mref[hh], tm = quad_max(top[hh]);
+                const float now = was == -INFINITY ? tm : was + (tm - kAtLift);
+                const float nm = fmaxf(was, now);
+                const float al = nm == was ? 1.f : ex2_approx(was - nm);
+                const float by = nm == was ? 0.f : was == -INFINITY ? kAtLift - nm : was - nm;
+#pragma unroll
+                for (int k = 0; k < 2 * Y; ++k) x[hh][k] = add2(x[hh][k], pack2(by, by));
+                mref[hh] = nm;
+                glimit[hh] = nm == -INFINITY ? -INFINITY : kAtLift + kAtSlack;
+                l[hh] *= al;
+#pragma unroll
+                for (int n = 0; n < 16; ++n) o[n][2 * hh] *= al, o[n][2 * hh + 1] *= al;
+              }
+            }
+            weigh();
           }
+          l[0] += sum[0], l[1] += sum[1];
           peek();
           // o += weights . values
 #pragma unroll
@@ -526,11 +582,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     l[0] = quad_sum(l[0]);
     l[1] = quad_sum(l[1]);
     if constexpr (FMT == 0) {
-      const float up = pow2i(ev);
+      const float up[2] = {pow2i(-exponent_of(unit[0])), pow2i(-exponent_of(unit[1]))};
 #pragma unroll
       for (int n = 0; n < 16; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][e] *= up;
+        for (int e = 0; e < 4; ++e) o[n][e] *= up[e >> 1];
     }
     const bool whole = v0 == 0 && v1 == v;
     float *pp = nullptr;  // the segment's partial result: [row][head][128], then (m, l)

@@ -27,7 +27,9 @@ constexpr int kAtMaxItems = 2048;                  // items the sliced grid list
 constexpr int kAtMaxWidth = 16384;                 // block-table width
 constexpr int kAtMaxTopk = 256;
 constexpr float kAtLift = 9.0f;   // weights are 2^9 exp2(s - m)
-constexpr float kAtSlack = 4.0f;  // m follows the maximum once that is 2^4 above it
+constexpr float kAtSlack = 4.0f;  // NVFP4: m follows the maximum once that is 2^4 above it
+constexpr float kAtMostSum = 65536.f;  // FP8: .. once a lane's weights of a step sum to more
+constexpr int kAtUnit = 100;      // FP8: the unit of the products before any is known is 2^100
 constexpr int kAtMaxSplit = 8;    // CTAs a cluster
 // (blocks a CTA) x (rows) of a cluster at most; twice that where clusters take a third of the SMs or more
 constexpr int kAtClusterWork = 12;
