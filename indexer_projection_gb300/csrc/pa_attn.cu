@@ -582,11 +582,19 @@ __global__ void __launch_bounds__(kAtThreads, 1) pa_attn_kernel(const __grid_con
     l[0] = quad_sum(l[0]);
     l[1] = quad_sum(l[1]);
     if constexpr (FMT == 0) {
-      const float up[2] = {pow2i(-exponent_of(unit[0])), pow2i(-exponent_of(unit[1]))};
+      // o leaves its unit, with l near 2^-kAtSumDown (where the values are not
+      // tiny): then no sum of parts exceeds the largest value, however near
+      // that is to the largest float
 #pragma unroll
-      for (int n = 0; n < 16; ++n)
+      for (int hh = 0; hh < 2; ++hh) {
+        const int eu = exponent_of(unit[hh]);
+        const int el = l[hh] > 0.f && l[hh] < INFINITY ? min(exponent_of(l[hh]) + kAtSumDown, 126 - eu) : 0;
+        const float up = pow2i(-eu - el);
+        mref[hh] += (float)el;
+        l[hh] *= pow2i(-el);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][e] *= up[e >> 1];
+        for (int n = 0; n < 16; ++n) o[n][2 * hh] *= up, o[n][2 * hh + 1] *= up;
+      }
     }
     const bool whole = v0 == 0 && v1 == v;
     float *pp = nullptr;  // the segment's partial result: [row][head][128], then (m, l)

@@ -29,6 +29,9 @@ constexpr int kAtMaxTopk = 256;
 constexpr float kAtLift = 9.0f;   // weights are 2^9 exp2(s - m)
 constexpr float kAtSlack = 4.0f;  // NVFP4: m follows the maximum once that is 2^4 above it
 constexpr float kAtMostSum = 65536.f;  // FP8: .. once a lane's weights of a step sum to more
+// FP8: a part's sum of weights, as it leaves its warp, is about 2^-16: up to
+// 8 warps, 8 CTAs of a cluster or 152 slices (each a warp or eight) then sum to less than one
+constexpr int kAtSumDown = 16;
 constexpr int kAtUnit = 100;      // FP8: the unit of the products before any is known is 2^100
 constexpr int kAtMaxSplit = 8;    // CTAs a cluster
 // (blocks a CTA) x (rows) of a cluster at most; twice that where clusters take a third of the SMs or more

@@ -120,3 +120,10 @@ def test_large_values_with_little_weight(copies, q_len, n):
     g = np.random.default_rng(n)
     big = g.permutation(n) < n // 2
     Scored(n, q_len, np.where(big, -22.0, 0.0), np.where(big, 2.0 ** -9, 2.0 ** -29).astype(np.float32), seed=n + 2).check(copies)
+
+
+@pytest.mark.parametrize("copies,q_len,n", SHAPES)
+@pytest.mark.parametrize("live", [118, -110])
+def test_values_near_the_largest_and_the_smallest(copies, q_len, n, live):
+    # values up to 448 * 2^118, a quarter of the largest bf16 (and down to 2^-105): the sums stay in range
+    Scored(n, q_len, np.zeros(n), np.full(n, 2.0 ** live, np.float32), seed=n + 3).check(copies)
