@@ -489,7 +489,7 @@ int pre_attn_drafter_attention(const pa_drafter_args *args, void *stream);
  * for j <= p in a block that is not pinned, -inf otherwise (as
  * pre_attn_index_scores); products exact, f32 sums.  Columns from nb * 128
  * on, and the scored columns of a block whose id lies outside the cache
- * (flagged), are not written. */
+ * (flagged), are not written: a selection from them is given the block table. */
 typedef struct pa_index_nvfp4_args {
   const void *iq;             /* [R * q_len, iq_stride] bf16, 8-byte aligned */
   int64_t iq_stride;          /* elements a row: a multiple of 4, >= (head + 1) * 128 */
@@ -526,7 +526,9 @@ int pre_attn_index_scores_nvfp4(const pa_index_nvfp4_args *args, void *stream);
  * not selected; equal scores go to the lower block.  blocks[m][h] gets the
  * ids (positions in the request, not physical blocks) in ascending order,
  * then -1 up to topk; counts[m][h] how many there are.  Only columns below
- * nb * 128 of unpinned blocks are read. */
+ * nb * 128 of unpinned blocks are read.  The scorers leave the columns of a
+ * block outside the index cache as they were: with block_table such a block
+ * is not selected (and is flagged); without it every block's columns count. */
 typedef struct pa_select_args {
   const float *scores;        /* [n_heads][R * q_len][score_stride] f32, 16-byte aligned */
   int64_t score_stride;       /* floats a row: a multiple of 4, >= bt_width * 128 */
@@ -541,6 +543,9 @@ typedef struct pa_select_args {
   int32_t *blocks;            /* [R * q_len, n_heads, topk] */
   int32_t *counts;            /* [R * q_len, n_heads] */
   uint32_t *status;           /* device status word: PA_DEV_SLOT_RANGE */
+  const int32_t *block_table; /* [R, bt_width] as the scorers had it, or NULL */
+  int64_t num_blocks;         /* with block_table: page-128 blocks of the index cache (num_index_slots / 128, or
+                                 idx_pages * block_size / 128), >= 1 */
 } pa_select_args;
 
 /* Select on `stream`, after the previous kernel on it (programmatic

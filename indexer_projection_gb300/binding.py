@@ -97,7 +97,8 @@ class pa_select_args(ctypes.Structure):
     _fields_ = [("scores", _vp), ("score_stride", ctypes.c_int64), ("score_head_stride", ctypes.c_int64),
                 ("n_heads", ctypes.c_int), ("seq_lens", _vp), ("R", ctypes.c_int), ("q_len", ctypes.c_int),
                 ("bt_width", ctypes.c_int), ("init_blocks", ctypes.c_int), ("local_blocks", ctypes.c_int),
-                ("topk", ctypes.c_int), ("blocks", _vp), ("counts", _vp), ("status", _vp)]
+                ("topk", ctypes.c_int), ("blocks", _vp), ("counts", _vp), ("status", _vp), ("block_table", _vp),
+                ("num_blocks", ctypes.c_int64)]
 
 
 class pa_attention_args(ctypes.Structure):

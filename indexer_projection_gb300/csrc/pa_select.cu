@@ -35,6 +35,8 @@ struct SelectParams {
   int R, q_len, bt_width, init_blocks, local_blocks, topk;
   int32_t *blocks, *counts;
   uint32_t *status;
+  const int32_t *block_table;  // or null
+  int64_t num_blocks;
 };
 
 // Order-preserving key of a block's maximum: greater score, greater key;
@@ -74,14 +76,19 @@ __global__ void __launch_bounds__(kSelThreads, 6) pa_select_kernel(const __grid_
   constexpr int kStep = kSelThreads / 8;
   for (int b = b0 + (tid >> 3); b < b1 + (tid >> 3); b += 2 * kStep) {  // the same number of turns for a warp's lanes
     float4 v[2][4];
-    bool read[2];
+    bool scored[2], lost[2];  // lost: scored columns that no scorer wrote
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int bu = b + u * kStep;
-      read[u] = bu < b1 && bu >= a.init_blocks && bu < nb - a.local_blocks;
+      scored[u] = bu < b1 && bu >= a.init_blocks && bu < nb - a.local_blocks;
+      lost[u] = false;
+      if (a.block_table && scored[u]) {
+        const int64_t id = __ldg(a.block_table + (int64_t)r * a.bt_width + bu);
+        lost[u] = id < 0 || id >= a.num_blocks;
+      }
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        v[u][k] = read[u] ? __ldg(reinterpret_cast<const float4 *>(row + bu * 128) + 8 * k + sub)
+        v[u][k] = scored[u] ? __ldg(reinterpret_cast<const float4 *>(row + bu * 128) + 8 * k + sub)
                           : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     }
 #pragma unroll
@@ -92,9 +99,12 @@ __global__ void __launch_bounds__(kSelThreads, 6) pa_select_kernel(const __grid_
       for (int k = 0; k < 4; ++k) x = fmaxf(fmaxf(fmaxf(x, v[u][k].x), fmaxf(v[u][k].y, v[u][k].z)), v[u][k].w);
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-      if (sub == 0 && bu < b1)
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(keys0 + 4 * bu), "r"(read[u] ? score_key(x) : 0xffffffffu)
+      if (lost[u]) x = -INFINITY;
+      if (sub == 0 && bu < b1) {
+        if (lost[u]) set_status(a.status, kDevSlotRange);
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(keys0 + 4 * bu), "r"(scored[u] ? score_key(x) : 0xffffffffu)
                      : "memory");
+      }
     }
   }
   cluster_sync();
@@ -244,10 +254,11 @@ extern "C" int pre_attn_select_blocks(const pa_select_args *in, void *stream) {
     return PA_ERR_SHAPE;
   if (x.init_blocks < 0 || x.local_blocks < 0 || (int64_t)x.init_blocks + x.local_blocks > x.topk) return PA_ERR_CONFIG;
   if (x.score_stride < (int64_t)x.bt_width * 128 ||
-      (x.n_heads > 1 && x.score_head_stride < (int64_t)x.R * x.q_len * x.score_stride))
+      (x.n_heads > 1 && x.score_head_stride < (int64_t)x.R * x.q_len * x.score_stride) ||
+      (x.block_table && x.num_blocks < 1))
     return PA_ERR_SHAPE;
   if (!aligned(x.scores, 16) || x.score_stride % 4 || x.score_head_stride % 4 || !aligned(x.seq_lens, 4) ||
-      !aligned(x.blocks, 4) || !aligned(x.counts, 4) || !aligned(x.status, 4))
+      !aligned(x.blocks, 4) || !aligned(x.counts, 4) || !aligned(x.status, 4) || !aligned(x.block_table, 4))
     return PA_ERR_ALIGN;
   if (x.R == 0) return PA_OK;
   pa::SelectParams a;
@@ -265,6 +276,8 @@ extern "C" int pre_attn_select_blocks(const pa_select_args *in, void *stream) {
   a.blocks = x.blocks;
   a.counts = x.counts;
   a.status = x.status;
+  a.block_table = x.block_table;
+  a.num_blocks = x.num_blocks;
   const cudaError_t e = pa::launch_select(a, (cudaStream_t)stream);
   return e == cudaSuccess ? PA_OK : pa::record_cuda_error(e);
 }

@@ -125,7 +125,7 @@ class CacheReader:
                                          bt_width, sm_scale, None, 0, self.status + 256, self.ws_bytes, self.status,
                                          flags)
         self._select = B.pa_select_args(None, 0, 0, 0, None, 0, q_len, bt_width, init_blocks, local_blocks, topk, None,
-                                        None, self.status)
+                                        None, self.status, None, 0)
         if cache_format == B.PA_CACHE_FP8:
             self._scores = B.pa_index_args(None, 0, 0, caches.index_cache, caches.num_index_slots, None, None, 0, q_len,
                                            bt_width, init_blocks, local_blocks, 0.0, None, 0, self.status, 0)
@@ -193,9 +193,10 @@ class CacheReader:
             return B.PA_OK
         return self._call(self._scores_entry, stream, check)
 
-    def select_blocks(self, scores, seq_lens, blocks, counts, *, stream=None, check: bool = True) -> int:
-        """The blocks of each row and head from scores [heads, M, >= bt_width * 128] into blocks [M, heads, topk]."""
-        R = self._requests(seq_lens)
+    def select_blocks(self, scores, seq_lens, blocks, counts, *, block_table=None, stream=None, check: bool = True) -> int:
+        """The blocks of each row and head from scores [heads, M, >= bt_width * 128] into blocks [M, heads, topk]; with
+        the block table, none whose id lies outside the index cache (whose columns index_scores leaves as they were)."""
+        R = self._requests(seq_lens, block_table)
         M, shape, stride, a = R * self.q_len, scores.shape, scores.stride(), self._select
         width = self.bt_width * 128
         if (scores.dtype is not torch.float32 or len(shape) != 3 or shape[0] < 1 or shape[1] != M or shape[2] < width
@@ -208,6 +209,11 @@ class CacheReader:
         a.score_head_stride = stride[0] if heads > 1 else M * a.score_stride
         a.scores, a.n_heads, a.seq_lens, a.R = scores.data_ptr(), heads, seq_lens.data_ptr(), R
         a.blocks, a.counts = blocks.data_ptr(), counts.data_ptr()
+        a.block_table = None
+        if block_table is not None:
+            c = self.caches
+            slots = c.num_index_slots if self.cache_format == B.PA_CACHE_FP8 else c.idx_pages * self.block_size
+            a.block_table, a.num_blocks = block_table.data_ptr(), slots // 128
         if R == 0:
             return B.PA_OK
         return self._call(self._select_entry, stream, check)
