@@ -87,9 +87,9 @@ class CacheReader:
     ``q_len`` rows whose block tables hold ``bt_width`` page-128 blocks.
 
     ``caches`` is PreAttn.fp8_caches(...) or PreAttn.nvfp4_caches(...), read at
-    every call: the fields that a call reads have to be set (the index cache
-    for ``index_scores``, the K / V ones for ``attend``) and their tensors kept
-    alive by the caller.  Owns a workspace, a status word and the calls'
+    every call (and may be replaced by another of the same format): the fields
+    that a call reads have to be set (the index cache for ``index_scores``, the
+    K / V ones for ``attend``) and their tensors kept alive by the caller.  Owns a workspace, a status word and the calls'
     argument structs: one host thread uses a reader at a time, and its calls,
     replays of captured ones among them, are ordered on the GPU by their
     stream, or by the caller (calls that may run together take a reader each).
@@ -107,7 +107,7 @@ class CacheReader:
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self.index = self.device.index
-        self.n_q_heads, self.n_kv_heads, self.cache_format, self.caches = n_q_heads, n_kv_heads, cache_format, caches
+        self.n_q_heads, self.n_kv_heads, self.cache_format = n_q_heads, n_kv_heads, cache_format
         self.max_requests, self.q_len, self.bt_width, self.topk = max_requests, q_len, bt_width, topk
         self.init_blocks, self.local_blocks, self.block_size = init_blocks, local_blocks, block_size
         self.index_scale = B.pre_attn_index_scale_log2e(sm_scale)
@@ -121,9 +121,10 @@ class CacheReader:
         self.status = self.workspace.data_ptr()
         # the calls' argument structs, of which a call sets what changes
         self._attn = B.pa_attention_args(None, None, 1.0, 0, n_q_heads, n_kv_heads, cache_format, block_size,
-                                         kv_page_stride, B.ctypes.pointer(caches), None, None, None, None, topk, 0, q_len,
+                                         kv_page_stride, None, None, None, None, None, topk, 0, q_len,
                                          bt_width, sm_scale, None, 0, self.status + 256, self.ws_bytes, self.status,
                                          flags)
+        self.caches = caches
         self._select = B.pa_select_args(None, 0, 0, 0, None, 0, q_len, bt_width, init_blocks, local_blocks, topk, None,
                                         None, self.status, None, 0)
         if cache_format == B.PA_CACHE_FP8:
@@ -138,6 +139,14 @@ class CacheReader:
         self._scores_entry = getattr(lib, name), B.ctypes.byref(self._scores), name
         self._select_entry = lib.pre_attn_select_blocks, B.ctypes.byref(self._select), "pre_attn_select_blocks"
         self._attn_entry = lib.pre_attn_attention, B.ctypes.byref(self._attn), "pre_attn_attention"
+
+    @property
+    def caches(self) -> B.pa_caches:
+        return self._caches
+
+    @caches.setter
+    def caches(self, caches: B.pa_caches):
+        self._caches, self._attn.caches = caches, B.ctypes.pointer(caches)
 
     def _on(self, stream):
         """The stream of a call: the reader's device has to be the current one."""
@@ -184,7 +193,7 @@ class CacheReader:
         a.iq, a.head, a.block_table, a.seq_lens = iq.data_ptr(), head, block_table.data_ptr(), seq_lens.data_ptr()
         a.R, a.scores = R, scores.data_ptr()
         a.index_scale = self.index_scale if scale is None else scale
-        c = self.caches
+        c = self._caches
         if self.cache_format == B.PA_CACHE_FP8:
             a.index_cache, a.num_index_slots = c.index_cache, c.num_index_slots
         else:
@@ -211,7 +220,7 @@ class CacheReader:
         a.blocks, a.counts = blocks.data_ptr(), counts.data_ptr()
         a.block_table = None
         if block_table is not None:
-            c = self.caches
+            c = self._caches
             slots = c.num_index_slots if self.cache_format == B.PA_CACHE_FP8 else c.idx_pages * self.block_size
             a.block_table, a.num_blocks = block_table.data_ptr(), slots // 128
         if R == 0:

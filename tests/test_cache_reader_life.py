@@ -1,0 +1,51 @@
+"""A CacheReader's life: its caches replaced, made on one stream and used on another, dropped early, on a device."""
+
+import gc
+import types
+
+import numpy as np
+import pytest
+import torch
+
+from tests import cache_reference as ref
+
+
+def attend(case, rd, **kw):
+    out = torch.full((case.M, case.nkv * case.group * 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    rd.attend(case.dev["q"], case.dev["bt"], case.dev["seq"], out, **kw)
+    return out
+
+
+def check(out, case, want=None):
+    want, tol = want or case.attention()
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+def test_other_caches_are_read_by_every_call(fmt):
+    a, b = (ref.Case(fmt, [300, 130], 1, 1, 16, seed=s).upload() for s in (51, 52))
+    b.dev["q"], b.q = a.dev["q"], a.q
+    rd = a.reader()
+    check(attend(a, rd), a)
+    assert rd.caches is a.caches
+    rd.caches = b.caches
+    assert rd.caches is b.caches
+    check(attend(b, rd), b)
+    assert rd.device_status() == 0
+    # the scores of one index cache, then of another
+    keys = [torch.randint(0, 0x38, (512, 128 if fmt == "fp8" else 72), dtype=torch.uint8, device="cuda") for _ in "ab"]
+    seq, bt = torch.tensor([200], dtype=torch.int32, device="cuda"), torch.tensor([[2, 1]], dtype=torch.int32, device="cuda")
+    iq = torch.ones(1, 128, dtype=torch.bfloat16, device="cuda")
+    got = []
+    from indexer_projection_gb300.runner import CacheReader, PreAttn
+    held = [PreAttn.fp8_caches(None, None, None, None, k, 0, 512) if fmt == "fp8" else PreAttn.nvfp4_caches(None, 0, 0, k, 32, 1152)
+            for k in keys]
+    for first in (0, 1):
+        rd = CacheReader(16, 1, cache_format=a.format, caches=held[first], max_requests=1, q_len=1, bt_width=2)
+        for k in (first, 1 - first):
+            rd.caches = held[k]
+            s = torch.zeros(1, 256, device="cuda")
+            rd.index_scores(iq, 0, bt, seq, s)
+            got.append(s)
+    assert torch.equal(got[0], got[3]) and torch.equal(got[1], got[2]) and not torch.equal(got[0], got[1])
