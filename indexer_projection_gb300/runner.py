@@ -95,7 +95,9 @@ class CacheReader:
     stream, or by the caller (calls that may run together take a reader each).
     Every tensor is on ``device``; seq_lens, block tables, block lists and
     counts are contiguous int32, scores and query rows have contiguous columns.
-    A call without requests does nothing.
+    A call without requests does nothing.  Making a reader waits for the
+    current stream (its status word is cleared there, for calls on any stream),
+    so it is made outside a capture.
     """
 
     def __init__(self, n_q_heads: int, n_kv_heads: int, *, cache_format: int, caches: B.pa_caches, max_requests: int,
@@ -111,13 +113,17 @@ class CacheReader:
         self.max_requests, self.q_len, self.bt_width, self.topk = max_requests, q_len, bt_width, topk
         self.init_blocks, self.local_blocks, self.block_size = init_blocks, local_blocks, block_size
         self.index_scale = B.pre_attn_index_scale_log2e(sm_scale)
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a CacheReader is made outside a capture")
         sms = torch.cuda.get_device_properties(self.device).multi_processor_count
         self.ws_bytes = B.pre_attn_attention_workspace_bytes(max_requests, q_len, n_kv_heads, sms)
         if self.ws_bytes == 0:
             raise ValueError(f"max_requests {max_requests}, q_len {q_len} or n_kv_heads {n_kv_heads} out of range")
         # the first 256 bytes hold the status word
         self.workspace = torch.empty(256 + self.ws_bytes, dtype=torch.uint8, device=self.device)
-        B.pre_attn_workspace_init(self.workspace, 256, torch.cuda.current_stream(self.device))
+        made_on = torch.cuda.current_stream(self.device)
+        B.pre_attn_workspace_init(self.workspace, 256, made_on)
+        made_on.synchronize()
         self.status = self.workspace.data_ptr()
         # the calls' argument structs, of which a call sets what changes
         self._attn = B.pa_attention_args(None, None, 1.0, 0, n_q_heads, n_kv_heads, cache_format, block_size,

@@ -49,3 +49,35 @@ def test_other_caches_are_read_by_every_call(fmt):
             rd.index_scores(iq, 0, bt, seq, s)
             got.append(s)
     assert torch.equal(got[0], got[3]) and torch.equal(got[1], got[2]) and not torch.equal(got[0], got[1])
+
+
+@pytest.mark.gpu
+def test_made_on_a_busy_stream_and_used_on_another():
+    # the status word is clear before the first call of another stream raises a bit in it
+    from indexer_projection_gb300 import binding as B
+
+    c = ref.Case("fp8", [300, 500], 1, 1, 16, seed=53).upload()
+    c.dev["seq"] = torch.tensor([128 * c.W + 1, 500], dtype=torch.int32, device="cuda")  # longer than its table
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(300_000_000)
+    rd = c.reader()
+    with torch.cuda.stream(s):
+        attend(c, rd)
+    torch.cuda.synchronize()
+    assert rd.device_status() == B.PA_DEV_SLOT_RANGE
+
+
+@pytest.mark.gpu
+def test_not_made_in_a_capture():
+    c = ref.Case("fp8", [300], 1, 1, 16, seed=54).upload()
+    x = torch.zeros(8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        with pytest.raises(RuntimeError, match="capture"):
+            c.reader()
+        x += 1
+    g.replay()
+    torch.cuda.synchronize()
+    assert (x == 1).all()
+    check(attend(c, c.reader()), c)
