@@ -7,6 +7,8 @@ workspace and turns tensors into the C structs of include/pre_attn.h.
 
 from __future__ import annotations
 
+import sys
+
 import torch
 
 from . import binding as B
@@ -97,7 +99,9 @@ class CacheReader:
     counts are contiguous int32, scores and query rows have contiguous columns.
     A call without requests does nothing.  Making a reader waits for the
     current stream (its status word is cleared there, for calls on any stream),
-    so it is made outside a capture.
+    so it is made outside a capture.  A reader may be dropped while its calls
+    run (its workspace is not reused before them), but has to outlive the
+    graphs that hold captured ones.
     """
 
     def __init__(self, n_q_heads: int, n_kv_heads: int, *, cache_format: int, caches: B.pa_caches, max_requests: int,
@@ -125,6 +129,8 @@ class CacheReader:
         B.pre_attn_workspace_init(self.workspace, 256, made_on)
         made_on.synchronize()
         self.status = self.workspace.data_ptr()
+        self._made_on = made_on.cuda_stream
+        self._used_on = set()  # streams of its calls
         # the calls' argument structs, of which a call sets what changes
         self._attn = B.pa_attention_args(None, None, 1.0, 0, n_q_heads, n_kv_heads, cache_format, block_size,
                                          kv_page_stride, None, None, None, None, None, topk, 0, q_len,
@@ -158,7 +164,18 @@ class CacheReader:
         """The stream of a call: the reader's device has to be the current one."""
         if torch._C._cuda_getDevice() != self.index:
             raise ValueError(f"the current device is not the reader's ({self.device})")
-        return torch._C._cuda_getCurrentRawStream(self.index) if stream is None else B.stream_ptr(stream)
+        s = torch._C._cuda_getCurrentRawStream(self.index) if stream is None else B.stream_ptr(stream)
+        self._used_on.add(s)
+        return s
+
+    def __del__(self):
+        # the allocator hands the workspace out again behind the work that is on these streams now
+        if sys is None or sys.is_finalizing():
+            return
+        for s in getattr(self, "_used_on", ()):
+            if s != self._made_on:
+                self.workspace.record_stream(torch.cuda.ExternalStream(s, device=self.device) if s else
+                                             torch.cuda.default_stream(self.device))
 
     def _call(self, entry, stream, check):
         """Run a C entry point (its function, the reference to its argument struct, its name)."""

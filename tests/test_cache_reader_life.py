@@ -81,3 +81,36 @@ def test_not_made_in_a_capture():
     torch.cuda.synchronize()
     assert (x == 1).all()
     check(attend(c, c.reader()), c)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("made_on_side", [False, True])
+@pytest.mark.parametrize("given", [False, True])
+def test_dropped_while_its_call_runs(made_on_side, given):
+    # the workspace goes back to the allocator, but not to another stream's tensors before the call is done
+    c = ref.Case("nvfp4", [40000, 300], 1, 1, 16, seed=55).upload()
+    want = c.attention()
+    side = torch.cuda.Stream()
+    used, made = (torch.cuda.default_stream(), side) if made_on_side else (side, torch.cuda.default_stream())
+    with torch.cuda.stream(made):
+        rd = c.reader()
+    at, size = rd.workspace.data_ptr(), rd.workspace.numel()
+    warm = c.reader()  # (loading the kernels waits for the device; it stays, so that its workspace is not handed out)
+    check(attend(c, warm), c, want)
+    out = torch.full((c.M, 2048), float("nan"), dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(used):
+        torch.cuda._sleep(300_000_000)
+    if given:
+        rd.attend(c.dev["q"], c.dev["bt"], c.dev["seq"], out, stream=used)
+    else:
+        with torch.cuda.stream(used):
+            rd.attend(c.dev["q"], c.dev["bt"], c.dev["seq"], out)
+    del rd
+    gc.collect()
+    with torch.cuda.stream(made):
+        other = torch.empty(size, dtype=torch.uint8, device="cuda")
+        assert not used.query() and other.data_ptr() != at
+        other.fill_(0xff)
+    torch.cuda.synchronize()
+    check(out, c, want)
