@@ -108,8 +108,10 @@ class CacheReader:
                  q_len: int, bt_width: int, topk: int = 0, init_blocks: int = 0, local_blocks: int = 0,
                  block_size: int = 16, kv_page_stride: int = 0, sm_scale: float = 128 ** -0.5, flags: int = 0,
                  device: torch.device | str | None = None):
+        self.device = torch.device("cuda" if device is None else device)
+        if self.device.type != "cuda":
+            raise ValueError(f"a CUDA device is wanted, not {self.device}")
         lib = B.load()
-        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self.index = self.device.index
@@ -117,17 +119,18 @@ class CacheReader:
         self.max_requests, self.q_len, self.bt_width, self.topk = max_requests, q_len, bt_width, topk
         self.init_blocks, self.local_blocks, self.block_size = init_blocks, local_blocks, block_size
         self.index_scale = B.pre_attn_index_scale_log2e(sm_scale)
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("a CacheReader is made outside a capture")
         sms = torch.cuda.get_device_properties(self.device).multi_processor_count
         self.ws_bytes = B.pre_attn_attention_workspace_bytes(max_requests, q_len, n_kv_heads, sms)
         if self.ws_bytes == 0:
             raise ValueError(f"max_requests {max_requests}, q_len {q_len} or n_kv_heads {n_kv_heads} out of range")
         # the first 256 bytes hold the status word
-        self.workspace = torch.empty(256 + self.ws_bytes, dtype=torch.uint8, device=self.device)
-        made_on = torch.cuda.current_stream(self.device)
-        B.pre_attn_workspace_init(self.workspace, 256, made_on)
-        made_on.synchronize()
+        with torch.cuda.device(self.device):
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("a CacheReader is made outside a capture")
+            self.workspace = torch.empty(256 + self.ws_bytes, dtype=torch.uint8, device=self.device)
+            made_on = torch.cuda.current_stream()
+            B.pre_attn_workspace_init(self.workspace, 256, made_on)
+            made_on.synchronize()
         self.status = self.workspace.data_ptr()
         self._made_on = made_on.cuda_stream
         self._used_on = set()  # streams of its calls
@@ -161,10 +164,15 @@ class CacheReader:
         self._caches, self._attn.caches = caches, B.ctypes.pointer(caches)
 
     def _on(self, stream):
-        """The stream of a call: the reader's device has to be the current one."""
+        """The stream of a call: the reader's device has to be the current one, and the stream's."""
         if torch._C._cuda_getDevice() != self.index:
             raise ValueError(f"the current device is not the reader's ({self.device})")
-        s = torch._C._cuda_getCurrentRawStream(self.index) if stream is None else B.stream_ptr(stream)
+        if stream is None:
+            s = torch._C._cuda_getCurrentRawStream(self.index)
+        else:
+            if getattr(stream, "device_index", self.index) != self.index:
+                raise ValueError(f"the stream is of another device than the reader's ({self.device})")
+            s = B.stream_ptr(stream)
         self._used_on.add(s)
         return s
 

@@ -114,3 +114,22 @@ def test_dropped_while_its_call_runs(made_on_side, given):
         other.fill_(0xff)
     torch.cuda.synchronize()
     check(out, c, want)
+
+
+@pytest.mark.parametrize("device", ["cpu", torch.device("cpu"), "meta"])
+def test_a_device_without_cuda_is_refused(device):
+    from indexer_projection_gb300 import binding as B
+    from indexer_projection_gb300.runner import CacheReader
+
+    with pytest.raises(ValueError, match="CUDA device"):
+        CacheReader(16, 1, cache_format=B.PA_CACHE_FP8, caches=B.pa_caches(), max_requests=1, q_len=1, bt_width=1, device=device)
+
+
+@pytest.mark.gpu
+def test_a_stream_of_another_device_is_refused():
+    c = ref.Case("fp8", [300], 1, 1, 16, seed=56).upload()
+    rd = c.reader(device="cuda")
+    with pytest.raises(ValueError, match="another device"):
+        attend(c, rd, stream=types.SimpleNamespace(cuda_stream=0, device_index=1))
+    check(attend(c, rd, stream=torch.cuda.current_stream()), c)
+    check(attend(c, rd, stream=torch.cuda.current_stream().cuda_stream), c)
