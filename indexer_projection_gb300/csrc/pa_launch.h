@@ -2,6 +2,8 @@
 #pragma once
 
 #include <mutex>
+#include <new>
+#include <vector>
 
 #include <cuda_runtime.h>
 
@@ -21,17 +23,22 @@ inline cudaError_t ensure_smem_attr(const void *kern, int bytes) {
     const void *k;
     int dev, bytes;
   };
-  static Entry table[64];
-  static int n = 0;
-  static std::mutex held;  // host threads may call at once
+  static std::vector<Entry> table;  // as many as there are kernels and devices in use
+  static std::mutex held;           // host threads may call at once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> guard(held);
-  for (int i = 0; i < n; ++i)
-    if (table[i].k == kern && table[i].dev == dev && table[i].bytes >= bytes) return cudaSuccess;
+  Entry *known = nullptr;
+  for (Entry &t : table)
+    if (t.k == kern && t.dev == dev) known = &t;
+  if (known && known->bytes >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && n < 64) table[n++] = Entry{kern, dev, bytes};
+  if (e == cudaSuccess && known) known->bytes = bytes;
+  else if (e == cudaSuccess) try {
+      table.push_back(Entry{kern, dev, bytes});
+    } catch (const std::bad_alloc &) {  // set again next time
+    }
   return e;
 }
 
