@@ -588,7 +588,7 @@ typedef struct pa_attention_args {
   int R;                      /* 0 .. 65535 */
   int q_len;                  /* 1 .. 16 */
   int bt_width;               /* 1 .. 16384 */
-  float sm_scale;             /* > 0, finite */
+  float sm_scale;             /* > 0, finite; sm_scale * log2(e) (* q_fp8_scale) (* k_global_scale) a normal f32 */
   void *out;                  /* [R * q_len, out_stride] bf16, 16-byte aligned; the span of its rows
                                  (first to last element) does not overlap that of q's */
   int64_t out_stride;         /* elements a row: a multiple of 8, >= n_q_heads * 128 */

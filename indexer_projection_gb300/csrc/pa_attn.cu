@@ -1046,6 +1046,10 @@ extern "C" int pre_attn_attention(const pa_attention_args *in, void *stream) {
       return PA_ERR_CONFIG;
     if (c.kv_page_bytes % 32 || !aligned(c.kv_cache, 32)) return PA_ERR_ALIGN;
   }
+  // what a product of scaled queries and codes is multiplied by: a normal number
+  const float score_scale = (float)((double)x.sm_scale * 1.4426950408889634 * (x.q ? 1.0 : (double)x.q_fp8_scale) *
+                                    (fp8 ? 1.0 : (double)c.k_global_scale));
+  if (!std::isnormal(score_scale)) return PA_ERR_CONFIG;
   if ((x.q && !aligned(x.q, 16)) || (x.q_fp8 && !aligned(x.q_fp8, 16)) || x.q_stride % 16 || !aligned(x.out, 16) ||
       x.out_stride % 8 || !aligned(x.block_table, 4) || !aligned(x.seq_lens, 4) || !aligned(x.blocks, 4) ||
       !aligned(x.counts, 4) || !aligned(x.status, 4))
@@ -1092,8 +1096,7 @@ extern "C" int pre_attn_attention(const pa_attention_args *in, void *stream) {
   a.rows_per = (x.q_len + a.lg_groups) >> a.lg_groups;
   a.items = x.R * x.n_kv_heads << a.lg_groups;
   a.mode = a.items <= pa::kAtMaxItems ? pa::kAtSliced : pa::kAtWhole;
-  a.score_scale = (float)((double)x.sm_scale * 1.4426950408889634 * (x.q ? 1.0 : (double)x.q_fp8_scale) *
-                          (fp8 ? 1.0 : (double)c.k_global_scale));
+  a.score_scale = score_scale;
   a.out_scale = fp8 ? 1.0f : c.v_global_scale;
   a.out = static_cast<__nv_bfloat16 *>(x.out);
   a.out_stride = x.out_stride;
