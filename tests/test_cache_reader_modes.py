@@ -163,3 +163,19 @@ def test_index_caches_beyond_32_bits(fmt):
         assert rd.device_status() == 0
         got.append(s)
     assert torch.equal(got[0], got[1]) and got[0][:, :128].abs().max() > 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows,q_len", [(45, 15), (64, 16), (39, 13)])
+def test_a_prompt_as_several_requests(fmt, rows, q_len):
+    # q_len rows each, the same row of the block table, the length up to their own last row
+    from indexer_projection_gb300.runner import CacheReader
+
+    c = ref.Case(fmt, [400 + rows], rows, 2, 8, seed=105).upload()
+    n = rows // q_len
+    rd = CacheReader(16, 2, cache_format=c.format, caches=c.caches, max_requests=n, q_len=q_len, bt_width=c.W)
+    out = torch.full((rows, 16 * 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    seq = torch.arange(400 + q_len, 400 + rows + 1, q_len, dtype=torch.int32, device="cuda")
+    rd.attend(c.dev["q"], c.dev["bt"].repeat(n, 1), seq, out)
+    assert rd.device_status() == 0
+    check(out, c)
