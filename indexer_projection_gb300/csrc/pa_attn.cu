@@ -35,16 +35,21 @@
 // its writer gives the scale 1) costs the others their bits.  The sum of the
 // weights is taken in f32 before that rounding.
 //
-// Bound and figures (one GB300, calls back to back; the floor is the bytes at
-// the measured copy rate).  Dense decode, ragged lengths up to 32768: FP8, 32
-// requests x 2 KV heads, 276 MB of blocks in 57.0 us (4.8 TB/s, 0.71 of the
-// copy rate); NVFP4, 64 x 4, 625 MB in 171 us (3.7 TB/s, 0.54).  FP8 is bound
-// by the stream and the ends of its slices; NVFP4 and several rows an item by
-// the compute warps: 750 instructions a warp for 32 keys (340 of them convert
-// codes), where two warps a scheduler reach 1.7 to 2 a clock against
-// fixed-latency waits and the ALU (35%) and tensor (34%) pipes.  Small calls
-// (8 requests on 16 blocks each: 7.1 us) are a chain of latencies: list and
-// table, first block, its products, the join.
+// Bound and figures (one GB300, calls back to back; the floor is the keys'
+// bytes at the measured copy rate).  Dense decode, ragged lengths up to 32768:
+// FP8, 32 requests x 2 KV heads, 277 MB in 57.9 us (4.8 TB/s, 0.71 of the
+// copy rate); NVFP4, 64 x 4, 606 MB in 171 us (3.6 TB/s, 0.52).  FP8 is bound
+// by the stream and the ends of its slices, NVFP4 by the compute warps: 750
+// instructions a warp for 32 keys (340 of them convert codes), where two warps
+// a scheduler reach 1.8 a clock against fixed-latency waits and the ALU (35%)
+// and tensor (35%) pipes.  Several rows on blocks of their choice (64 x 7 rows,
+// 2 KV heads, 16 blocks: FP8 76 us, NVFP4 100) wait for the ring as much as
+// they compute (FP8 1.3 instructions a clock, NVFP4 1.6): a stage is free when
+// the warps of every row have passed it, so a block of one row holds up the
+// others (none, 4 or 11 of a row's 16 blocks its own: FP8 67, 77, 98 us, NVFP4
+// 87, 100, 110, at the same products).  Small calls (8 requests on 16 blocks
+// each: 7.5 us) are a chain of latencies: list and table, first block, its
+// products, the join.
 //
 // Measured and kept out: the rows of an item as one tcgen05 tile (FP8 spec
 // rows 128 us against 77: softmax latency, instruction cache); two rows a warp

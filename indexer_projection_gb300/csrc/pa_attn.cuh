@@ -1,15 +1,14 @@
-// What the kernels of pre_attn_attention share: their parameters, the items
-// and the CTAs' shares of them, the ring of 128-key blocks with the warps that
-// fill it, and the kernel that joins partial results.
+// The producing side of pre_attn_attention: the kernels' parameters, the items
+// and the CTAs' shares of them (a cluster of CTAs an item, slices of all
+// items' blocks, or a CTA an item), and the ring of 128-key blocks with the
+// warps that fill it.
 //
 // Work.  An item is (request, up to 8 of its rows, KV head): the rows share
 // the key blocks, so a block is read from memory once for all rows that
-// attend it.  A persistent grid (a CTA an SM) walks the list of all items'
-// blocks in even contiguous slices; an item that several CTAs share leaves
-// partial sums in the workspace and pa_attn_join_kernel adds them up.  In a
-// CTA one warp works out which blocks come next, one thread keeps a ring of
-// them in flight with tensor-map copies (a copy a 2 KB page and scale row
-// took about 110 clocks each, more than the data), the others compute.
+// attend it.  In a CTA one warp works out which blocks come next, one thread
+// keeps a ring of them in flight with tensor-map copies (a copy a 2 KB page
+// and scale row took about 110 clocks each, more than the data), the others
+// compute.
 #pragma once
 
 #include <cuda_fp16.h>

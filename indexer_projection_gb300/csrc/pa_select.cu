@@ -12,9 +12,9 @@
 // to it, in block order.
 //
 // One GB300, calls back to back: 64 requests x 7 rows x 2 heads, lengths up to
-// 32767, 61 MB in 13.6 us (4.4 TB/s, 0.66 of the measured copy rate; the
+// 32767, 61 MB in 13.7 us (4.4 TB/s, 0.65 of the measured copy rate; the
 // selection behind the last loads is what is left); 3 rows x 4 heads of 131072
-// keys 6.7 us, 8 rows of up to 32768 3.7 us, latency.
+// keys 6.8 us, 8 rows of up to 32768 3.7 us, latency.
 #include <cstdint>
 
 #include "../../include/pre_attn.h"

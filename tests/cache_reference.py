@@ -3,8 +3,9 @@ indexer scores, the block selection and the attention, from the byte offsets
 that include/pre_attn.h gives, row by row, with the worst-case error that the
 kernels' arithmetic allows beside each attention value.
 
-Cache bytes that no key of a request owns hold what `stale` says ("nan":
-NaN codes and scales), so a kernel that looks at them fails.
+Cache bytes that no key of a request owns hold NaN: FP8 pages NaN scales and,
+with stale "nan", NaN codes; NVFP4 pages NaN scales and codes of -6 whatever
+`stale` says.  A kernel that looks at them fails.
 """
 
 import math
