@@ -58,7 +58,7 @@ enum pa_status {
   PA_ERR_ALIGN = 4,       /* a pointer or stride violates its alignment rule */
   PA_ERR_NO_Q_OUTPUT = 5, /* neither q output requested (epilogue page asserts one) */
   PA_ERR_NO_IQ_OUTPUT = 6,/* neither index_q output requested */
-  PA_ERR_ALIAS = 7,       /* residual_out overlaps ar or res (not supported) */
+  PA_ERR_ALIAS = 7,       /* an output overlaps a tensor that it may not (not supported) */
   PA_ERR_WORKSPACE = 8,   /* workspace NULL or smaller than pre_attn_workspace_bytes */
   PA_ERR_CUDA = 9,        /* a CUDA runtime call failed (launch, attribute, query) */
   PA_ERR_UNSUPPORTED = 10 /* a valid request this build does not implement */
@@ -68,7 +68,9 @@ enum pa_status {
 enum pa_device_status {
   PA_DEV_SLOT_RANGE = 1u << 0,  /* a slot pointed outside its cache: store skipped */
   PA_DEV_POS_RANGE = 1u << 1,   /* a position outside [0, max_pos): clamped */
-  PA_DEV_WAIT_TIMEOUT = 1u << 2 /* a bounded device wait gave up (results invalid) */
+  PA_DEV_WAIT_TIMEOUT = 1u << 2, /* a bounded device wait gave up (results invalid) */
+  PA_DEV_TOKEN_RANGE = 1u << 3, /* a drafted token outside the vocabulary: rejected */
+  PA_DEV_NO_TOKEN = 1u << 4     /* a row of probabilities without any: no token drawn */
 };
 
 /* ---------------------------------------------------------- formats */
@@ -99,6 +101,9 @@ enum pa_cache_format {
    * (t/4*4 + g/2)*8 + (g%2)*4 + t%4.  The index cache has one slot per page. */
   PA_CACHE_NVFP4 = 1
 };
+
+/* Types of probabilities (pre_attn_verify_drafts). */
+enum pa_prob_type { PA_PROB_F32 = 0, PA_PROB_BF16 = 1 };
 
 enum pa_flags {
   PA_FLAG_STATIC_KV_SCALE = 1 << 0, /* FP8 caches: K / V scales fixed at 1 */
@@ -613,6 +618,102 @@ size_t pre_attn_attention_workspace_bytes(int R, int q_len, int n_kv_heads, int 
  * PA_ERR_ALIGN, PA_ERR_ALIAS (out overlaps q), PA_ERR_WORKSPACE,
  * PA_ERR_UNSUPPORTED (block_size, as above); PA_ERR_CUDA if a launch fails. */
 int pre_attn_attention(const pa_attention_args *args, void *stream);
+
+/* ------------------------------------------- eviction from the caches
+ *
+ * What keeps a request's caches within a budget of page-128 blocks: the
+ * blocks with the least accumulated attention weight leave its row of the
+ * block table.  The pages have no counterpart; this is the definition.  A
+ * request with n = seq_lens[r] keys has nb = (n + 127) / 128 blocks.  With
+ * nb > keep, nb - keep of them are evicted: of those that are not pinned (the
+ * first init_blocks, the last max(local_blocks, 1)) the ones with the smallest
+ * weights[r][b], a NaN counting as -inf; of equal ones the higher block goes
+ * first (the order in which pre_attn_select_blocks prefers blocks).  Then
+ *   - the row of the block table and the row of weights lose the evicted
+ *     entries, what stands behind them (entries from nb on included) moves up
+ *     in its order, and the last nb - keep entries become -1 and 0;
+ *   - seq_lens_out[r] = n - 128 * (nb - keep): the remaining keys keep their
+ *     order and their places in their blocks, so that reads of the caches and
+ *     slots of new keys go on from the new row and length (a key keeps the
+ *     rotary position that it was written with);
+ *   - evicted[r] gets the evicted table entries in block order, then -1 up to
+ *     bt_width; counts[r] how many there are.
+ * Otherwise (nb <= keep, seq_lens[r] < 1, or nb > bt_width, which raises
+ * PA_DEV_SLOT_RANGE) the row and the length are copied and nothing is evicted.
+ * Each output may be its own input (in place); no other overlap. */
+typedef struct pa_evict_args {
+  const float *weights;       /* [R, weights_stride] f32: a block's accumulated weight (pre_attn_attention_ext) */
+  int64_t weights_stride;     /* floats a row: >= bt_width */
+  const int32_t *block_table; /* [R, bt_width] page-128 block ids */
+  const int32_t *seq_lens;    /* [R] */
+  int R;                      /* requests, 0 .. 65535 */
+  int bt_width;               /* 1 .. 16384 */
+  int keep;                   /* blocks a request keeps: >= init_blocks + max(local_blocks, 1) */
+  int init_blocks;            /* first blocks that stay */
+  int local_blocks;           /* last blocks that stay (at least one does) */
+  float *weights_out;         /* [R, weights_out_stride] */
+  int64_t weights_out_stride; /* >= bt_width; that of weights in place */
+  int32_t *block_table_out;   /* [R, bt_width] */
+  int32_t *seq_lens_out;      /* [R] */
+  int32_t *evicted;           /* [R, bt_width] */
+  int32_t *counts;            /* [R] */
+  uint32_t *status;           /* device status word: PA_DEV_SLOT_RANGE */
+} pa_evict_args;
+
+/* Evict on `stream`, after the previous kernel on it (programmatic dependent
+ * launch).  Allocates nothing, never synchronises.  Errors (nothing launched):
+ * PA_ERR_NULL, PA_ERR_SHAPE, PA_ERR_CONFIG (negative block counts, a keep
+ * below the pinned blocks), PA_ERR_ALIGN (4 bytes), PA_ERR_ALIAS (overlaps
+ * other than in place); PA_ERR_CUDA if the launch fails. */
+int pre_attn_evict_blocks(const pa_evict_args *args, void *stream);
+
+/* ------------------------------------------- verification of drafted tokens
+ *
+ * What ends a speculative step: request r has q_len rows of the target's
+ * probabilities, row i for the token after its i-th row's, and q_len - 1
+ * drafted tokens x_i with the drafter's probabilities q_i.  The pages have no
+ * counterpart; this is the definition.  A negative x_i ends the request's
+ * drafts: k_r of them come before it (q_len - 1 without one).  With uniforms
+ * u in [0, 1), draft i < k_r is accepted if u[r][i] * q_i(x_i) < p_i(x_i) (in
+ * exact arithmetic; never if p_i(x_i) is no number), and a_r is the number of
+ * drafts before the first that is not.  Then one token more is drawn, from
+ *   w(v) = max(p_a(v) - q_a(v), 0)   if a draft was rejected (a_r < k_r),
+ *   w(v) = p_a(v)                    otherwise, or if that is 0 everywhere:
+ * the first v whose running sum of w exceeds u[r][q_len - 1] times the sum of
+ * all.  So the tokens are distributed as the target's own.  Without q (a
+ * drafter that is certain of its drafts) q_i is 1 at x_i and w is p_a without
+ * x_a.  For w a probability counts as min(max(p, 0), 1), a NaN as 0, and what
+ * it has below 2^-62 is dropped; the sums are exact, in 64-bit integers, so
+ * the token does not depend on how the work is split (a row whose values sum to 4 or
+ * more, which no row of probabilities does, draws any token or none).
+ * An x_i >= vocab is never accepted and raises PA_DEV_TOKEN_RANGE (without q,
+ * w is then p_a).  A row without any probability draws no token: -1, and
+ * PA_DEV_NO_TOKEN.  tokens[r] gets the accepted drafts, the drawn token, then
+ * -1 up to q_len; accepted[r] is a_r. */
+typedef struct pa_verify_args {
+  const void *target;         /* [R * q_len, target_stride] probabilities */
+  int64_t target_stride;      /* elements a row: >= vocab */
+  int target_type;            /* enum pa_prob_type */
+  const void *draft_probs;    /* [R * (q_len - 1), draft_stride], or NULL: certain drafts */
+  int64_t draft_stride;       /* >= vocab, with draft_probs */
+  int draft_type;             /* enum pa_prob_type, with draft_probs */
+  const int32_t *drafts;      /* [R, q_len - 1]; unused for q_len 1 */
+  const float *uniforms;      /* [R, q_len]: one a draft, the last for the drawn token; below 0 (or NaN) counts as 0
+                                 there and 1 or above as the largest number below 1 */
+  int R;                      /* requests, 0 .. 65535 */
+  int q_len;                  /* rows a request, 1 .. 16 */
+  int vocab;                  /* 1 .. 2^24 */
+  int32_t *tokens;            /* [R, q_len] */
+  int32_t *accepted;          /* [R] */
+  uint32_t *status;           /* device status word: PA_DEV_TOKEN_RANGE, PA_DEV_NO_TOKEN */
+} pa_verify_args;
+
+/* Verify on `stream`, after the previous kernel on it (programmatic dependent
+ * launch).  Allocates nothing, never synchronises.  Errors (nothing launched):
+ * PA_ERR_NULL, PA_ERR_SHAPE, PA_ERR_CONFIG (an unknown type), PA_ERR_ALIGN (an
+ * element; 4 bytes for the rest), PA_ERR_ALIAS (an output overlaps another
+ * tensor); PA_ERR_CUDA if the launch fails. */
+int pre_attn_verify_drafts(const pa_verify_args *args, void *stream);
 
 /* Main kernels a call can run (pre_attn_path). */
 enum {

@@ -22,7 +22,8 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "pre_attn.h")
 PA_OK, PA_ERR_NULL, PA_ERR_CONFIG, PA_ERR_SHAPE, PA_ERR_ALIGN = 0, 1, 2, 3, 4
 PA_ERR_NO_Q_OUTPUT, PA_ERR_NO_IQ_OUTPUT, PA_ERR_ALIAS, PA_ERR_WORKSPACE = 5, 6, 7, 8
 PA_ERR_CUDA, PA_ERR_UNSUPPORTED = 9, 10
-PA_DEV_SLOT_RANGE, PA_DEV_POS_RANGE, PA_DEV_WAIT_TIMEOUT = 1, 2, 4
+PA_DEV_SLOT_RANGE, PA_DEV_POS_RANGE, PA_DEV_WAIT_TIMEOUT, PA_DEV_TOKEN_RANGE, PA_DEV_NO_TOKEN = 1, 2, 4, 8, 16
+PA_PROB_F32, PA_PROB_BF16 = 0, 1
 PA_WEIGHT_FP8_PER_CHANNEL, PA_WEIGHT_MXFP8 = 0, 1
 PA_CACHE_FP8, PA_CACHE_NVFP4 = 0, 1
 PA_FLAG_STATIC_KV_SCALE, PA_FLAG_FORCE_GEMV, PA_FLAG_FORCE_GEMM, PA_FLAG_NO_PDL = 1, 2, 4, 8
@@ -111,6 +112,20 @@ class pa_attention_args(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t), ("status", _vp), ("flags", ctypes.c_uint32)]
 
 
+class pa_evict_args(ctypes.Structure):
+    _fields_ = [("weights", _vp), ("weights_stride", ctypes.c_int64), ("block_table", _vp), ("seq_lens", _vp),
+                ("R", ctypes.c_int), ("bt_width", ctypes.c_int), ("keep", ctypes.c_int), ("init_blocks", ctypes.c_int),
+                ("local_blocks", ctypes.c_int), ("weights_out", _vp), ("weights_out_stride", ctypes.c_int64),
+                ("block_table_out", _vp), ("seq_lens_out", _vp), ("evicted", _vp), ("counts", _vp), ("status", _vp)]
+
+
+class pa_verify_args(ctypes.Structure):
+    _fields_ = [("target", _vp), ("target_stride", ctypes.c_int64), ("target_type", ctypes.c_int),
+                ("draft_probs", _vp), ("draft_stride", ctypes.c_int64), ("draft_type", ctypes.c_int), ("drafts", _vp),
+                ("uniforms", _vp), ("R", ctypes.c_int), ("q_len", ctypes.c_int), ("vocab", ctypes.c_int),
+                ("tokens", _vp), ("accepted", _vp), ("status", _vp)]
+
+
 class PreAttnError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -158,6 +173,8 @@ def load(path: str = LIB_PATH):
         "pre_attn_select_blocks": (i, [ctypes.POINTER(pa_select_args), _vp]),
         "pre_attn_attention_workspace_bytes": (sz, [i, i, i, i]),
         "pre_attn_attention": (i, [ctypes.POINTER(pa_attention_args), _vp]),
+        "pre_attn_evict_blocks": (i, [ctypes.POINTER(pa_evict_args), _vp]),
+        "pre_attn_verify_drafts": (i, [ctypes.POINTER(pa_verify_args), _vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
@@ -341,6 +358,20 @@ def pre_attn_attention(args: pa_attention_args, stream=None, check: bool = True)
     st = load().pre_attn_attention(ctypes.byref(args), stream_ptr(stream))
     if check and st != PA_OK:
         raise PreAttnError(st, "pre_attn_attention " + (pre_attn_last_cuda_error() if st == PA_ERR_CUDA else ""))
+    return st
+
+
+def pre_attn_evict_blocks(args: pa_evict_args, stream=None, check: bool = True) -> int:
+    st = load().pre_attn_evict_blocks(ctypes.byref(args), stream_ptr(stream))
+    if check and st != PA_OK:
+        raise PreAttnError(st, "pre_attn_evict_blocks " + (pre_attn_last_cuda_error() if st == PA_ERR_CUDA else ""))
+    return st
+
+
+def pre_attn_verify_drafts(args: pa_verify_args, stream=None, check: bool = True) -> int:
+    st = load().pre_attn_verify_drafts(ctypes.byref(args), stream_ptr(stream))
+    if check and st != PA_OK:
+        raise PreAttnError(st, "pre_attn_verify_drafts " + (pre_attn_last_cuda_error() if st == PA_ERR_CUDA else ""))
     return st
 
 

@@ -22,6 +22,8 @@ constexpr float kFp8Max = 448.0f;
 constexpr uint32_t kDevSlotRange = 1u << 0;
 constexpr uint32_t kDevPosRange = 1u << 1;
 constexpr uint32_t kDevWaitTimeout = 1u << 2;
+constexpr uint32_t kDevTokenRange = 1u << 3;
+constexpr uint32_t kDevNoToken = 1u << 4;
 
 // Everything a kernel of the step reads or writes.  Passed by value.
 struct Params {

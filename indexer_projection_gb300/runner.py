@@ -83,95 +83,40 @@ class PreAttn:
         return B.pre_attn_device_status(self.workspace, stream)
 
 
-class CacheReader:
-    """What a layer reads back of its caches: the indexer scores, the block
-    selection and the attention, for up to ``max_requests`` requests of
-    ``q_len`` rows whose block tables hold ``bt_width`` page-128 blocks.
+class _Calls:
+    """What the front ends below share: a device, a workspace that begins with a status word, and the calls' streams."""
 
-    ``caches`` is PreAttn.fp8_caches(...) or PreAttn.nvfp4_caches(...), read at
-    every call (and may be replaced by another of the same format): the fields
-    that a call reads have to be set (the index cache for ``index_scores``, the
-    K / V ones for ``attend``) and their tensors kept alive by the caller.  Owns a workspace, a status word and the calls'
-    argument structs: one host thread uses a reader at a time, and its calls,
-    replays of captured ones among them, are ordered on the GPU by their
-    stream, or by the caller (calls that may run together take a reader each).
-    Every tensor is on ``device``; seq_lens, block tables, block lists and
-    counts are contiguous int32, scores and query rows have contiguous columns.
-    A call without requests does nothing.  Making a reader waits for the
-    current stream (its status word is cleared there, for calls on any stream),
-    so it is made outside a capture.  A reader may be dropped while its calls
-    run (its workspace is not reused before them), but has to outlive the
-    graphs that hold captured ones.
-    """
-
-    def __init__(self, n_q_heads: int, n_kv_heads: int, *, cache_format: int, caches: B.pa_caches, max_requests: int,
-                 q_len: int, bt_width: int, topk: int = 0, init_blocks: int = 0, local_blocks: int = 0,
-                 block_size: int = 16, kv_page_stride: int = 0, sm_scale: float = 128 ** -0.5, flags: int = 0,
-                 device: torch.device | str | None = None):
+    def _take_device(self, device):
         self.device = torch.device("cuda" if device is None else device)
         if self.device.type != "cuda":
             raise ValueError(f"a CUDA device is wanted, not {self.device}")
-        lib = B.load()
+        B.load()
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self.index = self.device.index
-        self.n_q_heads, self.n_kv_heads, self.cache_format = n_q_heads, n_kv_heads, cache_format
-        self.max_requests, self.q_len, self.bt_width, self.topk = max_requests, q_len, bt_width, topk
-        self.init_blocks, self.local_blocks, self.block_size = init_blocks, local_blocks, block_size
-        self.index_scale = B.pre_attn_index_scale_log2e(sm_scale)
-        sms = torch.cuda.get_device_properties(self.device).multi_processor_count
-        self.ws_bytes = B.pre_attn_attention_workspace_bytes(max_requests, q_len, n_kv_heads, sms)
-        if self.ws_bytes == 0:
-            raise ValueError(f"max_requests {max_requests}, q_len {q_len} or n_kv_heads {n_kv_heads} out of range")
-        # the first 256 bytes hold the status word
+
+    def _take_workspace(self, nbytes):
+        """``nbytes`` behind the 256 bytes that hold the status word, which is clear when this returns."""
         with torch.cuda.device(self.device):
             if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("a CacheReader is made outside a capture")
-            self.workspace = torch.empty(256 + self.ws_bytes, dtype=torch.uint8, device=self.device)
+                raise RuntimeError(f"a {type(self).__name__} is made outside a capture")
+            self.workspace = torch.empty(256 + nbytes, dtype=torch.uint8, device=self.device)
             made_on = torch.cuda.current_stream()
             B.pre_attn_workspace_init(self.workspace, 256, made_on)
             made_on.synchronize()
         self.status = self.workspace.data_ptr()
         self._made_on = made_on.cuda_stream
         self._used_on = set()  # streams of its calls
-        # the calls' argument structs, of which a call sets what changes
-        self._attn = B.pa_attention_args(None, None, 1.0, 0, n_q_heads, n_kv_heads, cache_format, block_size,
-                                         kv_page_stride, None, None, None, None, None, topk, 0, q_len,
-                                         bt_width, sm_scale, None, 0, self.status + 256, self.ws_bytes, self.status,
-                                         flags)
-        self.caches = caches
-        self._select = B.pa_select_args(None, 0, 0, 0, None, 0, q_len, bt_width, init_blocks, local_blocks, topk, None,
-                                        None, self.status, None, 0)
-        if cache_format == B.PA_CACHE_FP8:
-            self._scores = B.pa_index_args(None, 0, 0, caches.index_cache, caches.num_index_slots, None, None, 0, q_len,
-                                           bt_width, init_blocks, local_blocks, 0.0, None, 0, self.status, 0)
-            name = "pre_attn_index_scores"
-        else:
-            self._scores = B.pa_index_nvfp4_args(None, 0, 0, caches.idx_cache, caches.idx_pages, caches.idx_page_bytes,
-                                                 block_size, None, None, 0, q_len, bt_width, init_blocks, local_blocks, 0.0,
-                                                 None, 0, self.status)
-            name = "pre_attn_index_scores_nvfp4"
-        self._scores_entry = getattr(lib, name), B.ctypes.byref(self._scores), name
-        self._select_entry = lib.pre_attn_select_blocks, B.ctypes.byref(self._select), "pre_attn_select_blocks"
-        self._attn_entry = lib.pre_attn_attention, B.ctypes.byref(self._attn), "pre_attn_attention"
-
-    @property
-    def caches(self) -> B.pa_caches:
-        return self._caches
-
-    @caches.setter
-    def caches(self, caches: B.pa_caches):
-        self._caches, self._attn.caches = caches, B.ctypes.pointer(caches)
 
     def _on(self, stream):
-        """The stream of a call: the reader's device has to be the current one, and the stream's."""
+        """The stream of a call: the front end's device has to be the current one, and the stream's."""
         if torch._C._cuda_getDevice() != self.index:
-            raise ValueError(f"the current device is not the reader's ({self.device})")
+            raise ValueError(f"the current device is not the {self._name}'s ({self.device})")
         if stream is None:
             s = torch._C._cuda_getCurrentRawStream(self.index)
         else:
             if getattr(stream, "device_index", self.index) != self.index:
-                raise ValueError(f"the stream is of another device than the reader's ({self.device})")
+                raise ValueError(f"the stream is of another device than the {self._name}'s ({self.device})")
             s = B.stream_ptr(stream)
         self._used_on.add(s)
         return s
@@ -193,15 +138,6 @@ class CacheReader:
             raise B.PreAttnError(st, name + " " + (B.pre_attn_last_cuda_error() if st == B.PA_ERR_CUDA else ""))
         return st
 
-    def _requests(self, seq_lens, block_table=None) -> int:
-        R = seq_lens.shape[0]
-        if R > self.max_requests:
-            raise ValueError(f"{R} requests: the reader holds {self.max_requests}")
-        self._ints(seq_lens, (R,), "seq_lens")
-        if block_table is not None:
-            self._ints(block_table, (R, self.bt_width), "block_table")
-        return R
-
     def _ints(self, x, shape, name):
         if x.dtype is not torch.int32 or x.shape != shape or not x.is_contiguous() or x.get_device() != self.index:
             raise ValueError(f"{name}: a contiguous int32 tensor of shape {shape} on {self.device} is wanted")
@@ -213,6 +149,90 @@ class CacheReader:
             raise ValueError(f"{name}: [{rows}, >= {cols}] with contiguous columns on {self.device} is wanted, not "
                              f"{x.dtype} {tuple(shape)} on {x.device}")
         return stride[0] if rows > 1 else cols  # elements a row (a single row's stride says nothing)
+
+    def device_status(self, stream=None) -> int:
+        """PA_DEV_* bits of the calls since the last reading (read and cleared; synchronises)."""
+        return B.pre_attn_device_status(self.workspace, self._on(stream))
+
+
+class CacheReader(_Calls):
+    """What a layer reads back of its caches: the indexer scores, the block
+    selection and the attention, for up to ``max_requests`` requests of
+    ``q_len`` rows whose block tables hold ``bt_width`` page-128 blocks.
+
+    ``caches`` is PreAttn.fp8_caches(...) or PreAttn.nvfp4_caches(...), read at
+    every call (and may be replaced by another of the same format): the fields
+    that a call reads have to be set (the index cache for ``index_scores``, the
+    K / V ones for ``attend``) and their tensors kept alive by the caller.  Owns a workspace, a status word and the calls'
+    argument structs: one host thread uses a reader at a time, and its calls,
+    replays of captured ones among them, are ordered on the GPU by their
+    stream, or by the caller (calls that may run together take a reader each).
+    Every tensor is on ``device``; seq_lens, block tables, block lists and
+    counts are contiguous int32, scores and query rows have contiguous columns.
+    A call without requests does nothing.  Making a reader waits for the
+    current stream (its status word is cleared there, for calls on any stream),
+    so it is made outside a capture.  A reader may be dropped while its calls
+    run (its workspace is not reused before them), but has to outlive the
+    graphs that hold captured ones.
+    """
+
+    _name = "reader"
+
+    def __init__(self, n_q_heads: int, n_kv_heads: int, *, cache_format: int, caches: B.pa_caches, max_requests: int,
+                 q_len: int, bt_width: int, topk: int = 0, init_blocks: int = 0, local_blocks: int = 0,
+                 block_size: int = 16, kv_page_stride: int = 0, sm_scale: float = 128 ** -0.5, flags: int = 0,
+                 device: torch.device | str | None = None):
+        self._take_device(device)
+        lib = B.load()
+        self.n_q_heads, self.n_kv_heads, self.cache_format = n_q_heads, n_kv_heads, cache_format
+        self.max_requests, self.q_len, self.bt_width, self.topk = max_requests, q_len, bt_width, topk
+        self.init_blocks, self.local_blocks, self.block_size = init_blocks, local_blocks, block_size
+        self.index_scale = B.pre_attn_index_scale_log2e(sm_scale)
+        sms = torch.cuda.get_device_properties(self.device).multi_processor_count
+        self.ws_bytes = B.pre_attn_attention_workspace_bytes(max_requests, q_len, n_kv_heads, sms)
+        if self.ws_bytes == 0:
+            raise ValueError(f"max_requests {max_requests}, q_len {q_len} or n_kv_heads {n_kv_heads} out of range")
+        self._take_workspace(self.ws_bytes)
+        # the calls' argument structs, of which a call sets what changes
+        self._attn = B.pa_attention_args(None, None, 1.0, 0, n_q_heads, n_kv_heads, cache_format, block_size,
+                                         kv_page_stride, None, None, None, None, None, topk, 0, q_len,
+                                         bt_width, sm_scale, None, 0, self.status + 256, self.ws_bytes, self.status,
+                                         flags)
+        self.caches = caches
+        self._select = B.pa_select_args(None, 0, 0, 0, None, 0, q_len, bt_width, init_blocks, local_blocks, topk, None,
+                                        None, self.status, None, 0)
+        if cache_format == B.PA_CACHE_FP8:
+            self._scores = B.pa_index_args(None, 0, 0, caches.index_cache, caches.num_index_slots, None, None, 0, q_len,
+                                           bt_width, init_blocks, local_blocks, 0.0, None, 0, self.status, 0)
+            name = "pre_attn_index_scores"
+        else:
+            self._scores = B.pa_index_nvfp4_args(None, 0, 0, caches.idx_cache, caches.idx_pages, caches.idx_page_bytes,
+                                                 block_size, None, None, 0, q_len, bt_width, init_blocks, local_blocks, 0.0,
+                                                 None, 0, self.status)
+            name = "pre_attn_index_scores_nvfp4"
+        self._scores_entry = getattr(lib, name), B.ctypes.byref(self._scores), name
+        self._select_entry = lib.pre_attn_select_blocks, B.ctypes.byref(self._select), "pre_attn_select_blocks"
+        self._attn_entry = lib.pre_attn_attention, B.ctypes.byref(self._attn), "pre_attn_attention"
+        self._evict = B.pa_evict_args(None, 0, None, None, 0, bt_width, 0, init_blocks, local_blocks, None, 0, None, None,
+                                      None, None, self.status)
+        self._evict_entry = lib.pre_attn_evict_blocks, B.ctypes.byref(self._evict), "pre_attn_evict_blocks"
+
+    @property
+    def caches(self) -> B.pa_caches:
+        return self._caches
+
+    @caches.setter
+    def caches(self, caches: B.pa_caches):
+        self._caches, self._attn.caches = caches, B.ctypes.pointer(caches)
+
+    def _requests(self, seq_lens, block_table=None) -> int:
+        R = seq_lens.shape[0]
+        if R > self.max_requests:
+            raise ValueError(f"{R} requests: the reader holds {self.max_requests}")
+        self._ints(seq_lens, (R,), "seq_lens")
+        if block_table is not None:
+            self._ints(block_table, (R, self.bt_width), "block_table")
+        return R
 
     def index_scores(self, iq, head: int, block_table, seq_lens, scores, *, scale: float | None = None, stream=None,
                      check: bool = True) -> int:
@@ -286,6 +306,78 @@ class CacheReader:
             return B.PA_OK
         return self._call(self._attn_entry, stream, check)
 
-    def device_status(self, stream=None) -> int:
-        """PA_DEV_* bits of the calls since the last reading (read and cleared; synchronises)."""
-        return B.pre_attn_device_status(self.workspace, self._on(stream))
+    def evict_blocks(self, weights, block_table, seq_lens, evicted, counts, *, keep: int, weights_out=None,
+                     block_table_out=None, seq_lens_out=None, stream=None, check: bool = True) -> int:
+        """Each request's blocks down to ``keep``: the first ``init_blocks`` and the last max(``local_blocks``, 1) stay
+        and of the others those with the largest weights [R, >= bt_width] (f32).  The block table, the lengths and the
+        weights without the evicted blocks go to the outputs (None: in place), the evicted table entries to evicted
+        [R, bt_width], -1 behind the last, and how many there are to counts [R]."""
+        R, a, W = self._requests(seq_lens, block_table), self._evict, self.bt_width
+        a.weights_stride = self._rows(weights, weights.dtype is torch.float32, R, W, "weights")
+        a.weights, a.block_table, a.seq_lens = weights.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr()
+        a.weights_out, a.weights_out_stride = a.weights, a.weights_stride
+        a.block_table_out, a.seq_lens_out = a.block_table, a.seq_lens
+        if weights_out is not None:
+            a.weights_out_stride = self._rows(weights_out, weights_out.dtype is torch.float32, R, W, "weights_out")
+            a.weights_out = weights_out.data_ptr()
+        if block_table_out is not None:
+            self._ints(block_table_out, (R, W), "block_table_out")
+            a.block_table_out = block_table_out.data_ptr()
+        if seq_lens_out is not None:
+            self._ints(seq_lens_out, (R,), "seq_lens_out")
+            a.seq_lens_out = seq_lens_out.data_ptr()
+        self._ints(evicted, (R, W), "evicted")
+        self._ints(counts, (R,), "counts")
+        a.evicted, a.counts, a.R, a.keep = evicted.data_ptr(), counts.data_ptr(), R, keep
+        if R == 0:
+            return B.PA_OK
+        return self._call(self._evict_entry, stream, check)
+
+
+class DraftVerifier(_Calls):
+    """The end of a speculative step: drafted tokens against the target's
+    probabilities over ``vocab`` tokens, for requests of ``q_len`` rows
+    (``q_len - 1`` drafts and one token more).
+
+    Owns a status word and the call's argument struct: one host thread uses a
+    verifier at a time (calls on several streams may run together).  Every
+    tensor is on ``device``.  Making one waits for the current stream, so it is
+    made outside a capture; it has to outlive the graphs that hold its calls.
+    """
+
+    _name = "verifier"
+    _types = {torch.float32: B.PA_PROB_F32, torch.bfloat16: B.PA_PROB_BF16}
+
+    def __init__(self, vocab: int, q_len: int, *, device: torch.device | str | None = None):
+        self._take_device(device)
+        if not (1 <= vocab <= 1 << 24 and 1 <= q_len <= 16):
+            raise ValueError(f"vocab {vocab} or q_len {q_len} out of range")
+        self.vocab, self.q_len = vocab, q_len
+        self._take_workspace(0)
+        self._args = B.pa_verify_args(None, 0, 0, None, 0, 0, None, None, 0, q_len, vocab, None, None, self.status)
+        self._entry = B.load().pre_attn_verify_drafts, B.ctypes.byref(self._args), "pre_attn_verify_drafts"
+
+    def verify(self, target, drafts, uniforms, tokens, accepted, *, draft_probs=None, stream=None,
+               check: bool = True) -> int:
+        """target [R * q_len, >= vocab] and draft_probs [R * (q_len - 1), >= vocab] (f32 or bf16; None: the drafter is
+        certain), drafts [R, q_len - 1] int32 (negative: no more drafts), uniforms [R, q_len] f32 in [0, 1) into tokens
+        [R, q_len] int32 (accepted drafts, one token more, -1) and accepted [R] int32 (how many drafts)."""
+        a, k = self._args, self.q_len - 1
+        R = accepted.shape[0] if accepted.dim() == 1 else -1
+        self._ints(accepted, (R,), "accepted")
+        self._ints(tokens, (R, self.q_len), "tokens")
+        self._ints(drafts, (R, k), "drafts")
+        if (uniforms.dtype is not torch.float32 or uniforms.shape != (R, self.q_len) or not uniforms.is_contiguous()
+                or uniforms.get_device() != self.index):
+            raise ValueError(f"uniforms: a contiguous f32 tensor of shape {(R, self.q_len)} on {self.device} is wanted")
+        a.target_stride = self._rows(target, target.dtype in self._types, R * self.q_len, self.vocab, "target")
+        a.target_type, a.target = self._types[target.dtype], target.data_ptr()
+        a.draft_probs = None
+        if draft_probs is not None and k:
+            a.draft_stride = self._rows(draft_probs, draft_probs.dtype in self._types, R * k, self.vocab, "draft_probs")
+            a.draft_type, a.draft_probs = self._types[draft_probs.dtype], draft_probs.data_ptr()
+        a.drafts, a.uniforms, a.R = drafts.data_ptr() or None, uniforms.data_ptr(), R
+        a.tokens, a.accepted = tokens.data_ptr(), accepted.data_ptr()
+        if R == 0:
+            return B.PA_OK
+        return self._call(self._entry, stream, check)
