@@ -619,6 +619,47 @@ size_t pre_attn_attention_workspace_bytes(int R, int q_len, int n_kv_heads, int 
  * PA_ERR_UNSUPPORTED (block_size, as above); PA_ERR_CUDA if a launch fails. */
 int pre_attn_attention(const pa_attention_args *args, void *stream);
 
+/* Within a sliding window, and the blocks' weights.  pre_attn_attention_ext
+ * is pre_attn_attention with either or both of
+ *   - a window: the row at position p sees key j <= p if j > p - window or
+ *     j < sinks (the request's first keys stay visible to every row);
+ *     sinks 0 is a plain sliding window, a window of bt_width * 128 or more
+ *     none.  Other keys are not looked at, whatever the caches and the block
+ *     table hold there.  Not together with `blocks`;
+ *   - weights: for each request and block b < nb = (seq_lens[r] + 127) / 128
+ *       weights[r][b] = decay * weights_before[r][b] + the softmax weights of
+ *                       b's keys, summed over the request's rows and all
+ *                       query heads (of a step's rows and heads: q_len *
+ *                       n_q_heads in all, where every row has a key),
+ *     and 0 for nb <= b < bt_width; the sums are f32.  With weights_before NULL or decay 0
+ *     nothing is read there.  It may be weights itself (in place), so that
+ *     calls of one layer after the other add up; the row of a request without
+ *     keys is not written. */
+typedef struct pa_attention_ext {
+  int window;                  /* keys a row sees, its own among them; 0: every key */
+  int sinks;                   /* first keys that every row sees, with a window */
+  float *weights;              /* [R, weights_stride] f32, or NULL; apart from q and out */
+  int64_t weights_stride;      /* floats a row: >= bt_width */
+  const float *weights_before; /* [R, before_stride], NULL, or weights with its stride; no other overlap */
+  int64_t before_stride;       /* >= bt_width */
+  float decay;                 /* >= 0, finite: 1 adds up, less forgets */
+  void *workspace;             /* with weights: pre_attn_attention_weights_bytes() of scratch, 256-byte aligned, as the
+                                  attention's own */
+  size_t workspace_bytes;
+} pa_attention_ext;
+
+/* Scratch bytes of a call with weights of these sizes (one number a block, row
+ * and head; up to four where few rows share a block).  Host arithmetic; 0 for
+ * arguments out of range. */
+size_t pre_attn_attention_weights_bytes(int R, int q_len, int n_q_heads, int n_kv_heads, int bt_width);
+
+/* Run it on `stream`: the kernels of pre_attn_attention and, with weights, one
+ * that turns the blocks' sums into weights.  Errors: those of
+ * pre_attn_attention for args; PA_ERR_NULL (ext), PA_ERR_CONFIG (negative
+ * window or sinks, sinks without a window, decay), PA_ERR_UNSUPPORTED (a window
+ * with blocks), PA_ERR_SHAPE, PA_ERR_ALIGN, PA_ERR_ALIAS, PA_ERR_WORKSPACE. */
+int pre_attn_attention_ext(const pa_attention_args *args, const pa_attention_ext *ext, void *stream);
+
 /* ------------------------------------------- eviction from the caches
  *
  * What keeps a request's caches within a budget of page-128 blocks: the

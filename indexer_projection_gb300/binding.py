@@ -112,6 +112,12 @@ class pa_attention_args(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t), ("status", _vp), ("flags", ctypes.c_uint32)]
 
 
+class pa_attention_ext(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int), ("sinks", ctypes.c_int), ("weights", _vp), ("weights_stride", ctypes.c_int64),
+                ("weights_before", _vp), ("before_stride", ctypes.c_int64), ("decay", ctypes.c_float), ("workspace", _vp),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 class pa_evict_args(ctypes.Structure):
     _fields_ = [("weights", _vp), ("weights_stride", ctypes.c_int64), ("block_table", _vp), ("seq_lens", _vp),
                 ("R", ctypes.c_int), ("bt_width", ctypes.c_int), ("keep", ctypes.c_int), ("init_blocks", ctypes.c_int),
@@ -173,6 +179,8 @@ def load(path: str = LIB_PATH):
         "pre_attn_select_blocks": (i, [ctypes.POINTER(pa_select_args), _vp]),
         "pre_attn_attention_workspace_bytes": (sz, [i, i, i, i]),
         "pre_attn_attention": (i, [ctypes.POINTER(pa_attention_args), _vp]),
+        "pre_attn_attention_weights_bytes": (sz, [i, i, i, i, i]),
+        "pre_attn_attention_ext": (i, [ctypes.POINTER(pa_attention_args), ctypes.POINTER(pa_attention_ext), _vp]),
         "pre_attn_evict_blocks": (i, [ctypes.POINTER(pa_evict_args), _vp]),
         "pre_attn_verify_drafts": (i, [ctypes.POINTER(pa_verify_args), _vp]),
     }
@@ -358,6 +366,17 @@ def pre_attn_attention(args: pa_attention_args, stream=None, check: bool = True)
     st = load().pre_attn_attention(ctypes.byref(args), stream_ptr(stream))
     if check and st != PA_OK:
         raise PreAttnError(st, "pre_attn_attention " + (pre_attn_last_cuda_error() if st == PA_ERR_CUDA else ""))
+    return st
+
+
+def pre_attn_attention_weights_bytes(R: int, q_len: int, n_q_heads: int, n_kv_heads: int, bt_width: int) -> int:
+    return int(load().pre_attn_attention_weights_bytes(int(R), int(q_len), int(n_q_heads), int(n_kv_heads), int(bt_width)))
+
+
+def pre_attn_attention_ext(args: pa_attention_args, ext: pa_attention_ext, stream=None, check: bool = True) -> int:
+    st = load().pre_attn_attention_ext(ctypes.byref(args), ctypes.byref(ext), stream_ptr(stream))
+    if check and st != PA_OK:
+        raise PreAttnError(st, "pre_attn_attention_ext " + (pre_attn_last_cuda_error() if st == PA_ERR_CUDA else ""))
     return st
 
 

@@ -69,6 +69,10 @@ struct CacheAttnParams {
   uint32_t *status;
   uint64_t lim;
   int test_timeout;
+  // pre_attn_attention_ext (kernels of EXT)
+  int window, sinks;                 // 0: every key; keys a row sees, first keys that every row sees
+  float *wpart;                      // or null: log2 of the blocks' sums of weights, [row][KV head][block][part][head]
+  int lg_heads;                      // log2 of the heads a (row, KV head) has there
 };
 
 // Tensor maps of a block's copies: FP8 K pages, V pages, K scales, V scales;
@@ -122,6 +126,27 @@ struct AttnItem {
   int r, h, row0, rows, seq, first;  // first: position of row row0
   __device__ int blocks_upto(int rows_) const { return seq > 0 ? (first + rows_ - 1) / 128 + 1 : 0; }
 };
+// The blocks that an item's rows see within a window: the first `sinks` of
+// the request and those from `from` on, up to nb.
+struct AttnSpan {
+  int sinks, from, nb;
+  __device__ int count() const { return sinks + nb - from; }
+  __device__ int block(int u) const { return u < sinks ? u : u - sinks + from; }
+};
+template <bool EXT>
+__device__ __forceinline__ AttnSpan attn_span(const CacheAttnParams &a, const AttnItem &x, int nb) {
+  if (!EXT || a.window == 0) return AttnSpan{0, 0, nb};
+  AttnSpan s;
+  s.nb = nb;
+  s.sinks = min((a.sinks >> 7) + ((a.sinks & 127) != 0), nb);
+  s.from = min(max(max(x.first - a.window + 1, 0) >> 7, s.sinks), nb);
+  return s;
+}
+// Whether a row at position p sees a key of block b <= p / 128.
+template <bool EXT>
+__device__ __forceinline__ bool attn_sees(const CacheAttnParams &a, int p, int b) {
+  return !EXT || a.window == 0 || b * 128 < a.sinks || b * 128 + 127 > p - a.window;
+}
 // its place, without the request's keys
 __device__ __forceinline__ AttnItem attn_place(const CacheAttnParams &a, int it) {
   AttnItem x;
@@ -147,10 +172,11 @@ __device__ __forceinline__ AttnItem attn_item(const CacheAttnParams &a, int it, 
 // The share of the grid's work that an item stands for (at least one unit):
 // its blocks, or the length of its rows' lists (whose union the producer
 // scales to it).
+template <bool EXT>
 __device__ __forceinline__ int attn_units(const CacheAttnParams &a, int it, bool *bad) {
   const AttnItem x = attn_item(a, it, bad);
   if (x.seq == 0) return 1;
-  if (a.topk == 0) return x.blocks_upto(x.rows);
+  if (a.topk == 0) return attn_span<EXT>(a, x, x.blocks_upto(x.rows)).count();
   int n = 0;
   const int32_t *c = a.counts + ((int64_t)x.r * a.q_len + x.row0) * a.n_kv + x.h;
 #pragma unroll
@@ -190,7 +216,7 @@ struct AttnSlice {
 
 // Every thread of the CTA calls it (WARPS: warps that share the scan); it
 // ends behind a barrier of the CTA.
-template <int WARPS, class S>
+template <int WARPS, bool EXT, class S>
 __device__ __forceinline__ AttnSlice attn_slice(const CacheAttnParams &a, S &sh, int mode) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   AttnSlice sl;
@@ -203,7 +229,7 @@ __device__ __forceinline__ AttnSlice attn_slice(const CacheAttnParams &a, S &sh,
     bool bad = false;
     for (int i0 = 0; i0 < a.items; i0 += 32 * WARPS) {
       const int it = i0 + tid;
-      const int n = warp < WARPS && it < a.items ? attn_units(a, it, &bad) : 0;
+      const int n = warp < WARPS && it < a.items ? attn_units<EXT>(a, it, &bad) : 0;
       int incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -281,7 +307,7 @@ __device__ __forceinline__ void attn_prefetch(const CacheAttnParams &a, int mode
 // One warp: what is to be copied, a batch of up to 32 blocks ahead of the
 // copies, so that the latency of the lists and the block table (behind the
 // copies already asked for) is hidden.
-template <int FMT, class S>
+template <int FMT, bool EXT, class S>
 __device__ __forceinline__ void attn_resolve(const CacheAttnParams &a, S &sh, const AttnSlice &sl, int mode) {
   const int lane = threadIdx.x & 31;
   bool ok = true;
@@ -300,9 +326,10 @@ __device__ __forceinline__ void attn_resolve(const CacheAttnParams &a, S &sh, co
     if (mode != kAtSliced && bad && lane == 0) set_status(a.status, kDevSlotRange);
     const int nb = x.blocks_upto(x.rows);
     int u0 = 0, u1 = 0;  // the segment's blocks (of the union list, or of the request)
+    const AttnSpan span = attn_span<EXT>(a, x, nb);
     if (a.topk == 0) {
-      u0 = (int)((int64_t)nb * v0 / v);
-      u1 = (int)((int64_t)nb * v1 / v);
+      u0 = (int)((int64_t)span.count() * v0 / v);
+      u1 = (int)((int64_t)span.count() * v1 / v);
     } else if (a.rows_per == 1 && a.topk <= 32) {
       // one short list: its distinct blocks in list order
       if (nb > 0) {
@@ -383,9 +410,10 @@ __device__ __forceinline__ void attn_resolve(const CacheAttnParams &a, S &sh, co
       int b = -1, rows = 0;
       int64_t blk = -1;
       if (base + lane < u1) {
-        b = a.topk ? sh.list[base + lane - u0] : base + lane;
+        b = a.topk ? sh.list[base + lane - u0] : span.block(base + lane);
         for (int i = 0; i < x.rows; ++i)
-          if (a.topk ? (sh.bits[i][b >> 5] >> (b & 31)) & 1u : b <= (x.first + i) / 128) rows |= 1 << i;
+          if (a.topk ? (sh.bits[i][b >> 5] >> (b & 31)) & 1u : b <= (x.first + i) / 128 && attn_sees<EXT>(a, x.first + i, b))
+            rows |= 1 << i;
         blk = __ldg(a.block_table + (int64_t)x.r * a.bt_width + b);
         const bool in = FMT == 0 ? blk >= 0 && blk * a.kps + 8 <= a.num_pages16
                                  : blk >= 0 && (blk + 1) * 128 <= a.kv_pages * a.bs;

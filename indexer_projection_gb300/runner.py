@@ -181,7 +181,7 @@ class CacheReader(_Calls):
     def __init__(self, n_q_heads: int, n_kv_heads: int, *, cache_format: int, caches: B.pa_caches, max_requests: int,
                  q_len: int, bt_width: int, topk: int = 0, init_blocks: int = 0, local_blocks: int = 0,
                  block_size: int = 16, kv_page_stride: int = 0, sm_scale: float = 128 ** -0.5, flags: int = 0,
-                 device: torch.device | str | None = None):
+                 weigh: bool = False, device: torch.device | str | None = None):
         self._take_device(device)
         lib = B.load()
         self.n_q_heads, self.n_kv_heads, self.cache_format = n_q_heads, n_kv_heads, cache_format
@@ -192,7 +192,13 @@ class CacheReader(_Calls):
         self.ws_bytes = B.pre_attn_attention_workspace_bytes(max_requests, q_len, n_kv_heads, sms)
         if self.ws_bytes == 0:
             raise ValueError(f"max_requests {max_requests}, q_len {q_len} or n_kv_heads {n_kv_heads} out of range")
-        self._take_workspace(self.ws_bytes)
+        # behind it what attend's weights need
+        self.ws_bytes = (self.ws_bytes + 255) // 256 * 256
+        weights_bytes = B.pre_attn_attention_weights_bytes(max_requests, q_len, n_q_heads, n_kv_heads, bt_width) if weigh else 0
+        if weigh and weights_bytes == 0:
+            raise ValueError(f"n_q_heads {n_q_heads} or bt_width {bt_width} out of range")
+        self.weigh = weigh
+        self._take_workspace(self.ws_bytes + weights_bytes)
         # the calls' argument structs, of which a call sets what changes
         self._attn = B.pa_attention_args(None, None, 1.0, 0, n_q_heads, n_kv_heads, cache_format, block_size,
                                          kv_page_stride, None, None, None, None, None, topk, 0, q_len,
@@ -213,6 +219,9 @@ class CacheReader(_Calls):
         self._scores_entry = getattr(lib, name), B.ctypes.byref(self._scores), name
         self._select_entry = lib.pre_attn_select_blocks, B.ctypes.byref(self._select), "pre_attn_select_blocks"
         self._attn_entry = lib.pre_attn_attention, B.ctypes.byref(self._attn), "pre_attn_attention"
+        self._ext = B.pa_attention_ext(0, 0, None, 0, None, 0, 1.0, self.status + 256 + self.ws_bytes, weights_bytes)
+        ext, ext_entry = B.ctypes.byref(self._ext), lib.pre_attn_attention_ext
+        self._ext_entry = (lambda args, stream: ext_entry(args, ext, stream)), self._attn_entry[1], "pre_attn_attention_ext"
         self._evict = B.pa_evict_args(None, 0, None, None, 0, bt_width, 0, init_blocks, local_blocks, None, 0, None, None,
                                       None, None, self.status)
         self._evict_entry = lib.pre_attn_evict_blocks, B.ctypes.byref(self._evict), "pre_attn_evict_blocks"
@@ -278,10 +287,15 @@ class CacheReader(_Calls):
             return B.PA_OK
         return self._call(self._select_entry, stream, check)
 
-    def attend(self, q, block_table, seq_lens, out, *, blocks=None, counts=None, q_fp8_scale: float = 1.0, stream=None,
+    def attend(self, q, block_table, seq_lens, out, *, blocks=None, counts=None, q_fp8_scale: float = 1.0,
+               window: int = 0, sinks: int = 0, weights=None, weights_before=None, decay: float = 1.0, stream=None,
                check: bool = True) -> int:
         """Attention of q [M, >= n_q_heads * 128] (bf16, or E4M3 with q_fp8_scale) into out (bf16, as wide): over the
-        blocks of each row and KV head (blocks [M, n_kv_heads, topk], counts [M, n_kv_heads]), or all without."""
+        blocks of each row and KV head (blocks [M, n_kv_heads, topk], counts [M, n_kv_heads]), or all without.  With a
+        window each row sees its last ``window`` keys and the request's first ``sinks``.  Into weights [R, >= bt_width]
+        (f32; a reader made with ``weigh``) goes the softmax weight that each block of a request got from its rows and
+        heads, on top of ``decay`` times weights_before (None: nothing; it may be weights itself); 0 behind a request's
+        last block."""
         R = self._requests(seq_lens, block_table)
         M, a, cols = R * self.q_len, self._attn, self.n_q_heads * 128
         half = q.dtype is torch.bfloat16
@@ -302,9 +316,24 @@ class CacheReader(_Calls):
             self._ints(blocks, (M, self.n_kv_heads, self.topk), "blocks")
             self._ints(counts, (M, self.n_kv_heads), "counts")
             a.blocks, a.counts = blocks.data_ptr(), counts.data_ptr()
-        if R == 0:
-            return B.PA_OK
-        return self._call(self._attn_entry, stream, check)
+        if window == 0 and sinks == 0 and weights is None:
+            if weights_before is not None:
+                raise ValueError("weights_before come with the weights")
+            return self._call(self._attn_entry, stream, check) if R else B.PA_OK
+        e = self._ext
+        e.window, e.sinks, e.weights, e.weights_before = window, sinks, None, None
+        if weights is not None:
+            if not self.weigh:
+                raise ValueError("weights come from a reader made with weigh=True")
+            e.weights_stride = self._rows(weights, weights.dtype is torch.float32, R, self.bt_width, "weights")
+            e.weights, e.decay = weights.data_ptr(), decay
+            if weights_before is not None:
+                e.before_stride = self._rows(weights_before, weights_before.dtype is torch.float32, R, self.bt_width,
+                                             "weights_before")
+                e.weights_before = weights_before.data_ptr()
+        elif weights_before is not None:
+            raise ValueError("weights_before come with the weights")
+        return self._call(self._ext_entry, stream, check) if R else B.PA_OK
 
     def evict_blocks(self, weights, block_table, seq_lens, evicted, counts, *, keep: int, weights_out=None,
                      block_table_out=None, seq_lens_out=None, stream=None, check: bool = True) -> int:
