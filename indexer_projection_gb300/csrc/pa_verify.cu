@@ -16,18 +16,20 @@
 // for any split.  (f32 sums of a vocabulary of 2^17 would move the drawn token
 // in about one draw of a hundred; f64 adds run at a sixty-fourth of the f32
 // rate here.)
+#include <algorithm>
 #include <cstdint>
 
 #include "../../include/pre_attn.h"
 #include "pa_device.cuh"
+#include "pa_f16.cuh"
 #include "pa_launch.h"
 
 namespace pa {
 
 constexpr int kVfThreads = 256;
 constexpr int kVfWarps = kVfThreads / 32;
-constexpr int kVfCluster = 8;  // CTAs a request
-constexpr int kVfRuns = kVfCluster * kVfWarps;
+constexpr int kVfMaxCtas = 8;  // CTAs a request, a cluster
+constexpr int kVfPerSm = 4;    // CTAs an SM holds
 
 struct VerifyParams {
   const void *target, *draft;  // draft: or null
@@ -35,6 +37,7 @@ struct VerifyParams {
   const int32_t *drafts;
   const float *uniforms;
   int R, q_len, vocab;
+  int ctas;  // a request
   int32_t *tokens, *accepted;
   uint32_t *status;
 };
@@ -44,16 +47,46 @@ __device__ __forceinline__ float prob(const __nv_bfloat16 *p) {
   return bf16_to_f32(__ldg(reinterpret_cast<const uint16_t *>(p)));
 }
 
-// floor(x 2^(32 + BITS)) of x in [0, 1] (BITS 30) or [0, 1) (BITS 32): its
-// integer part at 2^BITS, then the rest's at 2^32; each step is exact.
-template <int BITS>
-__device__ __forceinline__ uint64_t fixed(float x) {
-  const float y = x * (BITS == 30 ? 0x1p30f : 0x1p32f);
+// floor(x 2^64) of x in [0, 1): its first 32 bits, then the rest's; each step is exact.
+__device__ __forceinline__ uint64_t fraction(float x) {
+  const float y = x * 0x1p32f;
   const uint32_t hi = __float2uint_rz(y);
-  const uint32_t lo = __float2uint_rz((y - __uint2float_rz(hi)) * 0x1p32f);
-  return (uint64_t)hi << 32 | lo;
+  return (uint64_t)hi << 32 | __float2uint_rz((y - __uint2float_rz(hi)) * 0x1p32f);
 }
-__device__ __forceinline__ uint64_t fixed_prob(float p) { return fixed<30>(fminf(fmaxf(p, 0.f), 1.f)); }
+
+// floor(p 2^62) of p in [0, 1] as digits of 23, 23 and 16 bits, each with a
+// constant beside it: p + 1, rounded down, has its last place at 2^-23, so its
+// bits count p's 2^-23s; what that leaves of p (exact) likewise with 2^-23 for
+// 1, and the rest of that with 2^-39.  Seven additions, two tokens' in one
+// packed instruction, where a conversion to 64 bits takes a 64-bit shift or
+// three conversions at a quarter of their rate.
+__device__ __forceinline__ f32x2 add2_down(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rm.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+struct Digits {
+  int d[3][2];  // of two tokens
+};
+__device__ __forceinline__ Digits digits_of(float p0, float p1) {
+  const f32x2 c1 = pack2(1.f, 1.f), c2 = pack2(0x1p-23f, 0x1p-23f), c3 = pack2(0x1p-39f, 0x1p-39f);
+  const f32x2 m1 = pack2(-1.f, -1.f), m2 = pack2(-0x1p-23f, -0x1p-23f);
+  f32x2 p = pack2(p0, p1);
+  const f32x2 r1 = add2_down(p, c1);
+  p = fma2(add2(r1, m1), m1, p);  // (exact: multiples of 2^-23 below 2)
+  const f32x2 r2 = add2_down(p, c2);
+  p = fma2(add2(r2, m2), m1, p);
+  const f32x2 r3 = add2_down(p, c3);
+  const float2 a = unpack2(r1), b = unpack2(r2), c = unpack2(r3);
+  return Digits{{{__float_as_int(a.x), __float_as_int(a.y)},
+                 {__float_as_int(b.x), __float_as_int(b.y)},
+                 {__float_as_int(c.x), __float_as_int(c.y)}}};
+}
+__device__ __forceinline__ int64_t value_of(int d1, int d2, int d3) {
+  return ((int64_t)d1 << 39) + ((int64_t)d2 << 16) + d3;
+}
+// a probability as it counts: [0, 1], 0 for a NaN
+__device__ __forceinline__ float counted(float p) { return __saturatef(p); }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
 #pragma unroll
@@ -71,129 +104,292 @@ __device__ __forceinline__ uint64_t warp_running(uint64_t x) {
   return x;
 }
 
-template <typename TP, typename TQ>
-__global__ void __launch_bounds__(kVfThreads) pa_verify_kernel(const __grid_constant__ VerifyParams a) {
-  __shared__ uint64_t sums[2][kVfRuns];  // the runs' sums, in vocabulary order
+// A lane's IN values of a row in a step, as loaded: E consecutive tokens a
+// load, its value i that of token v + 32 E (i / E) + E lane + i % E.
+template <typename T, int E, int IN>
+struct ProbRow;
+template <typename T, int IN>
+struct ProbRow<T, 1, IN> {
+  T x[IN];
+  __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+    for (int i = 0; i < IN; ++i) x[i] = __ldg(p + 32 * i + (threadIdx.x & 31));
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 2) return bf16_to_f32(__bfloat16_as_ushort(x[i]));
+    else return x[i];
+  }
+};
+template <int E, int IN>
+struct ProbRowF32 {
+  float4 x[IN / 4];
+  __device__ __forceinline__ void load(const float *p) {  // (E 8: beside a row of 16-bit values)
+#pragma unroll
+    for (int i = 0; i < IN / 4; ++i)
+      x[i] = __ldg(reinterpret_cast<const float4 *>(p + 32 * E * (4 * i / E) + E * (threadIdx.x & 31) + 4 * i % E));
+  }
+  __device__ __forceinline__ float get(int i) const {
+    const float4 y = x[i / 4];
+    return i % 4 == 0 ? y.x : i % 4 == 1 ? y.y : i % 4 == 2 ? y.z : y.w;
+  }
+};
+template <int IN>
+struct ProbRow<float, 4, IN> : ProbRowF32<4, IN> {};
+template <int IN>
+struct ProbRow<float, 8, IN> : ProbRowF32<8, IN> {};
+template <int IN>
+struct ProbRow<__nv_bfloat16, 8, IN> {
+  uint4 x[IN / 8];
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+#pragma unroll
+    for (int i = 0; i < IN / 8; ++i) x[i] = __ldg(reinterpret_cast<const uint4 *>(p + 256 * i + 8 * (threadIdx.x & 31)));
+  }
+  __device__ __forceinline__ float get(int i) const {
+    const uint4 y = x[i / 8];
+    const uint32_t w = i % 8 < 2 ? y.x : i % 8 < 4 ? y.y : i % 8 < 6 ? y.z : y.w;
+    return __uint_as_float(i % 2 ? w & 0xffff0000u : w << 16);
+  }
+};
+
+// The rows that a request's token is drawn from.
+template <typename TP, typename TQ, int E>
+struct Draw {
+  const TP *P;
+  const TQ *Q;         // or null
+  int without;         // the token that weighs nothing, or -1
+  int drafts, acc, x;  // the request's drafts, how many are accepted, the lane's
+
+  // By a warp, the drafts one a lane.
+  __device__ __forceinline__ void accept(const VerifyParams &a, int r) {
+    const int lane = threadIdx.x & 31, k = a.q_len - 1;
+    const TP *target = static_cast<const TP *>(a.target) + (int64_t)r * a.q_len * a.target_stride;
+    const TQ *draft = static_cast<const TQ *>(a.draft);
+    if (draft) draft += (int64_t)r * k * a.draft_stride;
+    x = -1;
+    bool good = false;
+    if (lane < k) {
+      x = __ldg(a.drafts + (int64_t)r * k + lane);
+      const float u = __ldg(a.uniforms + (int64_t)r * a.q_len + lane);
+      if (x >= 0 && x < a.vocab) {
+        const float p = prob(target + lane * a.target_stride + x);
+        const float q = draft ? prob(draft + lane * a.draft_stride + x) : 1.f;
+        good = (double)u * (double)q < (double)p;  // 24 x 24 bits: exact
+      }
+    }
+    drafts = __ffs(__ballot_sync(0xffffffffu, x < 0)) - 1;  // lane k has none
+    acc = __ffs(~__ballot_sync(0xffffffffu, good)) - 1;     // <= drafts
+    const int xa = __shfl_sync(0xffffffffu, x, acc);
+    // from what the drafter leaves of the target's row: less its own, or without the token
+    P = target + acc * a.target_stride;
+    Q = draft && acc < drafts ? draft + acc * a.draft_stride : nullptr;
+    without = !draft && acc < drafts ? xa : -1;
+  }
+
+  // IN tokens of a lane: token i of a warp's step at v
+  static __device__ __forceinline__ int token(int v, int i) { return v + 32 * E * (i / E) + E * (threadIdx.x & 31) + i % E; }
+  // What token v weighs as p - q, q not above p; 0 from v1 on.
+  __device__ __forceinline__ void weigh(int v, int v1, float &p, float &q) const {
+    const bool in = v < v1 && v != without;
+    p = in ? prob(P + v) : 0.f;
+    q = in && Q ? prob(Q + v) : 0.f;
+  }
+  static __device__ __forceinline__ void clamp(float &p, float &q) {
+    p = counted(p);
+    q = fminf(counted(q), p);
+  }
+
+  // The lane's sum over the tokens v0 .. v1 of its warp, a step's loads ahead
+  // of the sums (64 bytes a lane of them).
+  template <bool DRAFT>
+  __device__ __forceinline__ uint64_t run(int v0, int v1) const {
+    constexpr int kMost = 64 / (sizeof(TP) + (DRAFT ? sizeof(TQ) : 0)) / 8 * 8, IN = E == 1 && kMost > 16 ? 16 : kMost, kStep = 32 * IN;
+    struct Loaded {
+      ProbRow<TP, E, IN> p;
+      ProbRow<TQ, E, DRAFT ? IN : E> q;
+    };
+    auto load = [&](Loaded &x, int v) {
+      x.p.load(P + v);
+      if constexpr (DRAFT) x.q.load(Q + v);
+    };
+    uint64_t sum = 0;
+    Loaded next;
+    int v = v0;
+    if (v + kStep <= v1) load(next, v);
+    for (; v + kStep <= v1; v += kStep) {
+      const Loaded x = next;
+      if (v + 2 * kStep <= v1) load(next, v + kStep);
+      // (without a draft row its digits are the constants')
+      const Digits none = digits_of(0.f, 0.f);
+      int d[3];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) d[k] = DRAFT ? 0 : -IN * none.d[k][0];
+#pragma unroll
+      for (int i = 0; i < IN; i += 2) {
+        float p0 = counted(x.p.get(i)), p1 = counted(x.p.get(i + 1));
+        const Digits s = digits_of(p0, p1);
+        if constexpr (DRAFT) {
+          const Digits y = digits_of(fminf(counted(x.q.get(i)), p0), fminf(counted(x.q.get(i + 1)), p1));
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            d[k] += s.d[k][0] - y.d[k][0];
+            d[k] += s.d[k][1] - y.d[k][1];
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 3; ++k) d[k] += s.d[k][0] + s.d[k][1];
+        }
+      }
+      sum += value_of(d[0], d[1], d[2]);
+    }
+    // `without` is among them: its weight once
+    if (!DRAFT && without >= v0 && without < v && (threadIdx.x & 31) == 0) {
+      const Digits y = digits_of(counted(prob(P + without)), 0.f);
+      sum -= value_of(y.d[0][0] - y.d[0][1], y.d[1][0] - y.d[1][1], y.d[2][0] - y.d[2][1]);
+    }
+    for (; v < v1; v += 32 * 8) sum += part(v, v1);
+    return sum;
+  }
+  // .. of 8 tokens, v + lane + 32 i; what each of them weighs
+  __device__ __forceinline__ uint64_t part(int v, int v1) const {
+    uint64_t each[8], sum = 0;
+    part(v, v1, each);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += each[i];
+    return sum;
+  }
+  __device__ __forceinline__ void part(int v, int v1, uint64_t (&each)[8]) const {
+    float p[8], q[8];
+    v += threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) weigh(v + 32 * i, v1, p[i], q[i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      clamp(p[i], q[i]);
+      const Digits s = digits_of(p[i], q[i]);
+      each[i] = value_of(s.d[0][0] - s.d[0][1], s.d[1][0] - s.d[1][1], s.d[2][0] - s.d[2][1]);
+    }
+  }
+  __device__ __forceinline__ uint64_t any(int v0, int v1) const { return Q ? run<true>(v0, v1) : run<false>(v0, v1); }
+};
+
+template <typename TP, typename TQ, int E>
+__global__ void __launch_bounds__(kVfThreads, kVfPerSm) pa_verify_kernel(const __grid_constant__ VerifyParams a) {
+  __shared__ uint64_t sums[2][kVfMaxCtas * kVfWarps];  // the runs' sums, in vocabulary order
+  __shared__ uint64_t step_sums[2][kVfWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cta_rank();
-  const int r = blockIdx.x / kVfCluster, k = a.q_len - 1, V = a.vocab;
-  const TP *target = static_cast<const TP *>(a.target) + (int64_t)r * a.q_len * a.target_stride;
-  const TQ *draft = static_cast<const TQ *>(a.draft);
-  if (draft) draft += (int64_t)r * k * a.draft_stride;
+  const int rank = cta_rank(), r = blockIdx.x / a.ctas, V = a.vocab, runs = a.ctas * kVfWarps;
   cluster_arrive_relaxed();  // the others' sums come once this CTA runs
   pdl_wait();
   pdl_trigger();
-  // every warp: the drafts, one a lane
-  int x = -1;
-  bool good = false;
-  if (lane < k) {
-    x = __ldg(a.drafts + (int64_t)r * k + lane);
-    if (x >= 0 && x < V) {
-      const float p = prob(target + lane * a.target_stride + x);
-      const float q = draft ? prob(draft + lane * a.draft_stride + x) : 1.f;
-      good = (double)__ldg(a.uniforms + (int64_t)r * a.q_len + lane) * (double)q < (double)p;  // 24 x 24 bits: exact
-    }
-  }
-  const float u = __ldg(a.uniforms + (int64_t)r * a.q_len + k);
-  const int drafts = __ffs(__ballot_sync(0xffffffffu, x < 0)) - 1;  // lane k has none
-  const int acc = __ffs(~__ballot_sync(0xffffffffu, good)) - 1;     // <= drafts
-  const int xa = __shfl_sync(0xffffffffu, x, acc);
+  Draw<TP, TQ, E> w;
+  w.accept(a, r);
+  const float u = __ldg(a.uniforms + (int64_t)r * a.q_len + a.q_len - 1);
+  int32_t *tokens = a.tokens + (int64_t)r * a.q_len;
   if (rank == 0 && warp == 0) {
-    if (__any_sync(0xffffffffu, lane < drafts && x >= V) && lane == 0) set_status(a.status, kDevTokenRange);
-    if (lane < a.q_len && lane != acc) a.tokens[(int64_t)r * a.q_len + lane] = lane < acc ? x : -1;
-    if (lane == 0) a.accepted[r] = acc;
+    if (__any_sync(0xffffffffu, lane < w.drafts && w.x >= V) && lane == 0) set_status(a.status, kDevTokenRange);
+    if (lane < a.q_len && lane != w.acc) tokens[lane] = lane < w.acc ? w.x : -1;
+    if (lane == 0) a.accepted[r] = w.acc;
   }
-  const TP *P = target + acc * a.target_stride;
-  const TQ *Q = draft ? draft + acc * a.draft_stride : nullptr;
-  bool rest = acc < drafts;  // draw from what the drafter leaves
-  auto weight = [&](int v) -> uint64_t {
-    const uint64_t p = fixed_prob(prob(P + v));
-    if (!rest) return p;
-    const uint64_t q = Q ? fixed_prob(prob(Q + v)) : (v == xa ? ~0ull >> 1 : 0ull);
-    return p > q ? p - q : 0ull;
-  };
-  // this warp's run of the vocabulary
+  // run i of the vocabulary, a warp's
+  auto begin = [&](int i) { return i == runs ? V : (int)((int64_t)V * i / runs) & -8; };
   const int run = rank * kVfWarps + warp;
-  const int v0 = (int)((int64_t)V * run / kVfRuns), v1 = (int)((int64_t)V * (run + 1) / kVfRuns);
   cluster_wait();
   for (int round = 0;; ++round) {
-    uint64_t sum = 0;
-    constexpr int kIn = 8;
-    int v = v0 + lane;
-    for (; v + 32 * (kIn - 1) < v1; v += 32 * kIn) {
-      uint64_t w[kIn];
-#pragma unroll
-      for (int i = 0; i < kIn; ++i) w[i] = weight(v + 32 * i);
-#pragma unroll
-      for (int i = 0; i < kIn; ++i) sum += w[i];
-    }
-    for (; v < v1; v += 32) sum += weight(v);
-    sum = warp_sum(sum);
-    if (lane < kVfCluster)
+    const uint64_t sum = warp_sum(w.any(begin(run), begin(run + 1)));
+    if (lane < a.ctas)
       asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa(smem_u32(&sums[round][run]), lane)), "l"(sum) : "memory");
     cluster_sync();
     // the runs in order, two a lane
-    static_assert(kVfRuns == 64, "two runs a lane");
-    const uint64_t s0 = sums[round][2 * lane], s1 = sums[round][2 * lane + 1];
+    static_assert(kVfMaxCtas * kVfWarps == 64, "two runs a lane");
+    const uint64_t s0 = 2 * lane < runs ? sums[round][2 * lane] : 0, s1 = 2 * lane < runs ? sums[round][2 * lane + 1] : 0;
     const uint64_t upto = warp_running(s0 + s1);
     const uint64_t total = __shfl_sync(0xffffffffu, upto, 31);
     if (total == 0) {
-      if (rest) {  // the drafter leaves nothing: from the target's own
-        rest = false;
+      if (w.acc < w.drafts && round == 0) {  // the drafter leaves nothing: from the target's own
+        w.Q = nullptr;
+        w.without = -1;
         continue;
       }
       if (rank == 0 && tid == 0) {
-        a.tokens[(int64_t)r * a.q_len + acc] = -1;
+        tokens[w.acc] = -1;
         set_status(a.status, kDevNoToken);
       }
       return;
     }
     // the running sum has to exceed u x total
-    const uint64_t bar = __umul64hi(u >= 1.f ? ~0ull : fixed<32>(fmaxf(u, 0.f)), total);
-    const int at = __ffs(__ballot_sync(0xffffffffu, upto > bar)) - 1;  // two runs
-    uint64_t before = __shfl_sync(0xffffffffu, upto - s0 - s1, at);
-    const uint64_t half = __shfl_sync(0xffffffffu, s0, at);
-    const bool second = before + half <= bar;
-    if (second) before += half;
-    if (run != 2 * at + second) return;
-    // the drawn token is in this warp's run
-    int found = -1;
-    for (v = v0 + lane; v - lane < v1; v += 32) {
-      const uint64_t upto_v = before + warp_running(v < v1 ? weight(v) : 0ull);
-      const uint32_t over = __ballot_sync(0xffffffffu, upto_v > bar);
-      if (over) {
-        found = v - lane + __ffs(over) - 1;
-        break;
+    const uint64_t bar = __umul64hi(u >= 1.f ? ~0ull : fraction(fmaxf(u, 0.f)), total);
+    int at = 2 * (__ffs(__ballot_sync(0xffffffffu, upto > bar)) - 1);
+    uint64_t before = __shfl_sync(0xffffffffu, upto - s0 - s1, at / 2);
+    const uint64_t half = __shfl_sync(0xffffffffu, s0, at / 2);
+    if (before + half <= bar) before += half, ++at;
+    if (at / kVfWarps != rank) return;
+    // the drawn token is in run `at`, one of this CTA's: its warps read the run
+    // again, 256 tokens each
+    const int v1 = begin(at + 1);
+    for (int v0 = begin(at), turn = 0; v0 < v1; v0 += 256 * kVfWarps, ++turn) {
+      const int v = v0 + warp * 256;
+      uint64_t each[8], mine = 0;
+      w.part(v, v1, each);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mine += each[i];
+      mine = warp_sum(mine);
+      if (lane == 0) step_sums[turn & 1][warp] = mine;
+      __syncthreads();
+      int hit = -1;  // the warp whose tokens have it, the same for every warp
+      uint64_t first = 0;
+#pragma unroll
+      for (int i = 0; i < kVfWarps; ++i) {
+        const uint64_t y = step_sums[turn & 1][i];
+        if (hit < 0 && before <= bar && bar < before + y) hit = i, first = before;
+        before += y;
       }
-      before = __shfl_sync(0xffffffffu, upto_v, 31);
+      if (hit >= 0) {
+        if (hit == warp) {
+          int found = -1;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) each[i] = warp_running(each[i]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t over = __ballot_sync(0xffffffffu, first + each[i] > bar);
+            if (over && found < 0) found = v + 32 * i + __ffs(over) - 1;
+            first += __shfl_sync(0xffffffffu, each[i], 31);
+          }
+          if (lane == 0) tokens[w.acc] = found;
+        }
+        return;
+      }
     }
-    if (lane == 0) {
-      a.tokens[(int64_t)r * a.q_len + acc] = found;
-      if (found < 0) set_status(a.status, kDevNoToken);
+    if (tid == 0) {  // (sums that wrapped)
+      tokens[w.acc] = -1;
+      set_status(a.status, kDevNoToken);
     }
     return;
   }
 }
 
-static cudaError_t launch_verify(const VerifyParams &a, bool target_bf16, bool draft_bf16, cudaStream_t stream) {
+template <typename TP, typename TQ>
+static cudaError_t launch_verify(VerifyParams a, int sms, cudaStream_t stream) {
+  a.ctas = kVfMaxCtas;  // as many as are resident at once
+  while (a.ctas > 1 && a.R * a.ctas > sms * kVfPerSm) --a.ctas;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kVfCluster;
+  attr[1].val.clusterDim.x = a.ctas;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   cfg.stream = stream;
-  cfg.gridDim = dim3((unsigned)a.R * kVfCluster);
+  cfg.gridDim = dim3((unsigned)a.R * a.ctas);
   cfg.blockDim = dim3(kVfThreads);
-  using bf = __nv_bfloat16;
-  if (target_bf16)
-    return draft_bf16 ? cudaLaunchKernelEx(&cfg, pa_verify_kernel<bf, bf>, a)
-                      : cudaLaunchKernelEx(&cfg, pa_verify_kernel<bf, float>, a);
-  return draft_bf16 ? cudaLaunchKernelEx(&cfg, pa_verify_kernel<float, bf>, a)
-                    : cudaLaunchKernelEx(&cfg, pa_verify_kernel<float, float>, a);
+  // 16-byte loads where every row begins on such a boundary
+  auto rows16 = [](const void *p, int64_t stride, size_t es) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * es % 16 == 0;
+  };
+  constexpr int E = sizeof(TP) == 2 || sizeof(TQ) == 2 ? 8 : 4;
+  const bool wide = rows16(a.target, a.target_stride, sizeof(TP)) && (!a.draft || rows16(a.draft, a.draft_stride, sizeof(TQ)));
+  return cudaLaunchKernelEx(&cfg, wide ? pa_verify_kernel<TP, TQ, E> : pa_verify_kernel<TP, TQ, 1>, a);
 }
 
 }  // namespace pa
@@ -241,9 +437,15 @@ extern "C" int pre_attn_verify_drafts(const pa_verify_args *in, void *stream) {
   a.R = x.R;
   a.q_len = x.q_len;
   a.vocab = x.vocab;
+  a.ctas = 0;
   a.tokens = x.tokens;
   a.accepted = x.accepted;
   a.status = x.status;
-  const cudaError_t e = pa::launch_verify(a, target_bf16, draft_bf16, (cudaStream_t)stream);
+  using bf = __nv_bfloat16;
+  const cudaStream_t s = (cudaStream_t)stream;
+  const int sms = pa::current_device_sms();
+  if (sms < 1) return pa::record_cuda_error(cudaGetLastError());
+  const cudaError_t e = target_bf16 ? (draft_bf16 || !a.draft ? pa::launch_verify<bf, bf>(a, sms, s) : pa::launch_verify<bf, float>(a, sms, s))
+                                    : (draft_bf16 ? pa::launch_verify<float, bf>(a, sms, s) : pa::launch_verify<float, float>(a, sms, s));
   return e == cudaSuccess ? PA_OK : pa::record_cuda_error(e);
 }
