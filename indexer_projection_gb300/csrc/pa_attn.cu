@@ -64,86 +64,15 @@
 
 namespace pa {
 
-// Join the partial results of items that several CTAs share, in CTA order:
-// W warps a (item, row, head), each every W-th partial, several of them in
-// flight a lane (four dims); the W sums meet in shared memory.  The first CTA's
-// partial is its slot 1 (the item starts there), the others' their slot 0.
-constexpr int kJoinWarps = 8;
 template <int W>
 __global__ void __launch_bounds__(32 * kJoinWarps) pa_attn_join_kernel(const __grid_constant__ CacheAttnParams a, int grid) {
-  __shared__ float4 acc_s[kJoinWarps][32];
-  __shared__ float2 ml_s[kJoinWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int it = blockIdx.x / a.rows_per, row = blockIdx.x % a.rows_per;
-  const int head = blockIdx.y * (kJoinWarps / W) + warp / W;
-  const int h = it & (a.n_kv - 1), rg = it >> a.lg_kv, r = rg >> a.lg_groups;
-  const int row0 = (rg - (r << a.lg_groups)) * a.rows_per;
   pdl_trigger();  // the next kernel's CTAs fit beside these; it waits for this grid's end
   pdl_wait();
-  const int2 s = a.shares[it];
-  const int c0 = max(s.x, 0), c1 = min(s.y, grid - 1);
-  if (c1 <= c0 || row0 + row >= a.q_len) return;  // the same for the whole CTA
-  const bool have = head < a.group;
-  const float *base = a.part + (int64_t)2 * c0 * kAtPartFloats + (row * 16 + (have ? head : 0)) * kHeadDim + 4 * lane;
-  const float *mls = a.part + (int64_t)2 * c0 * kAtPartFloats + kAtMaxRows * 16 * kHeadDim + (row * 16 + (have ? head : 0)) * 2;
-  float top = -INFINITY, sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kIn = W > 1 ? 16 : 4;
-  const int n = c1 - c0 + 1;
-  for (int k0 = warp % W; k0 < n; k0 += W * kIn) {
-    float4 y[kIn];
-    float2 ml[kIn];
-    float t2 = top;
-#pragma unroll
-    for (int k = 0; k < kIn; ++k) {
-      const int c = k0 + k * W;
-      const int64_t off = (int64_t)(2 * c + (c == 0 ? 1 : 0)) * kAtPartFloats;
-      ml[k] = c < n ? *reinterpret_cast<const float2 *>(mls + off) : make_float2(-INFINITY, 0.f);
-      y[k] = c < n ? *reinterpret_cast<const float4 *>(base + off) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int k = 0; k < kIn; ++k) t2 = fmaxf(t2, ml[k].x);
-    const float f0 = top == t2 ? 1.f : ex2_approx(top - t2);
-    top = t2;
-    sum *= f0, acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
-#pragma unroll
-    for (int k = 0; k < kIn; ++k) {
-      const float f = ml[k].x == top ? 1.f : ex2_approx(ml[k].x - top);
-      sum += f * ml[k].y;
-      if (f != 0.f) acc.x += f * y[k].x, acc.y += f * y[k].y, acc.z += f * y[k].z, acc.w += f * y[k].w;
-    }
-  }
-  if constexpr (W > 1) {
-    acc_s[warp][lane] = acc;
-    if (lane == 0) ml_s[warp] = make_float2(top, sum);
-    __syncthreads();
-    if (warp % W) return;
-    float t2 = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < W; ++w) t2 = fmaxf(t2, ml_s[warp + w].x);
-    sum = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float2 ml = ml_s[warp + w];
-      const float4 y = acc_s[warp + w][lane];
-      const float f = ml.x == t2 ? 1.f : ex2_approx(ml.x - t2);
-      sum += f * ml.y;
-      if (f != 0.f) acc.x += f * y.x, acc.y += f * y.y, acc.z += f * y.z, acc.w += f * y.w;
-    }
-  }
-  if (!have) return;
-  const float inv = sum == 0.f ? 0.f : a.out_scale / sum;
-  const int64_t m = (int64_t)r * a.q_len + row0 + row;
-  *reinterpret_cast<uint2 *>(a.out + m * a.out_stride + (int64_t)(h * a.group + head) * kHeadDim + 4 * lane) =
-      make_uint2(bf16x2_bits(acc.x * inv, acc.y * inv), bf16x2_bits(acc.z * inv, acc.w * inv));
+  attn_join<W>(a, grid, blockIdx.x, blockIdx.y);
 }
 
 cudaError_t launch_attn_join(const CacheAttnParams &a, int sms, bool pdl, cudaStream_t stream) {
-  // few (item, row)s: many partials each, a CTA a head; else a warp a head.
-  // Dense, whole calls with a CTA a head / a warp a head: 4 items x 4 rows 78 /
-  // 92 us, 32 items x 1 row 35.9 / 36.9, 64 x 1 58.9 / 57.7, 32 x 4 548 / 543
-  const bool many = a.items * a.rows_per * 4 <= sms;
+  const bool many = join_by_head(a, sms);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -151,7 +80,7 @@ cudaError_t launch_attn_join(const CacheAttnParams &a, int sms, bool pdl, cudaSt
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  cfg.gridDim = dim3(a.items * a.rows_per, many ? a.group : (a.group + kJoinWarps - 1) / kJoinWarps);
+  cfg.gridDim = join_grid(a, many);
   cfg.blockDim = dim3(32 * kJoinWarps);
   return cudaLaunchKernelEx(&cfg, many ? pa_attn_join_kernel<kJoinWarps> : pa_attn_join_kernel<1>, a, sms);
 }
@@ -274,12 +203,12 @@ int attn_params(const pa_attention_args &x, CacheAttnParams &a, int *num_sms) {
 extern "C" int pre_attn_attention(const pa_attention_args *in, void *stream) {
   if (!in) return PA_ERR_NULL;
   pa::CacheAttnParams a;
-  int sms = 0, parts;
+  int sms = 0;
   const int st = pa::attn_params(*in, a, &sms);
   if (st != PA_OK || a.R == 0) return st;
   const bool pdl = !(in->flags & PA_FLAG_NO_PDL);
   const cudaError_t e = in->cache_format == PA_CACHE_FP8
-                            ? pa::launch_attn<0, false>(a, sms, pdl, (cudaStream_t)stream, &parts)
-                            : pa::launch_attn<1, false>(a, sms, pdl, (cudaStream_t)stream, &parts);
+                            ? pa::launch_attn<0, false>(a, sms, pdl, (cudaStream_t)stream, nullptr)
+                            : pa::launch_attn<1, false>(a, sms, pdl, (cudaStream_t)stream, nullptr);
   return e == cudaSuccess ? PA_OK : pa::record_cuda_error(e);
 }

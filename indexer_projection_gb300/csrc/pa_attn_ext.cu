@@ -24,11 +24,12 @@
 
 namespace pa {
 
-constexpr int kWgThreads = 512;
+constexpr int kWgThreads = 32 * kJoinWarps;
 constexpr int kWgWarps = kWgThreads / 32;
 constexpr int kWgMaxCtas = 8;     // a cluster
 constexpr int kWgMaxPairs = 64;   // (row, KV head)s of a request
 constexpr int kWgMaxRun = 2048;   // blocks a CTA
+constexpr int kWgValues = 512;    // sums that a CTA reads, at least, before a request gets more CTAs
 
 struct WeightParams {
   const float *part;  // [R][row][KV head][W][2^lg_v]: parts x heads
@@ -40,33 +41,37 @@ struct WeightParams {
   const float *before;  // or null
   int64_t before_stride;
   float decay;
-  int words;  // of a pair's bit set
+  int words;         // of a pair's bit set
+  int ctas;          // a request
+  int join, join_x;  // CTAs behind the requests' that join partial results, in rows of join_x
+  int sms;
 };
 
-// (m, s) stands for s 2^m; a lane's, then joined over lanes `from` apart.
-__device__ __forceinline__ void join_ms(float &m, float &s, float m2, float s2) {
-  const float top = fmaxf(m, m2);
-  s = (m == top ? s : s * ex2_approx(m - top)) + (m2 == top ? s2 : s2 * ex2_approx(m2 - top));
-  m = top;
+// s 2^m with the maximum m of several, and its s.
+struct Scaled {
+  float m, s;
+};
+__device__ __forceinline__ Scaled join_scaled(Scaled a, Scaled b) {
+  const float top = fmaxf(a.m, b.m);
+  return {top, (a.m == top ? a.s : a.s * ex2_approx(a.m - top)) + (b.m == top ? b.s : b.s * ex2_approx(b.m - top))};
 }
 
-__global__ void __launch_bounds__(kWgThreads) pa_weights_kernel(const __grid_constant__ WeightParams w) {
+__device__ __forceinline__ void block_weights(const WeightParams &w) {
   extern __shared__ uint32_t bits[];  // [pairs][words] blocks that the pair's row attends
   __shared__ uint32_t held[kWgMaxRun / 32 + 1];
   __shared__ float2 way_ms[kWgWarps][16];
   __shared__ float2 col_ms[kWgMaxPairs * 16];  // of this CTA's blocks
   __shared__ float lse[kWgMaxPairs * 16];      // log2 of the (row, head)'s sum
+  __shared__ float old[kWgMaxRun + 1];         // of the blocks' weights, what they had
   const CacheAttnParams &a = w.at;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint32_t ctas;
-  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ctas));
-  const int rank = cta_rank(), r = blockIdx.x / ctas;
-  pdl_wait();
-  pdl_trigger();
-  int seq = __ldg(a.seq_lens + r);
-  if (seq < a.q_len || (seq - 1) / 128 + 1 > a.bt_width) return;  // without keys (the attention flags it): the whole cluster
-  const int nb = (seq - 1) / 128 + 1, first = seq - a.q_len;
-  const int c0 = (int)((int64_t)nb * rank / ctas), c1 = (int)((int64_t)nb * (rank + 1) / ctas), n = c1 - c0;
+  const int rank = cta_rank(), r = blockIdx.x / w.ctas;
+  // What the attention did not write can be read before the wait on it: the
+  // attention lets this kernel in when the kernels before it are done.
+  const int seq = __ldg(a.seq_lens + r);
+  const bool none = seq < a.q_len || (seq - 1) / 128 + 1 > a.bt_width;  // without keys (the attention flags it)
+  const int nb = none ? 0 : (seq - 1) / 128 + 1, first = seq - a.q_len;
+  const int c0 = (int)((int64_t)nb * rank / w.ctas), c1 = (int)((int64_t)nb * (rank + 1) / w.ctas), n = c1 - c0;
   const int pairs = a.q_len * a.n_kv, heads = 1 << w.lg_heads, v = 1 << w.lg_v;
   // the blocks that the attention has summed
   for (int wi = warp; 32 * wi < n; wi += kWgWarps) {
@@ -84,8 +89,10 @@ __global__ void __launch_bounds__(kWgThreads) pa_weights_kernel(const __grid_con
       }
     }
   }
+  const float *before = w.before && w.decay != 0.f ? w.before + r * w.before_stride : nullptr;
+  for (int b = tid; b < n; b += kWgThreads) old[b] = before ? w.decay * before[c0 + b] : 0.f;
   __syncthreads();
-  if (a.topk) {
+  if (a.topk && n > 0) {
     const int64_t at = (int64_t)r * pairs;
     for (int e = tid; e < pairs * a.topk; e += kWgThreads) {
       const int k = e / a.topk, b = __ldg(a.blocks + at * a.topk + e);
@@ -95,6 +102,9 @@ __global__ void __launch_bounds__(kWgThreads) pa_weights_kernel(const __grid_con
     }
     __syncthreads();
   }
+  pdl_wait();
+  pdl_trigger();
+  if (none) return;  // the whole cluster
   // the (row, head)s' sums over this CTA's blocks: a warp a (row, KV head),
   // or several of them a part of its blocks each
   const float *base = w.part + (((int64_t)r * pairs * a.bt_width + c0) << w.lg_v);
@@ -105,11 +115,11 @@ __global__ void __launch_bounds__(kWgThreads) pa_weights_kernel(const __grid_con
     const float *src = base + pair * pair_stride;
     const uint32_t *mine = bits + pair * w.words;
     const int e1 = (n * (way + 1) / ways) << w.lg_v;
-    float m = -INFINITY, s = 0.f;
-    constexpr int kIn = 8;
+    Scaled z = {-INFINITY, 0.f};
+    constexpr int kIn = 16;
     for (int e = ((n * way / ways) << w.lg_v) + lane; e < e1; e += 32 * kIn) {
       float x[kIn];
-      float top = m;
+      float top = z.m;
 #pragma unroll
       for (int k = 0; k < kIn; ++k) {
         const int ek = e + 32 * k, b = ek >> w.lg_v;
@@ -118,82 +128,130 @@ __global__ void __launch_bounds__(kWgThreads) pa_weights_kernel(const __grid_con
 #pragma unroll
       for (int k = 0; k < kIn; ++k) top = fmaxf(top, x[k]);
       if (top == -INFINITY) continue;  // no weight yet
-      s = m == top ? s : s * ex2_approx(m - top);
-      m = top;
+      z.s = z.m == top ? z.s : z.s * ex2_approx(z.m - top);
+      z.m = top;
 #pragma unroll
-      for (int k = 0; k < kIn; ++k) s += ex2_approx(x[k] - top);
+      for (int k = 0; k < kIn; ++k) z.s += ex2_approx(x[k] - top);
     }
-    for (int o = 16; o >= heads; o >>= 1) join_ms(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+    for (int o = 16; o >= heads; o >>= 1)
+      z = join_scaled(z, Scaled{__shfl_xor_sync(0xffffffffu, z.m, o), __shfl_xor_sync(0xffffffffu, z.s, o)});
     if (lane < heads) {
-      if (ways == 1) col_ms[(pair << w.lg_heads) + lane] = make_float2(m, s);
-      else way_ms[job][lane] = make_float2(m, s);
+      if (ways == 1) col_ms[(pair << w.lg_heads) + lane] = make_float2(z.m, z.s);
+      else way_ms[job][lane] = make_float2(z.m, z.s);
     }
   }
   __syncthreads();
   const int cols = pairs << w.lg_heads;
-  if (ways > 1) {
-    for (int c = tid; c < cols; c += kWgThreads) {
-      const int pair = c >> w.lg_heads, head = c & (heads - 1);
-      float m = -INFINITY, s = 0.f;
-      for (int k = 0; k < ways; ++k) {
-        const float2 y = way_ms[pair * ways + k][head];
-        join_ms(m, s, y.x, y.y);
-      }
-      col_ms[c] = make_float2(m, s);
-    }
-  }
-  cluster_sync();
+  // several parts of a column, all read before they are joined
+  auto joined = [](auto part, int parts) {
+    float2 y[8];
+    float top = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = k < parts ? part(k) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, y[k].x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += y[k].x == top ? y[k].y : y[k].y * ex2_approx(y[k].x - top);
+    return make_float2(top, s);
+  };
+  static_assert(kWgWarps <= 8 && kWgMaxCtas <= 8, "parts of a column");
+  auto finish = [&](int c, float2 y) { lse[c] = y.x == -INFINITY ? INFINITY : y.x + lg2_approx(y.y); };  // none: no weight anywhere
   for (int c = tid; c < cols; c += kWgThreads) {
-    float m = -INFINITY, s = 0.f;
-    for (uint32_t k = 0; k < ctas; ++k) {
-      float2 y;
-      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(y.x), "=f"(y.y) : "r"(mapa(smem_u32(col_ms + c), k)));
-      join_ms(m, s, y.x, y.y);
-    }
-    lse[c] = m == -INFINITY ? INFINITY : m + lg2_approx(s);  // none: no weight anywhere
+    const int pair = c >> w.lg_heads, head = c & (heads - 1);
+    const float2 y = ways > 1 ? joined([&](int k) { return way_ms[pair * ways + k][head]; }, ways) : col_ms[c];
+    if (w.ctas == 1) finish(c, y);
+    else col_ms[c] = y;
+  }
+  if (w.ctas > 1) {
+    cluster_sync();
+    for (int c = tid; c < cols; c += kWgThreads)
+      finish(c, joined(
+                    [&](int k) {
+                      float2 y;
+                      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                                   : "=f"(y.x), "=f"(y.y)
+                                   : "r"(mapa(smem_u32(col_ms + c), k)));
+                      return y;
+                    },
+                    w.ctas));
   }
   __syncthreads();
-  cluster_arrive_relaxed();  // (the others' sums have been read)
-  // the blocks' shares, a warp a block
+  if (w.ctas > 1) cluster_arrive_relaxed();  // (the others' sums have been read)
+  // the blocks' shares, a warp four blocks at a time
   float *out = w.weights + r * w.stride;
-  const float *before = w.before ? w.before + r * w.before_stride : nullptr;
   const int all = pairs << w.lg_v;
-  for (int b = warp; b < n; b += kWgWarps) {
-    const float old = before && w.decay != 0.f ? before[c0 + b] : 0.f;
-    float sum = 0.f;
-#pragma unroll 4
+  constexpr int kAt = 4;
+  for (int b = warp; b < n; b += kAt * kWgWarps) {
+    float sum[kAt];
+#pragma unroll
+    for (int k = 0; k < kAt; ++k) sum[k] = 0.f;
+#pragma unroll 2
     for (int f = lane; f < all; f += 32) {
       const int pair = f >> w.lg_v, off = f & (v - 1), head = off & (heads - 1);
-      if (head < a.group && ((bits[pair * w.words + (b >> 5)] >> (b & 31)) & 1u))
-        sum += ex2_approx(base[pair * pair_stride + ((int64_t)b << w.lg_v) + off] - lse[(pair << w.lg_heads) + head]);
+      const float *src = base + pair * pair_stride + off;
+      const float ref = lse[(pair << w.lg_heads) + head];
+      float x[kAt];
+#pragma unroll
+      for (int k = 0; k < kAt; ++k) {
+        const int bk = b + k * kWgWarps;
+        x[k] = bk < n && head < a.group && ((bits[pair * w.words + (bk >> 5)] >> (bk & 31)) & 1u) ? src[(int64_t)bk << w.lg_v]
+                                                                                               : -INFINITY;
+      }
+#pragma unroll
+      for (int k = 0; k < kAt; ++k) sum[k] += x[k] == -INFINITY ? 0.f : ex2_approx(x[k] - ref);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) out[c0 + b] = (before && w.decay != 0.f ? w.decay * old : 0.f) + sum;
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < kAt; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
+    if (lane == 0)
+#pragma unroll
+      for (int k = 0; k < kAt; ++k)
+        if (b + k * kWgWarps < n) out[c0 + b + k * kWgWarps] = old[b + k * kWgWarps] + sum[k];
   }
-  for (int b = nb + rank * kWgThreads + tid; b < a.bt_width; b += ctas * kWgThreads) out[b] = 0.f;
-  cluster_wait();
+  for (int b = nb + rank * kWgThreads + tid; b < a.bt_width; b += w.ctas * kWgThreads) out[b] = 0.f;
+  if (w.ctas > 1) cluster_wait();
 }
 
-static cudaError_t launch_weights(WeightParams w, int sms, bool pdl, cudaStream_t stream) {
+// The requests' weights, and beside them what pa_attn_join_kernel would do:
+// neither needs the other.
+template <bool BY_HEAD>
+__global__ void __launch_bounds__(kWgThreads, BY_HEAD ? 3 : 5) pa_weights_kernel(const __grid_constant__ WeightParams w) {
+  const int to_weigh = w.at.R * w.ctas;
+  if ((int)blockIdx.x < to_weigh) return block_weights(w);
+  pdl_trigger();
+  pdl_wait();
+  const int k = blockIdx.x - to_weigh;
+  if (k >= w.join) return;  // (the grid is whole clusters)
+  attn_join<BY_HEAD ? kJoinWarps : 1>(w.at, w.sms, k % w.join_x, k / w.join_x);
+}
+
+static cudaError_t launch_weights(WeightParams w, int sms, bool pdl, bool to_join, cudaStream_t stream) {
   const int W = w.at.bt_width;
-  int ctas = 1;
-  while (ctas < kWgMaxCtas && (W > ctas * kWgMaxRun || (w.at.R * ctas < 2 * sms && W >= 32 * ctas))) ctas *= 2;
-  w.words = ((W + ctas - 1) / ctas + 31) / 32;
+  const int64_t values = (int64_t)w.at.q_len * w.at.n_kv * W << w.lg_v;  // of a request
+  w.ctas = 1;
+  while (w.ctas < kWgMaxCtas && (W > w.ctas * kWgMaxRun || (w.at.R * w.ctas < 2 * sms && values > (int64_t)w.ctas * kWgValues)))
+    w.ctas *= 2;
+  w.words = ((W + w.ctas - 1) / w.ctas + 31) / 32;
+  w.sms = sms;
+  const bool by_head = join_by_head(w.at, sms);
+  const dim3 g = join_grid(w.at, by_head);
+  w.join_x = g.x;
+  w.join = to_join ? g.x * g.y : 0;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.x = w.ctas;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   cfg.stream = stream;
-  cfg.gridDim = dim3((unsigned)(w.at.R * ctas));
+  cfg.gridDim = dim3((unsigned)(w.at.R * w.ctas + (w.join + w.ctas - 1) / w.ctas * w.ctas));
   cfg.blockDim = dim3(kWgThreads);
   cfg.dynamicSmemBytes = (size_t)w.at.q_len * w.at.n_kv * w.words * 4;
-  return cudaLaunchKernelEx(&cfg, pa_weights_kernel, w);
+  return cudaLaunchKernelEx(&cfg, by_head && to_join ? pa_weights_kernel<true> : pa_weights_kernel<false>, w);
 }
 
 // log2 of the heads that a (row, KV head) has in the partial sums.
@@ -219,7 +277,7 @@ extern "C" int pre_attn_attention_ext(const pa_attention_args *in, const pa_atte
   if (ext->window < 0 || ext->sinks < 0 || (ext->sinks > 0 && ext->window == 0)) return PA_ERR_CONFIG;
   if (ext->weights && (!(ext->decay >= 0.0f) || !std::isfinite(ext->decay))) return PA_ERR_CONFIG;
   pa::CacheAttnParams a;
-  int sms = 0, parts = 0;
+  int sms = 0;
   const int st = pa::attn_params(*in, a, &sms);
   if (st != PA_OK) return st;
   if (ext->window && in->blocks) return PA_ERR_UNSUPPORTED;
@@ -254,21 +312,23 @@ extern "C" int pre_attn_attention_ext(const pa_attention_args *in, const pa_atte
   a.wpart = ext->weights ? static_cast<float *>(ext->workspace) : nullptr;
   a.lg_heads = pa::lg_heads_of(a.group);
   const bool pdl = !(in->flags & PA_FLAG_NO_PDL), fp8 = in->cache_format == PA_CACHE_FP8;
-  cudaError_t e = fp8 ? pa::launch_attn<0, true>(a, sms, pdl, (cudaStream_t)stream, &parts)
-                      : pa::launch_attn<1, true>(a, sms, pdl, (cudaStream_t)stream, &parts);
-  if (e == cudaSuccess && ext->weights && !a.test_timeout) {
+  pa::AttnLaunched did;
+  pa::AttnLaunched *done = ext->weights ? &did : nullptr;  // (then the weights' kernel joins)
+  cudaError_t e = fp8 ? pa::launch_attn<0, true>(a, sms, pdl, (cudaStream_t)stream, done)
+                      : pa::launch_attn<1, true>(a, sms, pdl, (cudaStream_t)stream, done);
+  if (e == cudaSuccess && done && !a.test_timeout) {
     pa::WeightParams w = {};
     w.part = a.wpart;
     w.lg_heads = a.lg_heads;
-    w.lg_v = a.lg_heads + (parts == 4 ? 2 : parts - 1);
-    w.at = a;
+    w.lg_v = a.lg_heads + (did.parts == 4 ? 2 : did.parts - 1);
+    w.at = did.a;
     w.num_blocks = fp8 ? (a.num_pages16 >= 8 ? (a.num_pages16 - 8) / a.kps + 1 : 0) : a.kv_pages * a.bs / 128;
     w.weights = ext->weights;
     w.stride = ext->weights_stride;
     w.before = ext->weights_before;
     w.before_stride = ext->before_stride;
     w.decay = ext->decay;
-    e = pa::launch_weights(w, sms, pdl, (cudaStream_t)stream);
+    e = pa::launch_weights(w, sms, pdl, did.to_join, (cudaStream_t)stream);
   }
   return e == cudaSuccess ? PA_OK : pa::record_cuda_error(e);
 }
