@@ -104,7 +104,7 @@ struct AttnBatch {
 };
 
 // What the producing warps and the readers of a ring of blocks share.
-template <int ROWS>  // rows of an item at most
+template <int ROWS, int WIDTH = kAtMaxWidth>  // rows of an item at most, blocks of a row that lists name
 struct AttnRing {
   uint64_t full[kAtMaxStages], empty[kAtMaxStages];
   uint64_t batch_full[2], batch_empty[2];
@@ -115,7 +115,7 @@ struct AttnRing {
   AttnBatch batch[2];
   int offs[kAtMaxItems + 8];
   uint16_t list[ROWS * kAtMaxTopk];
-  uint32_t bits[ROWS][kAtMaxWidth / 32];
+  uint32_t bits[ROWS][WIDTH / 32];
 };
 
 constexpr int kAtSmem = 232448;  // 227 KB a CTA
@@ -440,10 +440,10 @@ __device__ __forceinline__ void attn_resolve(const CacheAttnParams &a, S &sh, co
   }
 }
 
-// One thread: an item's queries when its first batch comes, then a stage a
+// One thread: (QUERIES) an item's queries when its first batch comes, then a stage a
 // block; kGroups groups of readers take the entries in turn, and each segment
 // ends with an entry without a block for each of them.
-template <int FMT, int kStages, int kGroups, class S>
+template <int FMT, int kStages, int kGroups, bool QUERIES = true, class S>
 __device__ __forceinline__ void attn_copies(const CacheAttnParams &a, const AttnMaps &maps, S &sh, const AttnSlice &sl,
                                             uint8_t *ring, uint8_t *q_smem) {
   using St = AttnStage<FMT>;
@@ -457,7 +457,7 @@ __device__ __forceinline__ void attn_copies(const CacheAttnParams &a, const Attn
     const AttnBatch &bt = sh.batch[nbt & 1];
     if (!(ok = mbar_wait(&sh.batch_full[nbt & 1], (uint32_t)(nbt >> 1) & 1, a.status, a.lim))) break;
     const AttnItem x = attn_place(a, it);
-    if (bt.first) {
+    if (QUERIES && bt.first) {
       if (!(ok = mbar_wait(&sh.q_empty, (uint32_t)(nq & 1) ^ 1, a.status, a.lim))) break;
       sh.q_item = make_int2(bt.first_pos, bt.seq);
       const int es = a.q_is_fp8 ? 1 : 2, bytes = a.group * kHeadDim * es;

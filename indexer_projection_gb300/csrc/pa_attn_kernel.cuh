@@ -10,6 +10,7 @@
 
 #include "../../include/pre_attn.h"
 #include "pa_attn.cuh"
+#include "pa_attn_tc.h"
 
 namespace pa {
 
@@ -919,6 +920,26 @@ int attn_params(const pa_attention_args &x, CacheAttnParams &a, int *num_sms);
 // The second kernel of the sliced mode (pa_attn.cu).
 cudaError_t launch_attn_join(const CacheAttnParams &a, int sms, bool pdl, cudaStream_t stream);
 
+// Whether pa_attn_tc_kernel takes a call: its time hardly depends on the rows
+// of an item, that of pa_attn_kernel is in steps of 1, 2, 4 and 8 of them.
+// 64 requests x 2 KV heads in a window of 2047 keys, this / that kernel, us:
+// FP8 1 row 59 / 20, 4 rows 62 / 43, 5 rows 64 / 73, 7 rows 66 / 74; NVFP4 1 row
+// 43 / 19, 2 rows 43 / 29, 3 rows 44 / 53, 7 rows 47 / 93.
+inline bool use_attn_tc(const CacheAttnParams &a, int fmt) {
+  return a.rows_per >= (fmt == 0 ? 5 : 3) && (a.topk == 0 || a.bt_width <= kTcMaxWidth);
+}
+
+// A CTA an item, instead of even slices, where the items are about as long as
+// one another (a window, lists) and the longest CTA then has no more to do
+// than with slices, whose second segments and second kernel take as long as
+// about five blocks.
+inline bool whole_items(const CacheAttnParams &a, int sms) {
+  if (a.topk == 0 && a.window == 0) return false;
+  const int64_t blocks = a.topk ? a.topk : ((int64_t)a.sinks + 127) / 128 + ((int64_t)a.window + a.rows_per + 125) / 128 + 1;
+  const int64_t turns = ((int64_t)a.items + sms - 1) / sms;
+  return turns * blocks * sms <= a.items * blocks + 5 * sms;
+}
+
 // What pre_attn_attention_ext needs to know of a launch: the parts of a block
 // whose sums of weights the kernel writes, and, of the sliced mode, that the
 // second kernel is still to come, with these parameters.
@@ -1013,6 +1034,15 @@ cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cudaStream
       }
     }
     cfg.numAttrs = 1;
+  }
+  if constexpr (EXT) {
+    if (a.mode == kAtSliced && whole_items(a, sms)) a.mode = kAtWhole;
+    if (use_attn_tc(a, FMT)) {
+      const bool join = a.mode == kAtSliced;
+      if (done) *done = AttnLaunched{1, join, a};
+      e = launch_attn_tc(FMT, maps, a, join ? sms : a.items, pdl, stream);
+      return e != cudaSuccess || a.test_timeout || done || !join ? e : launch_attn_join(a, sms, pdl, stream);
+    }
   }
   if ((e = use(kSliced[variant], regs[0][variant])) != cudaSuccess) return e;
   if (done) *done = AttnLaunched{kSliced[variant].parts, a.mode == kAtSliced, a};
