@@ -724,7 +724,8 @@ int pre_attn_evict_blocks(const pa_evict_args *args, void *stream);
  * all.  So the tokens are distributed as the target's own.  Without q (a
  * drafter that is certain of its drafts) q_i is 1 at x_i and w is p_a without
  * x_a.  For w a probability counts as min(max(p, 0), 1), a NaN as 0, and what
- * it has below 2^-62 is dropped; the sums are exact, in 64-bit integers, so
+ * it has below 2^-62 is dropped (2^-46 where all the call's probabilities are
+ * bf16); the sums are exact, in 64-bit integers, so
  * the token does not depend on how the work is split (a row whose values sum to 4 or
  * more, which no row of probabilities does, draws any token or none).
  * An x_i >= vocab is never accepted and raises PA_DEV_TOKEN_RANGE (without q,

@@ -68,6 +68,8 @@ __device__ __forceinline__ f32x2 add2_down(f32x2 a, f32x2 b) {
 struct Digits {
   int d[3][2];  // of two tokens
 };
+// N 2: the last digit left out.
+template <int N>
 __device__ __forceinline__ Digits digits_of(float p0, float p1) {
   const f32x2 c1 = pack2(1.f, 1.f), c2 = pack2(0x1p-23f, 0x1p-23f), c3 = pack2(0x1p-39f, 0x1p-39f);
   const f32x2 m1 = pack2(-1.f, -1.f), m2 = pack2(-0x1p-23f, -0x1p-23f);
@@ -75,8 +77,8 @@ __device__ __forceinline__ Digits digits_of(float p0, float p1) {
   const f32x2 r1 = add2_down(p, c1);
   p = fma2(add2(r1, m1), m1, p);  // (exact: multiples of 2^-23 below 2)
   const f32x2 r2 = add2_down(p, c2);
-  p = fma2(add2(r2, m2), m1, p);
-  const f32x2 r3 = add2_down(p, c3);
+  if constexpr (N == 3) p = fma2(add2(r2, m2), m1, p);
+  const f32x2 r3 = N == 3 ? add2_down(p, c3) : c3;
   const float2 a = unpack2(r1), b = unpack2(r2), c = unpack2(r3);
   return Digits{{{__float_as_int(a.x), __float_as_int(a.y)},
                  {__float_as_int(b.x), __float_as_int(b.y)},
@@ -154,6 +156,8 @@ struct ProbRow<__nv_bfloat16, 8, IN> {
 // The rows that a request's token is drawn from.
 template <typename TP, typename TQ, int E>
 struct Draw {
+  static constexpr int kDigits = sizeof(TP) == 2 && sizeof(TQ) == 2 ? 2 : 3;  // (16-bit values: see the head of this file)
+  static __device__ __forceinline__ Digits digits(float p0, float p1) { return digits_of<kDigits>(p0, p1); }
   const TP *P;
   const TQ *Q;         // or null
   int without;         // the token that weighs nothing, or -1
@@ -219,16 +223,16 @@ struct Draw {
       const Loaded x = next;
       if (v + 2 * kStep <= v1) load(next, v + kStep);
       // (without a draft row its digits are the constants')
-      const Digits none = digits_of(0.f, 0.f);
+      const Digits none = digits(0.f, 0.f);
       int d[3];
 #pragma unroll
       for (int k = 0; k < 3; ++k) d[k] = DRAFT ? 0 : -IN * none.d[k][0];
 #pragma unroll
       for (int i = 0; i < IN; i += 2) {
         float p0 = counted(x.p.get(i)), p1 = counted(x.p.get(i + 1));
-        const Digits s = digits_of(p0, p1);
+        const Digits s = digits(p0, p1);
         if constexpr (DRAFT) {
-          const Digits y = digits_of(fminf(counted(x.q.get(i)), p0), fminf(counted(x.q.get(i + 1)), p1));
+          const Digits y = digits(fminf(counted(x.q.get(i)), p0), fminf(counted(x.q.get(i + 1)), p1));
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
             d[k] += s.d[k][0] - y.d[k][0];
@@ -243,7 +247,7 @@ struct Draw {
     }
     // `without` is among them: its weight once
     if (!DRAFT && without >= v0 && without < v && (threadIdx.x & 31) == 0) {
-      const Digits y = digits_of(counted(prob(P + without)), 0.f);
+      const Digits y = digits(counted(prob(P + without)), 0.f);
       sum -= value_of(y.d[0][0] - y.d[0][1], y.d[1][0] - y.d[1][1], y.d[2][0] - y.d[2][1]);
     }
     for (; v < v1; v += 32 * 8) sum += part(v, v1);
@@ -265,7 +269,7 @@ struct Draw {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       clamp(p[i], q[i]);
-      const Digits s = digits_of(p[i], q[i]);
+      const Digits s = digits(p[i], q[i]);
       each[i] = value_of(s.d[0][0] - s.d[0][1], s.d[1][0] - s.d[1][1], s.d[2][0] - s.d[2][1]);
     }
   }

@@ -15,14 +15,14 @@ def B():
     return binding
 
 
-def units(p):
-    """Probabilities in whole units of 2^-62 (what is below is dropped), as uint64."""
+def units(p, bits=62):
+    """Probabilities in whole units of 2^-bits (what is below is dropped), as uint64."""
     p = np.nan_to_num(np.asarray(p, np.float64), nan=0.0)
-    return np.floor(np.clip(p, 0.0, 1.0) * 2.0 ** 62).astype(np.uint64)  # exact: a power of two times 24 bits
+    return np.floor(np.clip(p, 0.0, 1.0) * 2.0 ** bits).astype(np.uint64)  # exact: a power of two times 24 bits
 
 
-def expected(target, q, drafts, u, V):
-    """One request: target [q_len, V], q [q_len - 1, V] or None, as f64 arrays: (tokens, accepted, status)."""
+def expected(target, q, drafts, u, V, bits=62):
+    """One request: target [q_len, V], q [q_len - 1, V] or None, as f64 arrays, in units of 2^-bits: (tokens, accepted, status)."""
     k, status = len(drafts), 0
     n = next((i for i, x in enumerate(drafts) if x < 0), k)
     if any(x >= V for x in drafts[:n]):
@@ -33,16 +33,16 @@ def expected(target, q, drafts, u, V):
         if not float(u[a]) * (float(q[a][x]) if q is not None else 1.0) < float(target[a][x]):
             break
         a += 1
-    w = units(target[a])
+    w = units(target[a], bits)
     if a < n:
         if q is not None:
-            d = units(q[a])
+            d = units(q[a], bits)
             w = np.where(w > d, w - d, np.uint64(0))
         elif drafts[a] < V:
             w = w.copy()
             w[drafts[a]] = 0
         if not w.any():
-            w = units(target[a])
+            w = units(target[a], bits)
     total = int(w.sum(dtype=np.uint64))
     if total == 0:
         return list(drafts[:a]) + [-1] * (k + 1 - a), a, status | 16
@@ -73,9 +73,10 @@ def check(target, q, drafts, u, V, verifier=None, stride=None, status=None):
     torch.cuda.synchronize()
     got, acc, st = tokens.tolist(), accepted.tolist(), ver.device_status()
     want_st = 0
+    bits = 46 if target.dtype is torch.bfloat16 and (q is None or q.dtype is torch.bfloat16) else 62
     for r in range(R):
         tok, a, s = expected(target[r].double().numpy(), q[r].double().numpy() if q is not None else None,
-                             drafts[r].tolist(), u[r], V)
+                             drafts[r].tolist(), u[r], V, bits)
         assert (got[r], acc[r]) == (tok, a), r
         want_st |= s
     assert st == want_st and (status is None or st == status)
@@ -170,6 +171,10 @@ def test_values_that_are_no_probabilities():
     check(target, q, x, torch.rand(20, 3, generator=g).numpy(), V)
     target[0, 0, 5] = float("inf")   # counts as 1
     check(target, q, x, torch.rand(20, 3, generator=g).numpy(), V)
+    check(target.bfloat16(), q.bfloat16(), x, torch.rand(20, 3, generator=g).numpy(), V)
+    tiny = torch.exp2(-60 * torch.rand(20, 3, V, generator=g))  # over all of the units
+    check(tiny / V, tiny[:, :2] / V * 0.9, x, torch.rand(20, 3, generator=g).numpy(), V)
+    check((tiny / V).bfloat16(), (tiny[:, :2] / V * 0.9).bfloat16(), x, torch.rand(20, 3, generator=g).numpy(), V)
 
 
 @pytest.mark.gpu
