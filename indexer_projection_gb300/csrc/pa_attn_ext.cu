@@ -67,8 +67,9 @@ __device__ __forceinline__ void block_weights(const WeightParams &w) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = cta_rank(), r = blockIdx.x / w.ctas;
   // What the attention did not write can be read before the wait on it: the
-  // attention lets this kernel in when the kernels before it are done.
-  const int seq = __ldg(a.seq_lens + r);
+  // attention lets this kernel in when the kernels before it are done (loads
+  // that go to L2, which has what those wrote).
+  const int seq = __ldcg(a.seq_lens + r);
   const bool none = seq < a.q_len || (seq - 1) / 128 + 1 > a.bt_width;  // without keys (the attention flags it)
   const int nb = none ? 0 : (seq - 1) / 128 + 1, first = seq - a.q_len;
   const int c0 = (int)((int64_t)nb * rank / w.ctas), c1 = (int)((int64_t)nb * (rank + 1) / w.ctas), n = c1 - c0;
@@ -76,7 +77,7 @@ __device__ __forceinline__ void block_weights(const WeightParams &w) {
   // the blocks that the attention has summed
   for (int wi = warp; 32 * wi < n; wi += kWgWarps) {
     const int b = c0 + 32 * wi + lane;
-    const int64_t id = b < c1 ? __ldg(a.block_table + (int64_t)r * a.bt_width + b) : -1;
+    const int64_t id = b < c1 ? __ldcg(a.block_table + (int64_t)r * a.bt_width + b) : -1;
     const bool in = id >= 0 && id < w.num_blocks;
     if (a.topk) {
       const uint32_t all = __ballot_sync(0xffffffffu, in);
@@ -90,13 +91,13 @@ __device__ __forceinline__ void block_weights(const WeightParams &w) {
     }
   }
   const float *before = w.before && w.decay != 0.f ? w.before + r * w.before_stride : nullptr;
-  for (int b = tid; b < n; b += kWgThreads) old[b] = before ? w.decay * before[c0 + b] : 0.f;
+  for (int b = tid; b < n; b += kWgThreads) old[b] = before ? w.decay * __ldcg(before + c0 + b) : 0.f;
   __syncthreads();
   if (a.topk && n > 0) {
     const int64_t at = (int64_t)r * pairs;
     for (int e = tid; e < pairs * a.topk; e += kWgThreads) {
-      const int k = e / a.topk, b = __ldg(a.blocks + at * a.topk + e);
-      if (e - k * a.topk < __ldg(a.counts + at + k) && b >= c0 && b < c1 && b <= (first + k / a.n_kv) / 128 &&
+      const int k = e / a.topk, b = __ldcg(a.blocks + at * a.topk + e);
+      if (e - k * a.topk < __ldcg(a.counts + at + k) && b >= c0 && b < c1 && b <= (first + k / a.n_kv) / 128 &&
           ((held[(b - c0) >> 5] >> ((b - c0) & 31)) & 1u))
         atomicOr(&bits[k * w.words + ((b - c0) >> 5)], 1u << ((b - c0) & 31));
     }

@@ -19,9 +19,6 @@ namespace pa {
 
 constexpr int kEvMaxWidth = 16384;
 constexpr int kEvMaxThreads = 1024;
-// Counters a digit: weights have few exponents, and a warp's additions to one
-// counter go one after the other.
-constexpr int kEvCopies = 8;
 
 struct EvictParams {
   const float *weights;
@@ -52,15 +49,14 @@ __device__ __forceinline__ int warps_before(const int *c, int warps, int warp, i
 
 template <int K>  // entries a thread
 __global__ void __launch_bounds__(kEvMaxThreads) pa_evict_kernel(const __grid_constant__ EvictParams a) {
-  __shared__ __align__(16) uint32_t hist[2][256 * kEvCopies];  // counter of digit d: kEvCopies d .. + kEvCopies - 1, by the lane
-  __shared__ uint32_t digit_count[256];
+  __shared__ uint32_t hist[2][256];
   __shared__ int3 pick;  // the digit found, what remains to stay in it, what it holds
   __shared__ uint2 warp_range[32];
   __shared__ int warp_count[2][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
   const int r = blockIdx.x;
   const int first = warp * 32 * K + lane;  // entry k of the thread: first + 32 k
-  for (int d = tid; d < 2 * 256 * kEvCopies; d += blockDim.x) hist[0][d] = 0;
+  for (int d = tid; d < 512; d += blockDim.x) hist[d >> 8][d & 255] = 0;
   pdl_wait();
   pdl_trigger();
   const int n = a.seq_lens[r];  // (plain loads: the outputs may be the inputs)
@@ -112,17 +108,12 @@ __global__ void __launch_bounds__(kEvMaxThreads) pa_evict_kernel(const __grid_co
 #pragma unroll
         for (int k = 0; k < K; ++k)
           if (key[k] != 0xffffffffu && (left == 32 || ((key[k] ^ T) >> left) == 0))
-            atomicAdd(&h0[((key[k] >> shift) & ((1u << bits) - 1u)) * kEvCopies + (lane & (kEvCopies - 1))], 1u);
-        __syncthreads();
-        for (int d = tid; d < 256; d += blockDim.x) {
-          const uint4 x = *reinterpret_cast<const uint4 *>(h0 + d * kEvCopies), y = *reinterpret_cast<const uint4 *>(h0 + d * kEvCopies + 4);
-          digit_count[d] = x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
-        }
+            atomicAdd(&h0[(key[k] >> shift) & ((1u << bits) - 1u)], 1u);
         __syncthreads();
         if (warp == 0) {  // digits from the top: lane l holds 255 - 8 l .. 248 - 8 l
           int c[8], sum = 0;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) sum += c[k] = (int)digit_count[255 - 8 * lane - k];
+          for (int k = 0; k < 8; ++k) sum += c[k] = (int)h0[255 - 8 * lane - k];
           int incl = sum;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -144,7 +135,7 @@ __global__ void __launch_bounds__(kEvMaxThreads) pa_evict_kernel(const __grid_co
           T -= 1, need = 0;
           break;
         }
-        for (int d = tid; d < 256 * kEvCopies; d += blockDim.x) h0[d] = 0;  // (used again two passes on)
+        for (int d = tid; d < 256; d += blockDim.x) h0[d] = 0;  // (used again two passes on)
       }
     }
   }

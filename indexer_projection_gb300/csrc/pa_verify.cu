@@ -66,7 +66,7 @@ __device__ __forceinline__ f32x2 add2_down(f32x2 a, f32x2 b) {
   return r;
 }
 struct Digits {
-  int d[3][2];  // of two tokens
+  uint32_t d[3][2];  // of two tokens; sums and differences modulo 2^32
 };
 // N 2: the last digit left out.
 template <int N>
@@ -80,12 +80,13 @@ __device__ __forceinline__ Digits digits_of(float p0, float p1) {
   if constexpr (N == 3) p = fma2(add2(r2, m2), m1, p);
   const f32x2 r3 = N == 3 ? add2_down(p, c3) : c3;
   const float2 a = unpack2(r1), b = unpack2(r2), c = unpack2(r3);
-  return Digits{{{__float_as_int(a.x), __float_as_int(a.y)},
-                 {__float_as_int(b.x), __float_as_int(b.y)},
-                 {__float_as_int(c.x), __float_as_int(c.y)}}};
+  return Digits{{{__float_as_uint(a.x), __float_as_uint(a.y)},
+                 {__float_as_uint(b.x), __float_as_uint(b.y)},
+                 {__float_as_uint(c.x), __float_as_uint(c.y)}}};
 }
-__device__ __forceinline__ int64_t value_of(int d1, int d2, int d3) {
-  return ((int64_t)d1 << 39) + ((int64_t)d2 << 16) + d3;
+// (digits' differences are small, of either sign)
+__device__ __forceinline__ int64_t value_of(uint32_t d1, uint32_t d2, uint32_t d3) {
+  return (int64_t)(int)d1 * (1ll << 39) + (int64_t)(int)d2 * (1ll << 16) + (int)d3;
 }
 // a probability as it counts: [0, 1], 0 for a NaN
 __device__ __forceinline__ float counted(float p) { return __saturatef(p); }
@@ -224,9 +225,9 @@ struct Draw {
       if (v + 2 * kStep <= v1) load(next, v + kStep);
       // (without a draft row its digits are the constants')
       const Digits none = digits(0.f, 0.f);
-      int d[3];
+      uint32_t d[3];
 #pragma unroll
-      for (int k = 0; k < 3; ++k) d[k] = DRAFT ? 0 : -IN * none.d[k][0];
+      for (int k = 0; k < 3; ++k) d[k] = DRAFT ? 0u : 0u - (uint32_t)IN * none.d[k][0];
 #pragma unroll
       for (int i = 0; i < IN; i += 2) {
         float p0 = counted(x.p.get(i)), p1 = counted(x.p.get(i + 1));

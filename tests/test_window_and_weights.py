@@ -170,6 +170,24 @@ def test_weights_in_every_way_of_dealing_blocks(fmt, q_len, group, mode):
     assert torch.equal(out, again[0]) and torch.equal(w, again[1]) and rd.device_status() == 0  # the same bits
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("W", [4096, 4097, 16384])
+def test_lists_of_wide_tables(fmt, W):
+    c = case(fmt, [1000, 700, 129], 7, 1, 16, seed=W).upload()
+    blocks, counts, lists = ref.random_lists(c, 4, seed=3)
+    narrow = c.attention(lists), c.weights(lists)
+    c.bt = np.concatenate((c.bt, np.full((3, W), -1, np.int32)), 1)[:, :W].copy()
+    c.W, c.dev["bt"] = W, torch.from_numpy(c.bt).cuda()
+    rd = c.reader(topk=4, weigh=True)
+    out, w = win.attend(c, rd, (blocks, counts), weights=True)
+    assert rd.device_status() == 0
+    win.close(out, narrow[0])
+    k = narrow[1][0].shape[1]
+    assert (w[:, k:] == 0).all()
+    over = np.abs(w[:, :k].double().cpu().numpy() - narrow[1][0]) - narrow[1][1]
+    assert (over <= 0).all()
+
+
 @pytest.mark.parametrize("W", [33, 64, 2049, 16384])
 def test_weights_of_wide_tables(W):
     # short requests in wide tables: each cluster size, columns of zeros behind the last block
@@ -220,6 +238,81 @@ def test_weights_of_peaked_rows_and_far_magnitudes(fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("q_len", [1, 3, 5, 8])
+@pytest.mark.parametrize("window", [0, 260])
+def test_far_scales_and_peaked_rows(fmt, q_len, window):
+    # V scales over 2^24, a zero value row with scale 1 that takes nearly all the weight (FP8); head rows of queries from
+    # 2^-30 to 2^5: nearly even weights and a single one
+    c = case(fmt, [700, 130, 512], q_len, 2, 16, window, 4 if window else 0, seed=30 + q_len, spread=24.0)
+    c.q = (c.q.float().view(-1, 2, 16, 128) * torch.tensor([2.0 ** e for e in range(-30, 6, 9)] * 4)[:, None]).to(torch.bfloat16).view(c.M, -1)
+    if fmt == "fp8":
+        n = 700
+        slot = int(c.bt[0, (n - q_len) // 128]) * 128 + (n - q_len) % 128
+        page, t = slot // 128 * c.kps + slot % 128 // 16, slot % 16
+        for h in range(2):
+            base = (page * 2 + h) * 2048
+            c.bytes["v"][base + np.arange(128) * 16 + t] = 0
+            c.scales["v"][(page * 2 + h) * 16 + t] = 1.0
+            c.v[h, slot], c.vs[h, slot] = 0.0, 1.0
+    c.upload()
+    rd = c.reader(weigh=True)
+    out, w = win.attend(c, rd, weights=True)
+    win.close(out, c.attention())
+    win.close_weights(w, c, c.weights())
+    assert rd.device_status() == 0
+
+
+def put_nan(c, what, r, j):
+    """NaN in key j of request r, KV head 0: a value's code (FP8) or the scale of its dims 32 .. 47 (NVFP4), a scale of FP8."""
+    slot = int(c.bt[r, j // 128]) * 128 + j % 128
+    if c.fmt == "fp8":
+        page, t = slot // 128 * c.kps + slot % 128 // 16, slot % 16
+        if what == "value":
+            c.bytes["v"][page * c.nkv * 2048 + 37 * 16 + t] = 0xff
+        else:
+            c.scales[what][page * c.nkv * 16 + t] = float("nan")
+    else:
+        flat, t = c.kv.reshape(-1), slot % c.bs
+        base = slot // c.bs * c.page_bytes + c.bs * 64
+        flat[base + t * 8 + 2 if what == "k" else base + c.bs * 72 + (t // 4 * 4 + 1) * 8 + t % 4] = 0x7f
+
+
+@pytest.mark.parametrize("fmt,what", [("fp8", "value"), ("fp8", "k"), ("fp8", "v"), ("nvfp4", "value"), ("nvfp4", "k")])
+@pytest.mark.parametrize("q_len", [2, 4, 7])
+@pytest.mark.parametrize("lists", [False, True])
+def test_a_nan_reaches_the_rows_that_see_it(fmt, what, q_len, lists):
+    n, window = 700, 0 if lists else 260
+    c = case(fmt, [n, 300], q_len, 1, 16, window, 2 if window else 0, seed=50 + q_len)
+    sel = None
+    if lists:  # rows of even number attend block 1
+        blocks, counts = np.tile(np.array([0, 2, 5], np.int32), (c.M, 1, 1)), np.full((c.M, 1), 3, np.int32)
+        blocks[::2, 0, 1] = 1
+        sel = [[[b for b in blocks[m, 0] if b * 128 < (n if m < q_len else 300)]] for m in range(c.M)]
+        blocks[q_len:, 0, 2], counts[q_len:] = -1, 2
+        keys = [130, n - 2]
+    else:
+        keys = [n - q_len + 1 - window, n - 2, 300]  # the window's end, the rows' own keys, one that none sees
+    want = c.attention(sel)
+    for j in keys:
+        put_nan(c, what, 0, j)
+    c.upload()
+    got = win.attend(c, c.reader(topk=3 if lists else 0), (blocks, counts) if lists else None)
+    got = got.double().cpu().numpy().reshape(c.M, 16, 128)
+    dims = np.ones(128, bool)
+    if what == "value":
+        dims[:] = False
+        dims[37 if fmt == "fp8" else slice(32, 48)] = True
+    nan = np.zeros(got.shape, bool)
+    for i in range(q_len):
+        if set(keys) & set(c.row_positions(0, i, None if sel is None else sel[i][0]).tolist()):
+            nan[i][:, dims] = True
+    assert nan[:q_len].any() and (q_len == 2 or not nan[:q_len].all())
+    assert (np.isnan(got) == nan).all()
+    over = np.where(nan, -1.0, np.abs(got - want[0].reshape(got.shape)) - want[1].reshape(got.shape))
+    assert (over <= 0).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_a_row_of_nan_stays_in_its_request(fmt):
     c = case(fmt, [300, 200], 2, 1, 16, seed=20)
     c.q[1, 5 * 128 + 3] = float("nan")
@@ -259,12 +352,60 @@ def test_a_wait_that_runs_out_is_reported(fmt, q_len):
     win.close_weights(w, c, c.weights())
 
 
-@pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("seq", [[1000, 64, 5000], [40000, 700, 64]])
-def test_captured_in_order_and_on_another_stream(fmt, seq):
+@pytest.mark.parametrize("fmt,q_len,seq", [("fp8", 7, [20000, 700]), ("nvfp4", 3, [20000, 700]), ("nvfp4", 7, [300] * 2100)])
+def test_a_wait_that_runs_out_while_items_are_cut_or_whole(fmt, q_len, seq):
     from indexer_projection_gb300 import binding as B
 
-    c = case(fmt, seq, 2, 2, 16, 900, 130, seed=21).upload()
+    c = case(fmt, seq, q_len, 1, 2, 0, 0, seed=24).upload()
+    late, rd = c.reader(flags=B.PA_FLAG_TEST_WAIT_TIMEOUT, weigh=True), c.reader(weigh=True)
+    out, w = torch.full((c.M, 256), 3.0, dtype=torch.bfloat16, device="cuda"), torch.full((c.R, c.W), 3.0, device="cuda")
+    late.attend(c.dev["q"], c.dev["bt"], c.dev["seq"], out, weights=w)
+    assert late.device_status() == B.PA_DEV_WAIT_TIMEOUT and (w == 3).all()
+    first = win.attend(c, rd, weights=True)
+    again = win.attend(c, rd, weights=True)
+    assert rd.device_status() == 0 and torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    some = [0, 1, c.R - 1]
+    total = first[1][some].double().sum(1).cpu()
+    assert torch.allclose(total, torch.full_like(total, q_len * 2.0), rtol=2.0 ** -12)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_two_readers_at_once(fmt):
+    # on two streams, each with a workspace of its own, one of them in a graph: the results of one at a time
+    cases = [case(fmt, [9000, 300, 77], 7, 2, 16, 2000, 4, seed=25).upload(), case(fmt, [500, 12000], 2, 2, 16, 0, 0, seed=26).upload()]
+    readers = [c.reader(weigh=True) for c in cases]
+    want = [win.attend(c, rd, weights=True) for c, rd in zip(cases, readers)]
+    got = [[torch.zeros_like(x) for x in pair] for pair in want]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    go = lambda k: readers[k].attend(*(cases[k].dev[n] for n in ("q", "bt", "seq")), got[k][0], window=cases[k].window,  # noqa: E731
+                                     sinks=cases[k].sinks, weights=got[k][1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=streams[0]):
+        go(0)
+    for turn in range(6):
+        for pair in got:
+            for x in pair:
+                x.fill_(9)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            with torch.cuda.stream(streams[0]):
+                g.replay()
+            with torch.cuda.stream(streams[1]):
+                go(1)
+        torch.cuda.synchronize()
+        for k in range(2):
+            assert torch.equal(got[k][0], want[k][0]) and torch.equal(got[k][1], want[k][1])
+    assert all(rd.device_status() == 0 for rd in readers)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("seq", [[1000, 64, 5000], [40000, 700, 64]])
+@pytest.mark.parametrize("q_len", [2, 7])
+def test_captured_in_order_and_on_another_stream(fmt, seq, q_len):
+    from indexer_projection_gb300 import binding as B
+
+    c = case(fmt, seq, q_len, 2, 16, 900, 130, seed=21).upload()
     rd, ordered = c.reader(weigh=True), c.reader(weigh=True, flags=B.PA_FLAG_NO_PDL)
     out, w = torch.zeros(c.M, 32 * 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(c.R, c.W, device="cuda")
     want = c.attention(), c.weights()
