@@ -83,6 +83,11 @@ class PreAttn:
         return B.pre_attn_device_status(self.workspace, stream)
 
 
+def _int32(x: int) -> int:
+    """A count as the argument structs hold it (ctypes would drop the bits above)."""
+    return max(-2 ** 31, min(x, 2 ** 31 - 1))
+
+
 class _Calls:
     """What the front ends below share: a device, a workspace that begins with a status word, and the calls' streams."""
 
@@ -321,7 +326,7 @@ class CacheReader(_Calls):
                 raise ValueError("weights_before come with the weights")
             return self._call(self._attn_entry, stream, check) if R else B.PA_OK
         e = self._ext
-        e.window, e.sinks, e.weights, e.weights_before = window, sinks, None, None
+        e.window, e.sinks, e.weights, e.weights_before = _int32(window), _int32(sinks), None, None
         if weights is not None:
             if not self.weigh:
                 raise ValueError("weights come from a reader made with weigh=True")
@@ -357,7 +362,7 @@ class CacheReader(_Calls):
             a.seq_lens_out = seq_lens_out.data_ptr()
         self._ints(evicted, (R, W), "evicted")
         self._ints(counts, (R,), "counts")
-        a.evicted, a.counts, a.R, a.keep = evicted.data_ptr(), counts.data_ptr(), R, keep
+        a.evicted, a.counts, a.R, a.keep = evicted.data_ptr(), counts.data_ptr(), R, _int32(keep)
         if R == 0:
             return B.PA_OK
         return self._call(self._evict_entry, stream, check)

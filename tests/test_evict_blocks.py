@@ -120,7 +120,7 @@ def test_strides_reserved_entries_and_lengths_beyond_the_table(in_place):
 def test_every_number_kept():
     w, table = inputs(4, 37, 9, "ties")
     rd = reader(37, 1, 2)
-    for keep in range(3, 41):
+    for keep in (*range(3, 41), 2 ** 32 + 3):
         check(w, table, np.array([37 * 128, 35 * 128 + 1, 129, 20 * 128], np.int32), keep, 1, 2, rd=rd)
 
 

@@ -85,7 +85,7 @@ def test_a_window_as_wide_as_the_table_is_none(fmt):
     c = case(fmt, [900, 300], 2, 1, 16, seed=5).upload()
     rd = c.reader()
     want = win.attend(c, rd)
-    for c.window, c.sinks in ((c.W * 128, 3), (2 ** 31 - 1, 2 ** 31 - 1), (c.W * 128 - 1, 0)):
+    for c.window, c.sinks in ((c.W * 128, 3), (2 ** 31 - 1, 2 ** 31 - 1), (c.W * 128 - 1, 0), (2 ** 32 + 2, 2 ** 32)):
         assert torch.equal(win.attend(c, rd), want)
     c.window, c.sinks = 2, 2 ** 31 - 1  # sinks past every key
     win.close(win.attend(c, rd), c.attention())
