@@ -3,19 +3,27 @@
 // max(p - q, 0), or from p where every draft was accepted, by its running sum.
 //
 // The drafts' test takes a few scattered loads, the draw one row of p and one
-// of q (4 or 2 bytes a token and row: HBM bounds large batches, a chain of
-// latencies the small ones).  A cluster of CTAs takes a request; each CTA
-// finds the row by itself and sums its part of the vocabulary, a warp a
+// of q (4 or 2 bytes a token and row).  A cluster of CTAs takes a request; each
+// CTA finds the row by itself and sums its part of the vocabulary, a warp a
 // contiguous run; the warps' sums go to every CTA of the cluster, whose warps
-// then know which run the drawn token lies in, and that run's warp reads it
-// again (from L2) and finds it.
+// then know which run the drawn token lies in, and the CTA of that run reads it
+// again (from L2), 256 tokens a warp, and finds it.
 //
 // A weight is held in 64-bit fixed point, in units of 2^-62: a probability in
 // [2^-38, 1] exactly (24 bits of mantissa), so that the difference p - q and
 // all sums are exact, whatever their order, and equal inputs give equal tokens
 // for any split.  (f32 sums of a vocabulary of 2^17 would move the drawn token
 // in about one draw of a hundred; f64 adds run at a sixty-fourth of the f32
-// rate here.)
+// rate here.)  Where all probabilities have 8 bits of mantissa the units are
+// 2^-46, what [2^-38, 1] takes, and the last of the three digits below is left
+// out.
+//
+// Measured: 1 request of 32000 tokens 5.0 us (a launch and five dependent
+// latencies: drafts, rows, sums, the cluster's exchange, the run again); 64 of
+// 129281, f32 p and q, 17.5 us, 3.6 TB/s, of which the latencies, that nothing
+// runs beside, are about 7 (a vocabulary of 1000 on as many CTAs) and the rows 10;
+// 128 of 200064, bf16 p, 18.9 us, 2.7 TB/s (the same, and a 16-bit value costs
+// as many additions as a 32-bit one; rows that begin off a 16-byte boundary 23).
 #include <algorithm>
 #include <cstdint>
 
@@ -374,8 +382,16 @@ __global__ void __launch_bounds__(kVfThreads, kVfPerSm) pa_verify_kernel(const _
 
 template <typename TP, typename TQ>
 static cudaError_t launch_verify(VerifyParams a, int sms, cudaStream_t stream) {
-  a.ctas = kVfMaxCtas;  // as many as are resident at once
-  while (a.ctas > 1 && a.R * a.ctas > sms * kVfPerSm) --a.ctas;
+  // As many CTAs a request as are resident at once.  2 / 4 / 8 of them, us: 1
+  // request 6.9 / 5.6 / 5.0, 64 requests 31.4 / 20.6 / 17.5 (512 CTAs of 608), 128
+  // requests 22.6 / 18.8 / 21.4 (8: two turns)
+  // .. while a CTA has 2048 tokens or, beyond one an SM, 8192 (512 CTAs take 3 us
+  // more than 64 to start and join): 64 requests of 4000 tokens 7.5 on eight CTAs,
+  // 4.6 on two, 16000 tokens 7.5 on eight, 5.8 on two; 1 request of 16000 4.4 on
+  // eight, 5.4 on two.
+  auto least = [&] { return a.R * a.ctas > sms ? 8192 : 2048; };
+  a.ctas = kVfMaxCtas;
+  while (a.ctas > 1 && (a.R * a.ctas > sms * kVfPerSm || a.vocab < (a.ctas - 1) * least())) --a.ctas;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
