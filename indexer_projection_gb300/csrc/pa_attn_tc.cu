@@ -13,6 +13,17 @@
 // core's work for the other.  P replaces S in tensor memory, as the A operand
 // of the second product.
 //
+// What bounds it (FP8, 128 items of 7 rows x 16 heads and 18 blocks, 65 us, 1.2
+// TB/s): instructions.  A block takes 11400 warp instructions, 6850 of them the
+// softmax's (1700 a warp, of 32 (row, head)s x 128 keys), at about 0.57 a clock
+// and scheduler: 2.5 us.  In front are 5 us to the first keys and 8 to the first
+// products (code that is not in the caches yet), behind 6 to the last store.
+// NVFP4 1.5 us a block.  Right and no faster: one pass over the scores with the
+// references looked at turn by turn (65; fewer instructions, more of them in
+// branches); 16 softmax warps of 16 (row, head)s, a quarter of the keys a lane
+// (74: 30% more instructions); 16 converting warps (77: no registers left for
+// them); all eight converters on keys, then on values (70).
+//
 // Arithmetic as in pa_attn.cu (references, lift, unit of the products), the
 // state of a (row, head) in one thread's registers: no exchange but at the
 // segment's end, where the two groups' parts are added up.
@@ -34,7 +45,7 @@ namespace pa {
 constexpr int kTcThreads = 640;  // 8 softmax, 8 converting, 4 other warps
 constexpr int kTcSoftRegs = 136, kTcConvRegs = 72, kTcCtlRegs = 64;  // a thread, after the split
 constexpr int kTcTile = 128 * 256;  // bytes of an f16 tile of 128 x 128
-constexpr int kTcKeys = 32;         // keys a softmax thread takes at a time
+constexpr int kTcKeys = 32;         // keys a softmax thread takes at a time (tc_ld32)
 // When the references move: that of the products (NVFP4: the weights) once one
 // is above 2^15; FP8's weights stay in f32, and theirs when they leave that.
 constexpr float kTcMost = 15.f;
@@ -102,11 +113,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a_tmem, uint64_t
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void tc_st(uint32_t taddr, const float (&v)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
-}
 __device__ __forceinline__ void tc_st(uint32_t taddr, const float (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -114,8 +120,6 @@ __device__ __forceinline__ void tc_st(uint32_t taddr, const float (&v)[16]) {
       "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
       : "memory");
 }
-__device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[16]) { tc_ld16(taddr, v); }
-__device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[32]) { tc_ld32(taddr, v); }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -643,7 +647,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
           const f32x2 sc2 = pack2(sc, sc);
           constexpr int kTurns = 128 / kTcKeys;
           float next[kTcKeys];
-          tc_ld(s_col, next);
+          tc_ld32(s_col, next);
 #pragma unroll 1
           for (int i = 0; i < 2 * kTurns; ++i) {
             const int c = i & (kTurns - 1);
@@ -659,7 +663,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
               }
               y[e] = fma2(pack2(next[2 * e], next[2 * e + 1]), f0, off2), y[e + 1] = fma2(pack2(next[2 * e + 2], next[2 * e + 3]), f1, off2);
             }
-            tc_ld(s_col + kTcKeys * ((i + 1) & (kTurns - 1)), next);
+            tc_ld32(s_col + kTcKeys * ((i + 1) & (kTurns - 1)), next);
             uint32_t mask = 0xffffffffu;
             if (__builtin_expect(cut, 0)) {
               mask = keys_of_row(a, sees, p, key0 + kTcKeys * c);
@@ -687,7 +691,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
                 if (__builtin_expect(__any_sync(0xffffffffu, have && moves), 0)) {
                   tc_wait_ld();
                   st = move_references<FMT>(a, st, top, sc, ks, s_col, o_col, cut, sees, p, key0);
-                  tc_ld(s_col, next);
+                  tc_ld32(s_col, next);
                 }
                 off = st.m == -INFINITY ? 0.f : kAtLift - st.m;
                 if constexpr (FMT == 0) unit = st.m == -INFINITY ? 0.f : pow2i(whole_of(st.m) - st.gref);

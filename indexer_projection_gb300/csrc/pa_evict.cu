@@ -9,6 +9,13 @@
 // warps' counts.  The last key to stay is found by radix selection (8 bits a
 // pass from the highest bit in which the keys differ, until a digit stays
 // whole).
+//
+// Measured: 64 requests of up to 256 blocks 3.0 us (a launch, then 0.5 for the
+// length and the row, 1 for the radix passes); 3 of up to 8192 blocks 9.5 us, of
+// which the row's loads are 1, the radix passes 3 to 4, the order 1 and the
+// stores 2.  Eight counters a digit, by the lane, took 10.4 (more to clear and
+// add up than the additions to one counter cost).  The bytes, 16 a block, are
+// 0.04 us of HBM: latency on one SM a request bounds it.
 #include <cstdint>
 
 #include "../../include/pre_attn.h"
