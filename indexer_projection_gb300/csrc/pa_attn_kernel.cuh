@@ -923,7 +923,7 @@ cudaError_t launch_attn_join(const CacheAttnParams &a, int sms, bool pdl, cudaSt
 // Whether pa_attn_tc_kernel takes a call: its time hardly depends on the rows
 // of an item, that of pa_attn_kernel is in steps of 1, 2, 4 and 8 of them.
 // 64 requests x 2 KV heads in a window of 2047 keys, this / that kernel, us:
-// FP8 1 row 59 / 20, 4 rows 62 / 43, 5 rows 64 / 73, 7 rows 66 / 74; NVFP4 1 row
+// FP8 1 row 57 / 20, 4 rows 60 / 43, 5 rows 62 / 73, 7 rows 63 / 74; NVFP4 1 row
 // 43 / 19, 2 rows 43 / 29, 3 rows 44 / 53, 7 rows 47 / 93.
 inline bool use_attn_tc(const CacheAttnParams &a, int fmt) {
   return a.rows_per >= (fmt == 0 ? 5 : 3) && (a.topk == 0 || a.bt_width <= kTcMaxWidth);
@@ -932,8 +932,8 @@ inline bool use_attn_tc(const CacheAttnParams &a, int fmt) {
 // A CTA an item, instead of even slices, where the items are about as long as
 // one another (a window, lists) and the longest CTA then has no more to do
 // than with slices, whose second segments and second kernel take as long as
-// about five blocks.  This / slices, us: FP8, 128 items of 18 blocks 65 / 75;
-// NVFP4, 128 items of some 20 listed blocks, with weights, 61 / 71.
+// about five blocks.  This / slices, us: FP8, 128 items of 18 blocks 62 / 72;
+// NVFP4, 128 items of rows of 16 listed blocks, with weights, 61 / 67.
 inline bool whole_items(const CacheAttnParams &a, int sms) {
   if (a.topk == 0 && a.window == 0) return false;
   const int64_t blocks = a.topk ? a.topk : ((int64_t)a.sinks + 127) / 128 + ((int64_t)a.window + a.rows_per + 125) / 128 + 1;

@@ -13,14 +13,17 @@
 // core's work for the other.  P replaces S in tensor memory, as the A operand
 // of the second product.
 //
-// What bounds it (FP8, 128 items of 7 rows x 16 heads and 18 blocks, 65 us, 1.2
-// TB/s): instructions.  A block takes 11400 warp instructions, 6850 of them the
-// softmax's (1700 a warp, of 32 (row, head)s x 128 keys), at about 0.57 a clock
-// and scheduler: 2.5 us.  In front are 5 us to the first keys and 8 to the first
-// products (code that is not in the caches yet), behind 6 to the last store.
-// NVFP4 1.5 us a block.  Right and no faster: one pass over the scores with the
-// references looked at turn by turn (65; fewer instructions, more of them in
-// branches); 16 softmax warps of 16 (row, head)s, a quarter of the keys a lane
+// What bounds it (FP8, 128 items of 7 rows x 16 heads and 18 blocks, 62 us, 1.2
+// TB/s): instructions and their fetch.  A block takes 11400 warp instructions,
+// 6850 of them the softmax's (1700 a warp, of 32 (row, head)s x 128 keys), at
+// about 0.57 a clock and scheduler: 2.4 us (NVFP4 1.5).  In front are 5 us to the
+// first keys and some 6 to the first products, behind 6 to the last store.
+// Longer code is slower even where it has fewer instructions to run (the roles'
+// loops share the schedulers' instruction caches): turns of 64 keys 64.5,
+// the NVFP4 conversions unrolled 120 for 114 (every block of 64 x 7 rows); turns
+// of 16 keys pay their latencies more often (68).  Right and no faster, too: one
+// pass over the scores with the references looked at turn by turn (65 when this
+// took 65); 16 softmax warps of 16 (row, head)s, a quarter of the keys a lane
 // (74: 30% more instructions); 16 converting warps (77: no registers left for
 // them); all eight converters on keys, then on values (70).
 //
@@ -51,6 +54,10 @@ constexpr int kTcKeys = 32;         // keys a softmax thread takes at a time (tc
 constexpr float kTcMost = 15.f;
 template <int FMT>
 constexpr float kTcSlack = FMT == 0 ? 40.f : kTcMost - kAtLift;
+// FP8: while a block's V scales are within 2^kTcSpread of each other, the
+// largest weight x V scale is taken from the largest score and the smallest
+// scale; it is then no more than that, and less than 2^kTcMost with the lift.
+constexpr float kTcSpread = kTcMost - kAtLift - 2.f;
 
 template <int FMT>
 struct TcShared : AttnRing<kAtMaxRows, kTcMaxWidth> {
@@ -66,9 +73,9 @@ struct TcShared : AttnRing<kAtMaxRows, kTcMaxWidth> {
   uint32_t nan_rows[4][kHeadDim];  // rows that see a NaN value in a dim, of keys not all see
   float row_scale[2][128];
   float4 sums[2][128];             // a group's m, l, factor of o, and whether it had a block
-  // FP8, of entry n at n % 4: K and V scales, log2 |V scale| (-inf where the codes are all zero), the largest of those
+  // FP8, of entry n at n % 4: K and V scales, log2 |V scale| (-inf where the codes are all zero), the largest and smallest of those
   __align__(16) float scales[FMT == 0 ? 4 : 1][3][128];
-  __align__(16) float most_of[FMT == 0 ? 4 : 1][4];
+  __align__(16) float most_of[FMT == 0 ? 4 : 1][4], least_of[FMT == 0 ? 4 : 1][4];
 };
 
 template <int FMT>
@@ -163,7 +170,7 @@ __device__ __forceinline__ void convert_k(const uint8_t *st, uint8_t *tile, int 
     const int in = tok & (pt - 1);
     const uint8_t *base = st + (tok - in) * 144;
     const uint2 sf = *reinterpret_cast<const uint2 *>(base + pt * 64 + in * 8);
-#pragma unroll
+#pragma unroll 1  // (short code, see above)
     for (int k = 0; k < 4; ++k) {
       const int t = (k + tok) & 3;  // (neighbours' reads 64 bytes apart then meet in a bank two at a time)
       e2m1x32_tile(*reinterpret_cast<const uint4 *>(base + in * 64 + 16 * t), (t < 2 ? sf.x : sf.y) >> (16 * (t & 1)) & 0xffffu,
@@ -237,7 +244,7 @@ __device__ __forceinline__ void convert_v(const CacheAttnParams &a, const uint8_
     const uint4 s0 = *reinterpret_cast<const uint4 *>(base + pt * 64 + (in >> 2) * 32), s1 = *reinterpret_cast<const uint4 *>(base + pt * 64 + (in >> 2) * 32 + 16);
     const uint32_t by = (in & 3) | ((in & 3) + 4) << 4;
     const uint32_t sf4[4] = {__byte_perm(s0.x, s0.y, by), __byte_perm(s0.z, s0.w, by), __byte_perm(s1.x, s1.y, by), __byte_perm(s1.z, s1.w, by)};
-#pragma unroll
+#pragma unroll 1
     for (int k = 0; k < 4; ++k) {
       const int t = (k + tok) & 3;
       uint4 w = *reinterpret_cast<const uint4 *>(base + in * 64 + 16 * t);
@@ -279,10 +286,10 @@ __device__ __forceinline__ uint32_t keys_of_row(const CacheAttnParams &a, bool s
 // The references up to the largest score `top` (FP8: a whole number) and the
 // largest weight x V scale of the block, of every (row, head) of the warp when
 // one's have been outgrown, so that this comes two or three times a segment; o
-// and l follow.
+// and l follow.  lv: FP8, the block's largest and smallest log2 |V scale|.
 template <int FMT>
-__device__ __noinline__ TcRow move_references(const CacheAttnParams &a, TcRow r, float top, float sc, const float *scales, uint32_t s_col,
-                                             uint32_t o_col, bool cut, bool sees, int p, int key0) {
+__device__ __noinline__ TcRow move_references(const CacheAttnParams &a, TcRow r, float top, float2 lv, float sc, const float *scales,
+                                             uint32_t s_col, uint32_t o_col, bool cut, bool sees, int p, int key0) {
   const float was = r.m;
   if (r.m == -INFINITY || (FMT == 0 ? top > r.m + kTcSlack<FMT> : top > r.m)) r.m = FMT == 0 ? ceilf(top) : top;
   float al = 1.f;  // what o is multiplied by
@@ -293,8 +300,11 @@ __device__ __noinline__ TcRow move_references(const CacheAttnParams &a, TcRow r,
   }
   if constexpr (FMT == 0) {
     float most[2] = {-INFINITY, -INFINITY};
+    // (the keys one by one: 3400 clocks, of some 60000 that a group's nine blocks take)
+    const bool near = lv.x - lv.y <= kTcSpread;
+    if (near) most[0] = top + lv.y;
 #pragma unroll 1
-    for (int c = 0; c < 8; ++c) {  // (of keys that the row sees: the rest are not looked at)
+    for (int c = near ? 8 : 0; c < 8; ++c) {  // (of keys that the row sees: the rest are not looked at)
       float y[16];
       tc_ld16(s_col + 16 * c, y);
       const uint32_t mask = cut ? keys_of_row(a, sees, p, key0 + 16 * c) : 0xffffu;
@@ -553,10 +563,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
               sh.scales[j & 3][1][ct] = vz;
               const float lv = zero && fabsf(vz) < INFINITY ? -INFINITY : lg2_approx(fabsf(vz));
               sh.scales[j & 3][2][ct] = lv;
-              float most = lv;
+              float most = lv, least = lv;
 #pragma unroll
-              for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-              if (lane == 0) sh.most_of[j & 3][warp & 3] = most;
+              for (int o = 16; o > 0; o >>= 1) {
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+              }
+              if (lane == 0) sh.most_of[j & 3][warp & 3] = most, sh.least_of[j & 3][warp & 3] = least;
             }
             fence_proxy_async_smem();
           }
@@ -639,9 +652,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
           const bool cut = __any_sync(0xffffffffu, have && (!sees || key0 + 127 > p || (a.window && key0 <= low && key0 + 127 >= a.sinks)));
           const float *ks = sh.scales[FMT == 0 ? entry & 3 : 0][0];
           // Twice over the block's scores, kTcKeys a turn: their largest (the
-          // references move once it has outgrown them), then the weights.  One
-          // short loop: the warps' instructions come at about one in five
-          // clocks when the code of their parts does not fit beside each other
+          // references move once it has outgrown them), then the weights, in one
+          // short loop
           float tops[2] = {-INFINITY, -INFINITY}, off = 0.f, unit = 1.f;
           f32x2 s2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
           const f32x2 sc2 = pack2(sc, sc);
@@ -653,6 +665,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
             const int c = i & (kTurns - 1);
             f32x2 y[kTcKeys / 2];
             const f32x2 off2 = pack2(off, off);
+            uint32_t mask = 0xffffffffu;
+            bool masked = cut;
+            if constexpr (FMT == 0)  // (NVFP4: the look for turns without a mask cost more than it saved, 62.9 us for 61.5)
+              if (__builtin_expect(cut, 0)) {
+                mask = keys_of_row(a, sees, p, key0 + kTcKeys * c);
+                masked = __any_sync(0xffffffffu, have && mask != 0xffffffffu);
+              }
             tc_wait_ld();
 #pragma unroll
             for (int e = 0; e < kTcKeys / 2; e += 2) {
@@ -664,9 +683,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
               y[e] = fma2(pack2(next[2 * e], next[2 * e + 1]), f0, off2), y[e + 1] = fma2(pack2(next[2 * e + 2], next[2 * e + 3]), f1, off2);
             }
             tc_ld32(s_col + kTcKeys * ((i + 1) & (kTurns - 1)), next);
-            uint32_t mask = 0xffffffffu;
-            if (__builtin_expect(cut, 0)) {
-              mask = keys_of_row(a, sees, p, key0 + kTcKeys * c);
+            if (__builtin_expect(masked, 0)) {
+              if constexpr (FMT == 1) mask = keys_of_row(a, sees, p, key0 + kTcKeys * c);
 #pragma unroll
               for (int e = 0; e < kTcKeys / 2; ++e) {
                 const float2 z = unpack2(y[e]);
@@ -681,16 +699,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
               }
               if (i == kTurns - 1) {
                 const float top = fmaxf(tops[0], tops[1]);
-                float lv = 0.f;  // the largest log2 |V scale|
+                float2 lv = make_float2(0.f, 0.f);  // the largest and the smallest log2 |V scale|
                 if constexpr (FMT == 0) {
-                  const float4 z = *reinterpret_cast<const float4 *>(sh.most_of[entry & 3]);
-                  lv = max3(fmaxf(z.x, z.y), z.z, z.w);
+                  const float4 z = *reinterpret_cast<const float4 *>(sh.most_of[entry & 3]), y4 = *reinterpret_cast<const float4 *>(sh.least_of[entry & 3]);
+                  lv = make_float2(max3(fmaxf(z.x, z.y), z.z, z.w), fminf(fminf(y4.x, y4.y), fminf(y4.z, y4.w)));
                 }
                 const bool moves = top > st.m + kTcSlack<FMT> || st.m == -INFINITY ||
-                                   (FMT == 0 && (!st.begun || top + lv > (float)st.gref + (kTcMost - kAtLift)));
+                                   (FMT == 0 && (!st.begun || top + lv.x > (float)st.gref + (kTcMost - kAtLift)));
                 if (__builtin_expect(__any_sync(0xffffffffu, have && moves), 0)) {
                   tc_wait_ld();
-                  st = move_references<FMT>(a, st, top, sc, ks, s_col, o_col, cut, sees, p, key0);
+                  st = move_references<FMT>(a, st, top, lv, sc, ks, s_col, o_col, cut, sees, p, key0);
                   tc_ld32(s_col, next);
                 }
                 off = st.m == -INFINITY ? 0.f : kAtLift - st.m;
@@ -712,7 +730,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
               const float2 r0 = unpack2(w0), r1 = unpack2(w1);
               pk[e] = __uint_as_float(f16x2_bits(r0.x, r0.y)), pk[e + 1] = __uint_as_float(f16x2_bits(r1.x, r1.y));
             }
-            if (FMT == 0 && __builtin_expect(cut, 0)) {  // whatever the scale of a key that is not seen
+            if (FMT == 0 && __builtin_expect(masked, 0)) {  // whatever the scale of a key that is not seen
 #pragma unroll
               for (int e = 0; e < kTcKeys / 2; ++e)
                 pk[e] = __uint_as_float(__float_as_uint(pk[e]) & (((mask >> (2 * e)) & 1u ? 0xffffu : 0u) | ((mask >> (2 * e)) & 2u ? 0xffff0000u : 0u)));
