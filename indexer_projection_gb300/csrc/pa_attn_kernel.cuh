@@ -923,8 +923,8 @@ cudaError_t launch_attn_join(const CacheAttnParams &a, int sms, bool pdl, cudaSt
 // Whether pa_attn_tc_kernel takes a call: its time hardly depends on the rows
 // of an item, that of pa_attn_kernel is in steps of 1, 2, 4 and 8 of them.
 // 64 requests x 2 KV heads in a window of 2047 keys, this / that kernel, us:
-// FP8 1 row 57 / 20, 4 rows 60 / 43, 5 rows 62 / 73, 7 rows 63 / 74; NVFP4 1 row
-// 43 / 19, 2 rows 43 / 29, 3 rows 44 / 53, 7 rows 47 / 93.
+// FP8 1 row 56 / 20, 4 rows 59 / 43, 5 rows 62 / 73, 7 rows 63 / 74; NVFP4 1 row
+// 42 / 19, 2 rows 43 / 29, 3 rows 43 / 53, 7 rows 47 / 93.
 inline bool use_attn_tc(const CacheAttnParams &a, int fmt) {
   return a.rows_per >= (fmt == 0 ? 5 : 3) && (a.topk == 0 || a.bt_width <= kTcMaxWidth);
 }
