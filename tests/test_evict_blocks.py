@@ -125,6 +125,23 @@ def test_every_number_kept():
 
 
 @pytest.mark.gpu
+def test_as_many_requests_as_there_can_be():
+    w, table = inputs(65535, 6, 11, "ties")
+    R = 65535
+    rd = reader(6, 1, 1, R)
+    seq = (np.arange(R) * 37 % (6 * 128 + 1)).astype(np.int32)
+    t = [torch.from_numpy(x).cuda() for x in (w, table, seq)]
+    evicted, counts = torch.zeros_like(t[1]), torch.zeros_like(t[2])
+    rd.evict_blocks(*t, evicted, counts, keep=3)
+    torch.cuda.synchronize()
+    got = [x.cpu().numpy() for x in (*t, evicted, counts)]
+    for r in [0, 1, 2, R // 2, *range(R - 300, R)]:
+        want = expected(w[r].tolist(), table[r].tolist(), int(seq[r]), 3, 1, 1)
+        assert [got[0][r].tolist(), got[1][r].tolist(), int(got[2][r]), got[3][r].tolist(), int(got[4][r])] == list(want[:5])
+    assert (got[4] == np.maximum((seq + 127) // 128 - 3, 0)).all()
+
+
+@pytest.mark.gpu
 def test_captured_on_a_stream_and_again_until_nothing_is_left():
     w, table = inputs(2, 50, 4)
     seq = np.array([50 * 128 - 3, 30 * 128], np.int32)

@@ -115,6 +115,29 @@ def test_one_request_and_many():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("R,V", [(3, 12345), (20, 12345), (60, 12345), (100, 20000), (152, 2100), (153, 20000), (200, 30000)])
+def test_every_split_of_a_vocabulary(R, V):
+    check(*case(R, 2, V, R + V), V)  # (CTAs a request: 8 and fewer)
+
+
+@pytest.mark.gpu
+def test_as_many_requests_as_there_can_be():
+    from indexer_projection_gb300.runner import DraftVerifier
+
+    R, few, n, V = 65535, 257, 3, 40
+    target, q, x, u = (torch.as_tensor(y) for y in case(few, n, V, 71))
+    of = torch.arange(R) % few
+    dev = [y[of].contiguous().cuda() for y in (target, x, u, q)]
+    ver = DraftVerifier(V, n)
+    tokens, accepted = torch.full((R, n), -7, dtype=torch.int32, device="cuda"), torch.full((R,), -7, dtype=torch.int32, device="cuda")
+    ver.verify(dev[0].view(-1, V), dev[1], dev[2], tokens, accepted, draft_probs=dev[3].view(-1, V))
+    assert ver.device_status() == 0
+    want = [expected(target[r].double().numpy(), q[r].double().numpy(), x[r].tolist(), u[r].numpy(), V) for r in range(few)]
+    assert torch.equal(tokens.cpu(), torch.tensor([y[0] for y in want], dtype=torch.int32)[of])
+    assert torch.equal(accepted.cpu(), torch.tensor([y[1] for y in want], dtype=torch.int32)[of])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("certain", [False, True])
 def test_uniforms_at_their_ends(certain):
     target, q, x, u = case(12, 3, 300, 5)

@@ -456,6 +456,29 @@ def test_offsets_beyond_32_bits():
     assert (w[0] == 7).all() and (w[[1, R - 1]][:, c.W:] == 0).all()
 
 
+@pytest.mark.parametrize("fmt,q_len", [("fp8", 1), ("fp8", 7), ("nvfp4", 1), ("nvfp4", 7)])
+def test_as_many_requests_as_there_can_be(fmt, q_len):
+    # 65535 requests that share a block, 129 lengths in turn
+    R, lengths = 65535, 129
+    c = case(fmt, [128], q_len, 1, 2, 50, 3, seed=61)
+    block = int(c.bt[0, 0])
+    c.R, c.M, c.seq, c.bt = lengths, lengths * q_len, np.arange(lengths, dtype=np.int32), np.full((lengths, 1), block, np.int32)
+    c.q = ref.bf16(np.random.default_rng(62).standard_normal((c.M, 2 * 128)))
+    c.upload()
+    of = torch.arange(R) % lengths
+    rows = (of[:, None] * q_len + torch.arange(q_len)).flatten()
+    rd = c.reader(weigh=True, max_requests=R)
+    q, seq, table = c.q[rows].cuda(), of.int().cuda(), torch.full((R, 1), block, dtype=torch.int32, device="cuda")
+    out, w = torch.full_like(q, float("nan")), torch.full((R, 1), 7.0, device="cuda")
+    rd.attend(q, table, seq, out, window=50, sinks=3, weights=w)
+    assert rd.device_status() == (1 if q_len > 1 else 0)  # (lengths below q_len)
+    want, tol = c.attention()
+    over = (out.double().cpu() - torch.from_numpy(want)[rows]).abs() - torch.from_numpy(tol)[rows]
+    assert (over <= 0).all()  # (a NaN is not)
+    have = of >= max(q_len, 1)
+    assert (w.cpu()[~have] == 7).all() and torch.allclose(w.cpu()[have], torch.tensor(2.0 * q_len), rtol=2.0 ** -12)
+
+
 def test_what_the_reader_refuses():
     from indexer_projection_gb300 import binding as B
 
