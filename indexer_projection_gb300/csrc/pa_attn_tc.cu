@@ -14,9 +14,9 @@
 // of the second product.
 //
 // What bounds it (FP8, 128 items of 7 rows x 16 heads and 18 blocks, 62 us, 1.2
-// TB/s): instructions and their fetch.  A block takes 11400 warp instructions,
-// 6850 of them the softmax's (1700 a warp, of 32 (row, head)s x 128 keys), at
-// about 0.57 a clock and scheduler: 2.4 us (NVFP4 1.5).  In front are 5 us to the
+// TB/s): instructions and their fetch.  A block takes 10900 warp instructions,
+// some 6400 of them the softmax's (1600 a warp, of 32 (row, head)s x 128 keys),
+// at about 0.57 a clock and scheduler: 2.4 us (NVFP4 1.5).  In front are 5 us to the
 // first keys and some 6 to the first products, behind 6 to the last store.
 // Longer code is slower even where it has fewer instructions to run (the roles'
 // loops share the schedulers' instruction caches): turns of 64 keys 64.5,
