@@ -11,8 +11,10 @@ missing: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpre_attn.so")
@@ -130,6 +132,15 @@ class pa_verify_args(ctypes.Structure):
                 ("draft_probs", _vp), ("draft_stride", ctypes.c_int64), ("draft_type", ctypes.c_int), ("drafts", _vp),
                 ("uniforms", _vp), ("R", ctypes.c_int), ("q_len", ctypes.c_int), ("vocab", ctypes.c_int),
                 ("tokens", _vp), ("accepted", _vp), ("status", _vp)]
+
+
+def packed(cls):
+    """An argument struct that is filled at once, for calls whose fields nearly all change (a ctypes field after the
+    other takes three times as long): a function of its fields' values in their order, and the struct."""
+    codes = {_vp: "P", ctypes.c_int64: "q", ctypes.c_int: "i"}
+    layout = struct.Struct("@" + "".join(codes[t] for _, t in cls._fields_))
+    held = bytearray(ctypes.sizeof(cls))
+    return functools.partial(layout.pack_into, held, 0), cls.from_buffer(held)
 
 
 class PreAttnError(RuntimeError):

@@ -227,9 +227,8 @@ class CacheReader(_Calls):
         self._ext = B.pa_attention_ext(0, 0, None, 0, None, 0, 1.0, self.status + 256 + self.ws_bytes, weights_bytes)
         ext, ext_entry = B.ctypes.byref(self._ext), lib.pre_attn_attention_ext
         self._ext_entry = (lambda args, stream: ext_entry(args, ext, stream)), self._attn_entry[1], "pre_attn_attention_ext"
-        self._evict = B.pa_evict_args(None, 0, None, None, 0, bt_width, 0, init_blocks, local_blocks, None, 0, None, None,
-                                      None, None, self.status)
-        self._evict_entry = lib.pre_attn_evict_blocks, B.ctypes.byref(self._evict), "pre_attn_evict_blocks"
+        self._fill_evict, evict = B.packed(B.pa_evict_args)
+        self._evict_entry = lib.pre_attn_evict_blocks, B.ctypes.byref(evict), "pre_attn_evict_blocks"
 
     @property
     def caches(self) -> B.pa_caches:
@@ -346,23 +345,25 @@ class CacheReader(_Calls):
         and of the others those with the largest weights [R, >= bt_width] (f32).  The block table, the lengths and the
         weights without the evicted blocks go to the outputs (None: in place), the evicted table entries to evicted
         [R, bt_width], -1 behind the last, and how many there are to counts [R]."""
-        R, a, W = self._requests(seq_lens, block_table), self._evict, self.bt_width
-        a.weights_stride = self._rows(weights, weights.dtype is torch.float32, R, W, "weights")
-        a.weights, a.block_table, a.seq_lens = weights.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr()
-        a.weights_out, a.weights_out_stride = a.weights, a.weights_stride
-        a.block_table_out, a.seq_lens_out = a.block_table, a.seq_lens
-        if weights_out is not None:
-            a.weights_out_stride = self._rows(weights_out, weights_out.dtype is torch.float32, R, W, "weights_out")
-            a.weights_out = weights_out.data_ptr()
-        if block_table_out is not None:
+        R, W = self._requests(seq_lens, block_table), self.bt_width
+        stride_out = stride = self._rows(weights, weights.dtype is torch.float32, R, W, "weights")
+        if weights_out is None:
+            weights_out = weights
+        else:
+            stride_out = self._rows(weights_out, weights_out.dtype is torch.float32, R, W, "weights_out")
+        if block_table_out is None:
+            block_table_out = block_table
+        else:
             self._ints(block_table_out, (R, W), "block_table_out")
-            a.block_table_out = block_table_out.data_ptr()
-        if seq_lens_out is not None:
+        if seq_lens_out is None:
+            seq_lens_out = seq_lens
+        else:
             self._ints(seq_lens_out, (R,), "seq_lens_out")
-            a.seq_lens_out = seq_lens_out.data_ptr()
         self._ints(evicted, (R, W), "evicted")
         self._ints(counts, (R,), "counts")
-        a.evicted, a.counts, a.R, a.keep = evicted.data_ptr(), counts.data_ptr(), R, _int32(keep)
+        self._fill_evict(weights.data_ptr(), stride, block_table.data_ptr(), seq_lens.data_ptr(), R, W, _int32(keep),
+                         self.init_blocks, self.local_blocks, weights_out.data_ptr(), stride_out, block_table_out.data_ptr(),
+                         seq_lens_out.data_ptr(), evicted.data_ptr(), counts.data_ptr(), self.status)
         if R == 0:
             return B.PA_OK
         return self._call(self._evict_entry, stream, check)
@@ -388,15 +389,15 @@ class DraftVerifier(_Calls):
             raise ValueError(f"vocab {vocab} or q_len {q_len} out of range")
         self.vocab, self.q_len = vocab, q_len
         self._take_workspace(0)
-        self._args = B.pa_verify_args(None, 0, 0, None, 0, 0, None, None, 0, q_len, vocab, None, None, self.status)
-        self._entry = B.load().pre_attn_verify_drafts, B.ctypes.byref(self._args), "pre_attn_verify_drafts"
+        self._fill, args = B.packed(B.pa_verify_args)
+        self._entry = B.load().pre_attn_verify_drafts, B.ctypes.byref(args), "pre_attn_verify_drafts"
 
     def verify(self, target, drafts, uniforms, tokens, accepted, *, draft_probs=None, stream=None,
                check: bool = True) -> int:
         """target [R * q_len, >= vocab] and draft_probs [R * (q_len - 1), >= vocab] (f32 or bf16; None: the drafter is
         certain), drafts [R, q_len - 1] int32 (negative: no more drafts), uniforms [R, q_len] f32 in [0, 1) into tokens
         [R, q_len] int32 (accepted drafts, one token more, -1) and accepted [R] int32 (how many drafts)."""
-        a, k = self._args, self.q_len - 1
+        k = self.q_len - 1
         R = accepted.shape[0] if accepted.dim() == 1 else -1
         self._ints(accepted, (R,), "accepted")
         self._ints(tokens, (R, self.q_len), "tokens")
@@ -404,14 +405,14 @@ class DraftVerifier(_Calls):
         if (uniforms.dtype is not torch.float32 or uniforms.shape != (R, self.q_len) or not uniforms.is_contiguous()
                 or uniforms.get_device() != self.index):
             raise ValueError(f"uniforms: a contiguous f32 tensor of shape {(R, self.q_len)} on {self.device} is wanted")
-        a.target_stride = self._rows(target, target.dtype in self._types, R * self.q_len, self.vocab, "target")
-        a.target_type, a.target = self._types[target.dtype], target.data_ptr()
-        a.draft_probs = None
+        types = self._types
+        stride = self._rows(target, target.dtype in types, R * self.q_len, self.vocab, "target")
+        q, q_stride, q_type = 0, 0, 0
         if draft_probs is not None and k:
-            a.draft_stride = self._rows(draft_probs, draft_probs.dtype in self._types, R * k, self.vocab, "draft_probs")
-            a.draft_type, a.draft_probs = self._types[draft_probs.dtype], draft_probs.data_ptr()
-        a.drafts, a.uniforms, a.R = drafts.data_ptr() or None, uniforms.data_ptr(), R
-        a.tokens, a.accepted = tokens.data_ptr(), accepted.data_ptr()
+            q_stride = self._rows(draft_probs, draft_probs.dtype in types, R * k, self.vocab, "draft_probs")
+            q, q_type = draft_probs.data_ptr(), types[draft_probs.dtype]
+        self._fill(target.data_ptr(), stride, types[target.dtype], q, q_stride, q_type, drafts.data_ptr(), uniforms.data_ptr(), R,
+                   self.q_len, self.vocab, tokens.data_ptr(), accepted.data_ptr(), self.status)
         if R == 0:
             return B.PA_OK
         return self._call(self._entry, stream, check)

@@ -52,3 +52,16 @@ def test_bytes(B):
     for bad in ((-1, 1, 16, 1, 1), (65536, 1, 16, 1, 1), (1, 0, 16, 1, 1), (1, 17, 16, 1, 1), (1, 1, 17, 1, 1), (1, 1, 0, 1, 1),
                 (1, 1, 16, 3, 1), (1, 1, 15, 2, 1), (1, 1, 16, 1, 0), (1, 1, 16, 1, 16385)):
         assert n(*bad) == 0
+
+
+def test_a_packed_struct_holds_what_its_fields_do():
+    from indexer_projection_gb300 import binding as B
+
+    for cls in (B.pa_evict_args, B.pa_verify_args):
+        fill, args = B.packed(cls)
+        values = [2 ** 40 + k if t is B.ctypes.c_void_p else -k if t is B.ctypes.c_int64 else k - 5
+                  for k, (_, t) in enumerate(cls._fields_)]
+        for _ in range(2):
+            fill(*values)
+            assert [getattr(args, name) for name, _ in cls._fields_] == values
+            values[0] += 1
