@@ -409,6 +409,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
       int v0, v1, v;
       for (int it = sl.first; ok && sl.segment(a, sh, it, v0, v1, v); ++it, ++seg) {
         bool begun[2] = {false, false}, pending = false, any = false;
+        // every softmax warp has taken the last entries of the segment before: a
+        // phase of s_full does not pass one by (within a segment S of the group's
+        // next entry waits for P of its last)
+        if (seg > 0 && !(ok = mbar_wait(&sh.meet, (seg - 1) & 1, a.status, a.lim))) break;
         for (int ends = 0; ok && ends < 2; ++n) {
           const int g = n & 1;
           if (!(ok = mbar_wait(&sh.k_full, n & 1, a.status, a.lim))) break;
