@@ -64,7 +64,7 @@ struct TcShared : AttnRing<kAtMaxRows, kTcMaxWidth> {
   uint64_t k_full, k_empty;        // the tile of keys; entries without a block go through too
   uint64_t v_full, v_empty;        // that of values
   uint64_t s_full[2], p_full[2], pv_done[2];  // by the softmax group
-  uint64_t item_full;              // an item's queries and what goes with them
+  uint64_t item_full, item_seen;   // an item's queries and what goes with them; every softmax warp has waited for them
   uint64_t meet, seg_done;         // the groups' sums are there; a segment's O has been read
   uint64_t never, drain;
   uint32_t tmem;
@@ -374,6 +374,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
     mbar_init(&sh.v_full, 4);
     mbar_init(&sh.v_empty, 1);
     mbar_init(&sh.item_full, 4);
+    mbar_init(&sh.item_seen, 8);
     mbar_init(&sh.meet, 8);
     mbar_init(&sh.seg_done, 8);
     mbar_init(&sh.never, 1);
@@ -583,8 +584,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
             mbar_arrive(&sh.empty[s]);
           }
           if (!more && ends++ == 0 && next) {
-            // (the last S of this segment is done: its queries may be replaced)
-            if (seg > 0 && !all_got(mbar_wait(&sh.seg_done, (seg - 1) & 1, a.status, a.lim))) break;
+            // (the last S of this segment is done: its queries may be replaced; the
+            // softmax warps are behind the segment before and its item_full)
+            if (!all_got(mbar_wait(&sh.item_seen, seg & 1, a.status, a.lim))) break;
             lay_out(seg + 1);
           }
         }
@@ -633,6 +635,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
     int v0, v1, v;
     for (int it = sl.first; ok && sl.segment(a, sh, it, v0, v1, v); ++it, ++seg) {
       if (!wait(&sh.item_full, seg & 1)) break;
+      if (lane == 0) mbar_arrive(&sh.item_seen);
       const AttnItem x = attn_place(a, it);
       const int first = sh.first[seg & 1];
       const bool have = at < x.rows * a.group;

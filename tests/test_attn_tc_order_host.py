@@ -16,7 +16,7 @@ def kernel(segments, stages, without=()):
     o = Order()
 
     def wait(agent, bar, phase, name=None):
-        if name not in without:
+        if (name or bar) not in without:
             o.wait(agent, bar, phase)
     entries = [(seg, i < n, i == n) for seg, n in enumerate(segments) for i in range(n + 2)]  # segment, a block, the first end
     for j, (seg, block, _) in enumerate(entries):  # the copies
@@ -44,7 +44,7 @@ def kernel(segments, stages, without=()):
             o.arrive(k, "k_full", j, 4)
             o.arrive(k, f"empty{j % stages}", j // stages, 8)
             if end and seg + 1 < len(segments):
-                wait(k, "seg_done", seg - 1)
+                wait(k, "item_seen", seg)
                 lay_out(seg + 1)
     for i in range(4):  # values
         v, nv = f"values{i}", 0
@@ -105,6 +105,7 @@ def kernel(segments, stages, without=()):
         s, n, blocks = f"softmax{g}{i}", 0, 0
         for seg in range(len(segments)):
             wait(s, "item_full", seg)
+            o.arrive(s, "item_seen", seg, 8)
             for part in range(4):
                 o.touch(s, "r", f"row_scale{seg & 1} {part}", seg)
             mine = [j for j, e in enumerate(entries) if e[0] == seg and j & 1 == g]
@@ -149,5 +150,12 @@ def test_no_scores_are_missed(stages):
         assert not faults(segments, stages, "s_full"), segments
 
 
+@pytest.mark.parametrize("stages", [3, 4, 5])
+def test_no_item_is_missed(stages):
+    for segments in SEGMENTS:
+        assert not faults(segments, stages, "item_"), segments
+
+
 def test_a_missing_wait_is_found():
     assert faults((1, 0, 1), 3, "s_full", ["ends taken"])  # the product's thread runs ahead of a softmax group
+    assert faults((1, 1, 1), 3, "item_full", ["item_seen"])  # .. the queries' warps
