@@ -69,7 +69,7 @@ struct TcShared : AttnRing<kAtMaxRows, kTcMaxWidth> {
   uint64_t never, drain;
   uint32_t tmem;
   int first[2];                    // by the segment's parity: the first row's position
-  int nan_any[4];                  // by the segment, modulo 4:
+  int nan_any[4];                  // by the segment, modulo 4 (written and cleared by the value warps):
   uint32_t nan_rows[4][kHeadDim];  // rows that see a NaN value in a dim, of keys not all see
   float row_scale[2][128];
   float4 sums[2][128];             // a group's m, l, factor of o, and whether it had a block
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
     mbar_init(&sh.k_empty, 1);
     mbar_init(&sh.v_full, 4);
     mbar_init(&sh.v_empty, 1);
-    mbar_init(&sh.item_full, 4);
+    mbar_init(&sh.item_full, 8);
     mbar_init(&sh.item_seen, 8);
     mbar_init(&sh.meet, 8);
     mbar_init(&sh.seg_done, 8);
@@ -595,6 +595,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
       // values
       uint32_t nv = 0;  // blocks
       for (int it = sl.first; ok && sl.segment(a, sh, it, v0, v1, v); ++it, ++seg) {
+        // The next segment's notes are cleared when the softmax is in the segment
+        // before, so past that which had their place, and before it comes to this
+        // one: nothing is noted for the next segment until it has
+        if (seg > 0 && !all_got(mbar_wait(&sh.item_seen, (seg - 1) & 1, a.status, a.lim))) break;
+        sh.nan_rows[(seg + 1) & 3][ct] = 0;
+        if (ct == 0) sh.nan_any[(seg + 1) & 3] = 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.item_full);
         bool bad = false;
         const AttnItem x = attn_item(a, it, &bad);
         const uint32_t every = (1u << x.rows) - 1u;
@@ -837,11 +845,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
         }
         if (have && !whole && g == 0)
           *reinterpret_cast<float2 *>(pp + kAtMaxRows * 16 * kHeadDim + (row * 16 + head) * 2) = make_float2(top, all);
-      }
-      // the notes of the segment before the last are read: room for the one after the next
-      if (g == 0) {
-        sh.nan_rows[(seg + 2) & 3][at] = 0;
-        if (at == 0) sh.nan_any[(seg + 2) & 3] = 0;
       }
       tc_fence_before();
       __syncwarp();
