@@ -660,6 +660,19 @@ size_t pre_attn_attention_weights_bytes(int R, int q_len, int n_q_heads, int n_k
  * with blocks), PA_ERR_SHAPE, PA_ERR_ALIGN, PA_ERR_ALIAS, PA_ERR_WORKSPACE. */
 int pre_attn_attention_ext(const pa_attention_args *args, const pa_attention_ext *ext, void *stream);
 
+/* How pre_attn_attention_path says that a call is dealt to the GPU. */
+enum {
+  PA_ATTN_WHOLE = 0,   /* a CTA a (request, up to 8 of its rows, KV head) */
+  PA_ATTN_SLICED = 1,  /* even slices of all of them, joined by a second kernel */
+  PA_ATTN_CLUSTER = 2, /* a cluster of CTAs each */
+  PA_ATTN_TILES = 4    /* added where the kernel is the one that takes several rows as one tcgen05 tile */
+};
+
+/* Which of them pre_attn_attention(args) (ext NULL) or pre_attn_attention_ext(args,
+ * ext) takes on the current device; launches nothing.  Returns a negative
+ * PA_ERR_* value for a call that is refused, or without requests (-PA_ERR_SHAPE). */
+int pre_attn_attention_path(const pa_attention_args *args, const pa_attention_ext *ext);
+
 /* ------------------------------------------- eviction from the caches
  *
  * What keeps a request's caches within a budget of page-128 blocks: the

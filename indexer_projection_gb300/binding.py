@@ -26,6 +26,7 @@ PA_ERR_NO_Q_OUTPUT, PA_ERR_NO_IQ_OUTPUT, PA_ERR_ALIAS, PA_ERR_WORKSPACE = 5, 6, 
 PA_ERR_CUDA, PA_ERR_UNSUPPORTED = 9, 10
 PA_DEV_SLOT_RANGE, PA_DEV_POS_RANGE, PA_DEV_WAIT_TIMEOUT, PA_DEV_TOKEN_RANGE, PA_DEV_NO_TOKEN = 1, 2, 4, 8, 16
 PA_PROB_F32, PA_PROB_BF16 = 0, 1
+PA_ATTN_WHOLE, PA_ATTN_SLICED, PA_ATTN_CLUSTER, PA_ATTN_TILES = 0, 1, 2, 4
 PA_WEIGHT_FP8_PER_CHANNEL, PA_WEIGHT_MXFP8 = 0, 1
 PA_CACHE_FP8, PA_CACHE_NVFP4 = 0, 1
 PA_FLAG_STATIC_KV_SCALE, PA_FLAG_FORCE_GEMV, PA_FLAG_FORCE_GEMM, PA_FLAG_NO_PDL = 1, 2, 4, 8
@@ -192,6 +193,7 @@ def load(path: str = LIB_PATH):
         "pre_attn_attention": (i, [ctypes.POINTER(pa_attention_args), _vp]),
         "pre_attn_attention_weights_bytes": (sz, [i, i, i, i, i]),
         "pre_attn_attention_ext": (i, [ctypes.POINTER(pa_attention_args), ctypes.POINTER(pa_attention_ext), _vp]),
+        "pre_attn_attention_path": (i, [ctypes.POINTER(pa_attention_args), ctypes.POINTER(pa_attention_ext)]),
         "pre_attn_evict_blocks": (i, [ctypes.POINTER(pa_evict_args), _vp]),
         "pre_attn_verify_drafts": (i, [ctypes.POINTER(pa_verify_args), _vp]),
     }
@@ -389,6 +391,11 @@ def pre_attn_attention_ext(args: pa_attention_args, ext: pa_attention_ext, strea
     if check and st != PA_OK:
         raise PreAttnError(st, "pre_attn_attention_ext " + (pre_attn_last_cuda_error() if st == PA_ERR_CUDA else ""))
     return st
+
+
+def pre_attn_attention_path(args: pa_attention_args, ext: pa_attention_ext | None = None) -> int:
+    """How the call is dealt (PA_ATTN_*), or a negative PA_ERR_* value."""
+    return int(load().pre_attn_attention_path(ctypes.byref(args), ctypes.byref(ext) if ext is not None else None))
 
 
 def pre_attn_evict_blocks(args: pa_evict_args, stream=None, check: bool = True) -> int:

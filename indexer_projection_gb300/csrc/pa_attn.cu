@@ -198,6 +198,11 @@ int attn_params(const pa_attention_args &x, CacheAttnParams &a, int *num_sms) {
   return PA_OK;
 }
 
+cudaError_t plain_attn_path(const CacheAttnParams &a, int fmt, int sms, int *path) {
+  return fmt == 0 ? launch_attn<0, false>(a, sms, true, nullptr, nullptr, path)
+                  : launch_attn<1, false>(a, sms, true, nullptr, nullptr, path);
+}
+
 }  // namespace pa
 
 extern "C" int pre_attn_attention(const pa_attention_args *in, void *stream) {

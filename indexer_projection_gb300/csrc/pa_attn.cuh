@@ -13,6 +13,7 @@
 
 #include <cuda_fp16.h>
 
+#include "../../include/pre_attn.h"
 #include "pa_device.cuh"
 #include "pa_f16.cuh"
 #include "pa_launch.h"
@@ -41,7 +42,7 @@ constexpr int kAtPartFloats = kAtMaxRows * 16 * (kHeadDim + 2);  // o, then (m, 
 // blocks over a persistent grid, with partial results joined by a second
 // kernel; or a cluster of CTAs an item, joined through distributed shared
 // memory (small calls: no scan of the items, no second kernel).
-enum { kAtWhole = 0, kAtSliced = 1, kAtCluster = 2 };
+enum { kAtWhole = PA_ATTN_WHOLE, kAtSliced = PA_ATTN_SLICED, kAtCluster = PA_ATTN_CLUSTER };
 
 struct CacheAttnParams {
   const uint8_t *q;

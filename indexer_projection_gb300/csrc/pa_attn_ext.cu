@@ -282,13 +282,15 @@ extern "C" size_t pre_attn_attention_weights_bytes(int R, int q_len, int n_q_hea
   return std::max<size_t>((size_t)R * q_len * n_kv_heads * bt_width * (parts << pa::lg_heads_of(n_q_heads / n_kv_heads)) * 4, 4);
 }
 
-extern "C" int pre_attn_attention_ext(const pa_attention_args *in, const pa_attention_ext *ext, void *stream) {
+namespace pa {
+
+// The checks of pre_attn_attention_ext and the kernels' parameters; a.R is 0
+// where there is nothing to do, and *plain whether it is pre_attn_attention.
+static int ext_params(const pa_attention_args *in, const pa_attention_ext *ext, CacheAttnParams &a, int *sms, bool *plain) {
   if (!in || !ext) return PA_ERR_NULL;
   if (ext->window < 0 || ext->sinks < 0 || (ext->sinks > 0 && ext->window == 0)) return PA_ERR_CONFIG;
   if (ext->weights && (!(ext->decay >= 0.0f) || !std::isfinite(ext->decay))) return PA_ERR_CONFIG;
-  pa::CacheAttnParams a;
-  int sms = 0;
-  const int st = pa::attn_params(*in, a, &sms);
+  const int st = attn_params(*in, a, sms);
   if (st != PA_OK) return st;
   if (ext->window && in->blocks) return PA_ERR_UNSUPPORTED;
   if (ext->weights) {
@@ -318,9 +320,36 @@ extern "C" int pre_attn_attention_ext(const pa_attention_args *in, const pa_atte
   if (a.R == 0) return PA_OK;
   const int keys = in->bt_width * 128;  // a window of that many is none
   if (ext->window < keys) a.window = ext->window, a.sinks = std::min(ext->sinks, keys);
-  if (a.window == 0 && !ext->weights) return pre_attn_attention(in, stream);
+  *plain = a.window == 0 && !ext->weights;
   a.wpart = ext->weights ? static_cast<float *>(ext->workspace) : nullptr;
-  a.lg_heads = pa::lg_heads_of(a.group);
+  a.lg_heads = lg_heads_of(a.group);
+  return PA_OK;
+}
+
+}  // namespace pa
+
+extern "C" int pre_attn_attention_path(const pa_attention_args *in, const pa_attention_ext *ext) {
+  if (!in) return -PA_ERR_NULL;
+  pa::CacheAttnParams a;
+  int sms = 0, path = 0;
+  bool plain = true;
+  const int st = ext ? pa::ext_params(in, ext, a, &sms, &plain) : pa::attn_params(*in, a, &sms);
+  if (st != PA_OK) return -st;
+  if (a.R == 0) return -PA_ERR_SHAPE;
+  const bool fp8 = in->cache_format == PA_CACHE_FP8;
+  const cudaError_t e = plain ? pa::plain_attn_path(a, fp8 ? 0 : 1, sms, &path)
+                        : fp8 ? pa::launch_attn<0, true>(a, sms, true, nullptr, nullptr, &path)
+                              : pa::launch_attn<1, true>(a, sms, true, nullptr, nullptr, &path);
+  return e == cudaSuccess ? path : -pa::record_cuda_error(e);
+}
+
+extern "C" int pre_attn_attention_ext(const pa_attention_args *in, const pa_attention_ext *ext, void *stream) {
+  pa::CacheAttnParams a;
+  int sms = 0;
+  bool plain = false;
+  const int st = pa::ext_params(in, ext, a, &sms, &plain);
+  if (st != PA_OK || a.R == 0) return st;
+  if (plain) return pre_attn_attention(in, stream);
   const bool pdl = !(in->flags & PA_FLAG_NO_PDL), fp8 = in->cache_format == PA_CACHE_FP8;
   pa::AttnLaunched did;
   pa::AttnLaunched *done = ext->weights ? &did : nullptr;  // (then the weights' kernel joins)

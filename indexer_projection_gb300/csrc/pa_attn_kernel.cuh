@@ -917,6 +917,8 @@ inline bool attn_maps(AttnMaps *maps, const CacheAttnParams &a, int fmt) {
 // The checks of a call's arguments and the kernels' parameters from them
 // (pa_attn.cu); a.R is 0 where there is nothing to do.
 int attn_params(const pa_attention_args &x, CacheAttnParams &a, int *num_sms);
+// The path of a call without a window and weights (pa_attn.cu).
+cudaError_t plain_attn_path(const CacheAttnParams &a, int fmt, int sms, int *path);
 // The second kernel of the sliced mode (pa_attn.cu).
 cudaError_t launch_attn_join(const CacheAttnParams &a, int sms, bool pdl, cudaStream_t stream);
 
@@ -950,8 +952,10 @@ struct AttnLaunched {
   CacheAttnParams a;
 };
 
+// path: only says which kernel and mode it is (pre_attn_attention_path).
 template <int FMT, bool EXT>
-cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cudaStream_t stream, AttnLaunched *done) {
+cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cudaStream_t stream, AttnLaunched *done,
+                        int *path = nullptr) {
   AttnMaps maps;
   if (!attn_maps(&maps, a0, FMT)) return cudaErrorInvalidValue;
   CacheAttnParams a = a0;
@@ -1030,6 +1034,7 @@ cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cudaStream
         a.split = n;
         cfg.gridDim = dim3(a.items * n);
         cfg.numAttrs = 2;
+        if (path) return *path = a.mode, cudaSuccess;
         if (done) *done = AttnLaunched{v.parts, false, a};
         return cudaLaunchKernelEx(&cfg, v.kern, maps, a);
       }
@@ -1040,11 +1045,13 @@ cudaError_t launch_attn(const CacheAttnParams &a0, int sms, bool pdl, cudaStream
     if (a.mode == kAtSliced && whole_items(a, sms)) a.mode = kAtWhole;
     if (use_attn_tc(a, FMT)) {
       const bool join = a.mode == kAtSliced;
+      if (path) return *path = a.mode | PA_ATTN_TILES, cudaSuccess;
       if (done) *done = AttnLaunched{1, join, a};
       e = launch_attn_tc(FMT, maps, a, join ? sms : a.items, pdl, stream);
       return e != cudaSuccess || a.test_timeout || done || !join ? e : launch_attn_join(a, sms, pdl, stream);
     }
   }
+  if (path) return *path = a.mode, cudaSuccess;
   if ((e = use(kSliced[variant], regs[0][variant])) != cudaSuccess) return e;
   if (done) *done = AttnLaunched{kSliced[variant].parts, a.mode == kAtSliced, a};
   cfg.gridDim = dim3(a.mode == kAtSliced ? sms : a.items);
