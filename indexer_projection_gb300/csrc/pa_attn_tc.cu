@@ -562,11 +562,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) pa_attn_tc_kernel(const __grid_
               for (int o = 4; o < 32; o <<= 1)
                 some[0] |= __shfl_xor_sync(0xffffffffu, some[0], o), some[1] |= __shfl_xor_sync(0xffffffffu, some[1], o);
               const uint32_t lo = __shfl_sync(0xffffffffu, some[0], (lane >> 2) & 3), hi = __shfl_sync(0xffffffffu, some[1], (lane >> 2) & 3);
-              const bool zero = (((lane < 16 ? lo : hi) >> (8 * (lane & 3))) & 0x7fu) == 0u;
               const float kz = *reinterpret_cast<const float *>(st + St::kKs + 4 * ct), vz = *reinterpret_cast<const float *>(st + St::kVs + 4 * ct);
+              // a row of zeros counts for nothing, whatever its scale: it does not
+              // set the products' unit, in which its weight x scale could leave f16
+              const bool zero = (((lane < 16 ? lo : hi) >> (8 * (lane & 3))) & 0x7fu) == 0u && fabsf(vz) < INFINITY;
               sh.scales[j & 3][0][ct] = kz;
-              sh.scales[j & 3][1][ct] = vz;
-              const float lv = zero && fabsf(vz) < INFINITY ? -INFINITY : lg2_approx(fabsf(vz));
+              sh.scales[j & 3][1][ct] = zero ? 0.f : vz;
+              const float lv = zero ? -INFINITY : lg2_approx(fabsf(vz));
               sh.scales[j & 3][2][ct] = lv;
               float most = lv, least = lv;
 #pragma unroll

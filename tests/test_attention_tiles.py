@@ -76,3 +76,40 @@ def test_path_of_a_call(fmt, q_len, tiles):
     rd = many.reader(weigh=True)
     win.attend(many, rd, weights=True)
     assert path(rd) == tiles | WHOLE
+
+
+# ---------------------------------------------------- rows of V that are zero
+
+def zero_value(c, r, j, scale=1.0):
+    """Key j of request r: a value row of zeros, whose writer gives it the scale 1 (FP8).  It does not count to the
+    largest weight x V scale."""
+    slot = int(c.bt[r, j // 128]) * 128 + j % 128
+    page, t = slot // 128 * c.kps + slot % 128 // 16, slot % 16
+    for h in range(c.nkv):
+        c.bytes["v"][(page * c.nkv + h) * 2048 + np.arange(128) * 16 + t] = 0x80 if j % 3 == 0 else 0  # (either zero)
+        c.scales["v"][(page * c.nkv + h) * 16 + t] = scale
+        c.v[h, slot], c.vs[h, slot] = 0.0, 0.0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", [SLICED, WHOLE])
+@pytest.mark.parametrize("zeros", ["some", "blocks", "first block", "all"])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 100])
+def test_zero_values_beside_small_scales(mode, zeros, scale):
+    q_len = 5
+    if mode == SLICED:
+        c = case("fp8", [700, 130, 512], q_len, 1, 8, seed=70, extra_width=WIDE)
+    else:
+        c = case("fp8", [700, 130, 512, 300] * 20, q_len, 1, 8, 600, 130, seed=70)
+    for w in "kv":
+        c.scales[w][np.isfinite(c.scales[w])] *= np.float32(2.0 ** -9 if w == "v" else 1)
+    c.v, c.vs = c.v * 2.0 ** -9, c.vs * 2.0 ** -9
+    for r, n in enumerate(c.seq.tolist()):
+        which = {"some": [j for j in range(n) if j % 7 == 2 or j == n - 1], "blocks": [j for j in range(n) if j // 128 % 2 == 1],
+                 "first block": [j for j in range(n) if j < 128], "all": range(n)}[zeros]
+        for j in which:
+            zero_value(c, r, j, scale)
+    c.upload()
+    out, _ = check(c, mode)
+    if zeros == "all":
+        assert (out == 0).all()
