@@ -168,6 +168,35 @@ def test_nan_values_behind_requests_without_keys(fmt, q_len):
     win.close_weights(w, c, c.weights())
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,q_len", [("fp8", 5), ("nvfp4", 7)])
+def test_a_padded_batch_in_a_graph(fmt, q_len):
+    # captured once, replayed with other lengths: every request there, some, one, none
+    c = padded(fmt, q_len, 700, 0, 0, 1, 2, 90 + q_len)
+    full = c.seq.copy()
+    c.upload()
+    rd = c.reader(weigh=True)
+    out, w = torch.zeros(c.M, 2 * 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(c.R, c.W, device="cuda")
+    call = lambda: rd.attend(c.dev["q"], c.dev["bt"], c.dev["seq"], out, weights=w)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    assert path(rd) == TILES | SLICED
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    live = np.nonzero(full)[0]
+    for kept in (live, live[::3], live[:1], live[-1:], live[:0], live):
+        c.seq = np.zeros_like(full)
+        c.seq[kept] = full[kept]
+        c.dev["seq"].copy_(torch.from_numpy(c.seq))
+        out.fill_(3), w.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        win.close(out, c.attention())
+        win.close_weights(w, c, c.weights())
+    assert rd.device_status() == 0
+
+
 # ----------------------------------------------------- windows, rows, layouts
 
 @pytest.mark.gpu
