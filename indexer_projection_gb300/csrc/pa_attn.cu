@@ -51,8 +51,9 @@
 // each: 7.5 us) are a chain of latencies: list and table, first block, its
 // products, the join.
 //
-// Measured and kept out: the rows of an item as one tcgen05 tile (FP8 spec
-// rows 128 us against 77: softmax latency, instruction cache); two rows a warp
+// Measured and kept out: the rows of an item as one tcgen05 tile in a first form
+// (FP8 spec rows 128 us against 77: softmax latency, instruction cache; calls
+// with a window or weights take a later one, pa_attn_tc.cu); two rows a warp
 // sharing converted codes (114 against 77 where rows pick blocks of their own,
 // 70 against 77 on every block); the value products of a step issued behind
 // the next step's scores (179 to 186); twelve compute warps of 144 registers.

@@ -924,9 +924,13 @@ cudaError_t launch_attn_join(const CacheAttnParams &a, int sms, bool pdl, cudaSt
 
 // Whether pa_attn_tc_kernel takes a call: its time hardly depends on the rows
 // of an item, that of pa_attn_kernel is in steps of 1, 2, 4 and 8 of them.
-// 64 requests x 2 KV heads in a window of 2047 keys, this / that kernel, us:
-// FP8 1 row 56 / 20, 4 rows 59 / 43, 5 rows 62 / 73, 7 rows 63 / 74; NVFP4 1 row
-// 42 / 19, 2 rows 43 / 29, 3 rows 43 / 53, 7 rows 47 / 93.
+// This / that kernel, us, 2 KV heads, at the rows on both sides of the rule:
+//                                   FP8, 4 rows   5 rows       NVFP4, 2 rows  3 rows
+// 64 requests, window 2047          59 / 43       63 / 74      43 / 30        44 / 53
+// 64, 16 listed blocks, weights     68 / 59       73 / 84      50 / 47        52 / 65
+// 64, every block of 8..8192, w.    112 / 87      118 / 132    81 / 66        83 / 99
+// 1, window 40000                   30 / 22       31 / 31      24 / 18        25 / 25
+// 1, every block of 131072, w.      70 / 71       80 / 91      48 / 59        54 / 74
 inline bool use_attn_tc(const CacheAttnParams &a, int fmt) {
   return a.rows_per >= (fmt == 0 ? 5 : 3) && (a.topk == 0 || a.bt_width <= kTcMaxWidth);
 }
@@ -934,8 +938,11 @@ inline bool use_attn_tc(const CacheAttnParams &a, int fmt) {
 // A CTA an item, instead of even slices, where the items are about as long as
 // one another (a window, lists) and the longest CTA then has no more to do
 // than with slices, whose second segments and second kernel take as long as
-// about five blocks.  This / slices, us: FP8, 128 items of 18 blocks 62 / 72;
-// NVFP4, 128 items of rows of 16 listed blocks, with weights, 61 / 67.
+// about five blocks.  The lists of an item's rows are taken to be much the same,
+// as selections by neighbouring rows are; eight lists without a block in common
+// make an item eight times as long, and slices would be the more even share.
+// This / slices, us: FP8, 128 items of 18 blocks 62 / 72; NVFP4, 128 items of
+// rows of 16 listed blocks (4 their own), with weights, 61 / 67.
 inline bool whole_items(const CacheAttnParams &a, int sms) {
   if (a.topk == 0 && a.window == 0) return false;
   const int64_t blocks = a.topk ? a.topk : ((int64_t)a.sinks + 127) / 128 + ((int64_t)a.window + a.rows_per + 125) / 128 + 1;

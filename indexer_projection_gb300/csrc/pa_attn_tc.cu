@@ -1,5 +1,6 @@
-// The attention of pre_attn_attention_ext on tcgen05, for calls whose items
-// are dealt in slices (pa_attn.cuh): the (row, head)s of an item are the 128
+// The attention of pre_attn_attention_ext on tcgen05, for items of several rows
+// (use_attn_tc) that are dealt in slices or a CTA each (pa_attn.cuh; small
+// calls go to clusters of pa_attn_kernel): the (row, head)s of an item are the 128
 // rows of S = Q K^T and of O = P V (f16 operands, f32 in tensor memory), so a
 // block's codes are converted to f16 once for all of them, and a softmax
 // thread has one (row, head) to itself.  (pa_attn_kernel converts them again
@@ -20,7 +21,7 @@
 // first keys and some 6 to the first products, behind 6 to the last store.
 // Longer code is slower even where it has fewer instructions to run (the roles'
 // loops share the schedulers' instruction caches): turns of 64 keys 64.5,
-// the NVFP4 conversions unrolled 120 for 114 (every block of 64 x 7 rows); turns
+// the NVFP4 conversions unrolled 120 for 114 (64 x 7 rows on every block); turns
 // of 16 keys pay their latencies more often (68).  Right and no faster, too: one
 // pass over the scores with the references looked at turn by turn (65 when this
 // took 65); 16 softmax warps of 16 (row, head)s, a quarter of the keys a lane
@@ -30,6 +31,14 @@
 // Arithmetic as in pa_attn.cu (references, lift, unit of the products), the
 // state of a (row, head) in one thread's registers: no exchange but at the
 // segment's end, where the two groups' parts are added up.
+//
+// Order.  A segment (an item's part of a slice) is its blocks' entries of the
+// ring, then one without a block for each softmax group; it may have no block at
+// all (a request without keys).  A wait names a phase of an mbarrier by its
+// parity alone, so whoever completes a phase first waits for evidence that all
+// readers are past the one before: the products' thread for `meet` of the
+// segment before, the queries' and the values' warps for item_seen.  (The 62 us,
+// and 30 for one long request's rows in slices, are the same with and without.)
 //
 // Keys that a row does not see have no weight, but the tile of values is all
 // rows': keys that no row sees are written as zeros, and where not every row

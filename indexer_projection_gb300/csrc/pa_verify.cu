@@ -24,6 +24,9 @@
 // runs beside, are about 7 (a vocabulary of 1000 on as many CTAs) and the rows 10;
 // 128 of 200064, bf16 p, 18.9 us, 2.7 TB/s (the same, and a 16-bit value costs
 // as many additions as a 32-bit one; rows that begin off a 16-byte boundary 23).
+// 64 registers (four CTAs an SM) do not hold everything where p is bf16: spills of
+// 60 bytes a thread with bf16 q or none, off a 16-byte boundary 476, there with f32
+// q 64.
 #include <algorithm>
 #include <cstdint>
 
