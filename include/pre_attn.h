@@ -754,7 +754,7 @@ typedef struct pa_verify_args {
   int draft_type;             /* enum pa_prob_type, with draft_probs */
   const int32_t *drafts;      /* [R, q_len - 1]; unused for q_len 1 */
   const float *uniforms;      /* [R, q_len]: one a draft, the last for the drawn token; below 0 (or NaN) counts as 0
-                                 there and 1 or above as the largest number below 1; in units of 2^-64 */
+                                 there and 1 or above as the largest number below 1; it counts in whole units of 2^-64 */
   int R;                      /* requests, 0 .. 65535 */
   int q_len;                  /* rows a request, 1 .. 16 */
   int vocab;                  /* 1 .. 2^24 */

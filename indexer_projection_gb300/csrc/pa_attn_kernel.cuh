@@ -942,7 +942,7 @@ inline bool use_attn_tc(const CacheAttnParams &a, int fmt) {
 // as selections by neighbouring rows are; eight lists without a block in common
 // make an item eight times as long, and slices would be the more even share.
 // This / slices, us: FP8, 128 items of 18 blocks 62 / 72; NVFP4, 128 items of
-// rows of 16 listed blocks (4 their own), with weights, 61 / 67.
+// rows of 16 listed blocks, with weights, 61 / 67.
 inline bool whole_items(const CacheAttnParams &a, int sms) {
   if (a.topk == 0 && a.window == 0) return false;
   const int64_t blocks = a.topk ? a.topk : ((int64_t)a.sinks + 127) / 128 + ((int64_t)a.window + a.rows_per + 125) / 128 + 1;
